@@ -295,6 +295,107 @@ hsl_status hsl_permute(const void* W, int64_t m, int64_t n, hsl_dtype dtype,
 hsl_status hsl_set_permutation(hsl_handle h, const int32_t* row_order, const int32_t* col_order,
                                hsl_stream s);
 
+/* ---- Microscaled blocks: 4-bit weights and 8-bit activations ------------------
+ * 32 consecutive values of a row share one power of two.  A matrix in blocks
+ * is plain device memory of the caller's, in this layout:
+ *   scales  [rows][scale_pitch] bytes e (ue8m0): the block's power of two is
+ *           2^(e − 127); e = 255: the block stands for NaN.  scale_pitch is
+ *           ceil(cols/32) rounded up to a multiple of 16; padding bytes are 0.
+ *   codes   [rows][code_pitch] bytes, whole blocks per row, padding codes 0:
+ *     HSL_MX_E2M1  code_pitch = 16·ceil(cols/32).  4-bit floats; bit 3 is the
+ *                  sign, codes 0..7 stand for 0, 0.5, 1, 1.5, 2, 3, 4, 6;
+ *                  element 2i of a row is the low half of byte i.
+ *     HSL_MX_INT8  code_pitch = 32·ceil(cols/32).  Integers in −127..127 that
+ *                  stand for q/64.
+ * Both arrays must be 16-byte aligned.  These are the element and scale types
+ * of the OCP Microscaling Formats specification v1.0 (MXFP4, MXINT8).
+ *
+ * What they serve: [SQZ] §2–4, Dense-and-Sparse: W = D + S with a low-bit dense
+ * D and the outliers in a sparse S, multiplied in parallel; here D (e2m1) joins
+ * the layer's S and U Vᵀ through the `add` argument of the products.  [HSS]
+ * §Implementation and operational patterns, backward pass: the gradients of the
+ * factors, taken from activations kept in 8 bits.
+ *
+ * The calls own nothing and keep nothing between calls.  Those that need
+ * scratch memory take it from the caller: hsl_mx_workspace gives the bytes for
+ * the sizes of a call (16-byte aligned; contents need not survive the call, and
+ * calls that may overlap need one each).  The device of the pointers and the
+ * stream must be current.  All are asynchronous on s, allocate nothing and can
+ * be captured. */
+typedef enum { HSL_MX_E2M1 = 0, HSL_MX_INT8 = 1 } hsl_mx_elem;
+typedef struct {
+  const void* codes;
+  const void* scales;
+  int64_t rows, cols;
+  hsl_mx_elem elem;
+} hsl_mx;
+typedef enum {
+  HSL_MX_OP_APPLY = 0,
+  HSL_MX_OP_APPLY_T = 1,
+  HSL_MX_OP_MATMUL = 2,
+  HSL_MX_OP_FACTOR_GRAD = 3
+} hsl_mx_op;
+
+/* Row pitches in bytes of a matrix with `cols` columns.  Host-only.
+ * [HSS] §Implementation and operational patterns, mixed precision (the storage
+ * format of a compressed weight). */
+hsl_status hsl_mx_pitch(int64_t cols, hsl_mx_elem elem, int64_t* code_pitch, int64_t* scale_pitch);
+
+/* Scratch bytes of a product: batch (rows of X, dY, A or of the checkpoint),
+ * m×n of D (or B rows × cols, or U rows × V rows), r of the factors.
+ * Host-only.  [HSS] §Implementation and operational patterns (the forward and
+ * backward products whose scratch this is). */
+hsl_status hsl_mx_workspace(hsl_mx_op op, int64_t batch, int64_t m, int64_t n, int64_t r,
+                            hsl_dtype dtype, size_t* bytes);
+
+/* Quantise X (device, rows×cols row-major) into blocks along its rows:
+ *   s = 2^(floor(log2 max|x|) − emax), emax = 2 (e2m1) or 0 (int8), exponent
+ *       clamped to −127..127;   q = x/s rounded to nearest even, saturating.
+ * Every code is determined by this (division by s is exact).  A block of zeros
+ * gets e = 0 and zero codes; a block with a NaN or an infinity e = 255 and zero
+ * codes.  rows = 0 is a no-op.
+ * [SQZ] §2–4 (the low-bit dense part); the rule is that of the OCP
+ * specification, §6.3. */
+hsl_status hsl_mx_quantize(const void* X, hsl_dtype dtype, int64_t rows, int64_t cols,
+                           hsl_mx_elem elem, void* codes, void* scales, hsl_stream s);
+
+/* X[rows][cols] = the values the blocks stand for (exact in both dtypes; a
+ * value past the dtype's range becomes infinite).  [SQZ] §2–4, as
+ * hsl_mx_quantize. */
+hsl_status hsl_mx_dequantize(const hsl_mx* q, void* X, hsl_dtype dtype, hsl_stream s);
+
+/* Y = X Dᵀ (+ add): y[t][i] = add[t][i] + Σ_j x[t][j] d[i][j], D m×n in e2m1 blocks,
+ * X [batch][n], Y and add [batch][m] of dtype (add may be NULL, or Y itself);
+ * products and sums in fp32, one rounding at the end.  batch = 0 is a no-op.
+ * [SQZ] §2–4: the dense term of (D + S) x; [SQZ] §1 for why it is bound by the
+ * bytes of D at small batches. */
+hsl_status hsl_mx4_apply(const hsl_mx* D, const void* X, const void* add, void* Y, int64_t batch,
+                         hsl_dtype dtype, void* ws, size_t ws_bytes, hsl_stream s);
+
+/* dX = dY D (+ add): the gradient of hsl_mx4_apply's input; dY [batch][m], dX and
+ * add [batch][n] (add may be NULL, or dX itself).
+ * [HSS] §Implementation and operational patterns, backward pass. */
+hsl_status hsl_mx4_apply_t(const hsl_mx* D, const void* dY, const void* add, void* dX, int64_t batch,
+                           hsl_dtype dtype, void* ws, size_t ws_bytes, hsl_stream s);
+
+/* Y = A Bᵀ (+ add), both in e2m1 blocks with the same number of columns; Y and add
+ * [A.rows][B.rows] of dtype (add may be NULL, or Y itself), sums in fp32.
+ * [SQZ] §2–4, as hsl_mx4_apply, with the activations in 4 bits as well. */
+hsl_status hsl_mx4_matmul(const hsl_mx* A, const hsl_mx* B, const void* add, void* Y, hsl_dtype dtype,
+                          void* ws, size_t ws_bytes, hsl_stream s);
+
+/* Backward pass of x → U (Vᵀ x) from a checkpoint of its input in int8 blocks:
+ *   Z = X V, G = dY U;  dU = dYᵀ Z, dV = Xᵀ G, dX = G Vᵀ (+ add)
+ * X [T][n] blocks (T = X.rows; T = 0 writes zeros to dU and dV), dY [T][m],
+ * U and dU [m][r], V and dV [n][r], dX and add [T][n] of dtype; dX may be NULL
+ * (then add must be), add may be NULL or dX itself.  1 ≤ r ≤ 256.  Z and G are
+ * kept to 16 bits of significand or more, sums in fp32.
+ * [HSS] §Implementation and operational patterns, backward pass (the gradients
+ * of U and V, as derived from the forward decomposition). */
+hsl_status hsl_mx8_factor_grad(const hsl_mx* X, const void* dY, int64_t m, const void* U,
+                               const void* V, int32_t r, const void* add, void* dU, void* dV, void* dX,
+                               hsl_dtype dtype, void* ws, size_t ws_bytes, hsl_stream s);
+
 /* Synchronise s and return, then clear, the device-side error of the handle
  * (HSL_ERR_NAN_INPUT, HSL_ERR_TIMEOUT) — HSL_OK if none.
  * [HSS] §Risks and mitigations, risk 1: keep the uncompressed weights as a

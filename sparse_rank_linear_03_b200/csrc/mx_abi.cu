@@ -1,0 +1,213 @@
+// C ABI of the microscaled operators (declared in include/hsl.h): argument checks,
+// workspace layout and the choice of kernel.  Nothing is kept between calls: all
+// data, the workspace included, is the caller's.
+#include <cstring>
+#include <string>
+
+#include "common.cuh"
+#include "internal.h"
+#include "mx.cuh"
+#include "mx_ops.h"
+
+namespace hsl {
+namespace {
+
+hsl_status bad_arg(const char* why) {
+  set_message(why);
+  return HSL_ERR_INVALID_ARG;
+}
+hsl_status not_supported(const char* why) {
+  set_message(why);
+  return HSL_ERR_UNSUPPORTED;
+}
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+bool dtype_ok(hsl_dtype d) { return d == HSL_F32 || d == HSL_BF16; }
+bool size_ok(int64_t v) { return v >= 1 && v <= INT32_MAX; }
+
+// The checks that every operator makes of a matrix in blocks.
+hsl_status check_mx(const hsl_mx* q, int elem, const char* what) {
+  if (!q) return bad_arg((std::string(what) + " is NULL").c_str());
+  if (q->elem != HSL_MX_E2M1 && q->elem != HSL_MX_INT8)
+    return bad_arg((std::string(what) + ": unknown element type").c_str());
+  if (elem >= 0 && int(q->elem) != elem)
+    return not_supported((std::string(what) + (elem == HSL_MX_E2M1 ? " must hold e2m1 blocks"
+                                                                     : " must hold int8 blocks")).c_str());
+  if (q->rows < 0 || q->rows > INT32_MAX || !size_ok(q->cols))
+    return bad_arg((std::string(what) + ": rows or cols out of range").c_str());
+  if (q->rows > 0 && (!q->codes || !q->scales))
+    return bad_arg((std::string(what) + ": codes/scales is NULL").c_str());
+  if (!aligned16(q->codes) || !aligned16(q->scales))
+    return bad_arg((std::string(what) + ": codes and scales must be 16-byte aligned").c_str());
+  return HSL_OK;
+}
+
+MxOperand operand(const hsl_mx* q, bool trans) {
+  MxOperand o;
+  o.p = q->codes;
+  o.scales = static_cast<const uint8_t*>(q->scales);
+  o.pitch = mx::code_pitch(q->cols, q->elem == HSL_MX_INT8);
+  o.spitch = mx::scale_pitch(q->cols);
+  o.kind = q->elem == HSL_MX_INT8 ? MxOperand::kInt8 : MxOperand::kE2M1;
+  o.trans = trans ? 1 : 0;
+  return o;
+}
+MxOperand operand(const void* p, hsl_dtype dt, int64_t pitch, bool trans) {
+  MxOperand o;
+  o.p = p;
+  o.scales = nullptr;
+  o.pitch = pitch;
+  o.spitch = 0;
+  o.kind = dt == HSL_F32 ? MxOperand::kF32 : MxOperand::kBF16;
+  o.trans = trans ? 1 : 0;
+  return o;
+}
+
+size_t workspace_bytes(hsl_mx_op op, int64_t T, int64_t m, int64_t n, int64_t r, hsl_dtype dt) {
+  switch (op) {
+    case HSL_MX_OP_FACTOR_GRAD: return size_t(2 * T * r * 4);
+    default: return 0;
+  }
+}
+
+hsl_status check_workspace(const void* ws, size_t have, size_t need) {
+  if (need == 0) return HSL_OK;
+  if (!ws || have < need)
+    return bad_arg(("workspace too small: " + std::to_string(need) + " bytes needed").c_str());
+  if (!aligned16(ws)) return bad_arg("workspace must be 16-byte aligned");
+  return HSL_OK;
+}
+
+}  // namespace
+}  // namespace hsl
+
+using namespace hsl;
+
+extern "C" {
+
+hsl_status hsl_mx_pitch(int64_t cols, hsl_mx_elem elem, int64_t* code_pitch, int64_t* scale_pitch) {
+  set_message("");
+  if (!code_pitch || !scale_pitch) return bad_arg("NULL argument");
+  if (elem != HSL_MX_E2M1 && elem != HSL_MX_INT8) return bad_arg("unknown element type");
+  if (!size_ok(cols)) return bad_arg("cols out of range");
+  *code_pitch = mx::code_pitch(cols, elem == HSL_MX_INT8);
+  *scale_pitch = mx::scale_pitch(cols);
+  return HSL_OK;
+}
+
+hsl_status hsl_mx_quantize(const void* X, hsl_dtype dtype, int64_t rows, int64_t cols,
+                           hsl_mx_elem elem, void* codes, void* scales, hsl_stream s) {
+  set_message("");
+  if (!dtype_ok(dtype)) return bad_arg("unknown dtype");
+  const hsl_mx q = {codes, scales, rows, cols, elem};
+  if (hsl_status e = check_mx(&q, -1, "the result")) return e;
+  if (rows == 0) return HSL_OK;
+  if (!X) return bad_arg("X is NULL");
+  return mx_quantize_run(X, dtype, rows, cols, elem == HSL_MX_INT8, codes, scales,
+                         static_cast<cudaStream_t>(s));
+}
+
+hsl_status hsl_mx_dequantize(const hsl_mx* q, void* X, hsl_dtype dtype, hsl_stream s) {
+  set_message("");
+  if (!dtype_ok(dtype)) return bad_arg("unknown dtype");
+  if (hsl_status e = check_mx(q, -1, "the matrix")) return e;
+  if (q->rows == 0) return HSL_OK;
+  if (!X) return bad_arg("X is NULL");
+  return mx_dequantize_run(q->codes, q->scales, q->rows, q->cols, q->elem == HSL_MX_INT8, X, dtype,
+                           static_cast<cudaStream_t>(s));
+}
+
+hsl_status hsl_mx_workspace(hsl_mx_op op, int64_t batch, int64_t m, int64_t n, int64_t r,
+                            hsl_dtype dtype, size_t* bytes) {
+  set_message("");
+  if (!bytes) return bad_arg("bytes is NULL");
+  if (op < HSL_MX_OP_APPLY || op > HSL_MX_OP_FACTOR_GRAD) return bad_arg("unknown operator");
+  if (!dtype_ok(dtype)) return bad_arg("unknown dtype");
+  if (batch < 0 || batch > INT32_MAX || m < 0 || m > INT32_MAX || !size_ok(n) || r < 0 || r > 256)
+    return bad_arg("a size is out of range");
+  *bytes = workspace_bytes(op, batch, m, n, r, dtype);
+  return HSL_OK;
+}
+
+hsl_status hsl_mx4_apply(const hsl_mx* D, const void* X, const void* add, void* Y, int64_t batch,
+                         hsl_dtype dtype, void* ws, size_t ws_bytes, hsl_stream stream) {
+  set_message("");
+  if (!dtype_ok(dtype)) return bad_arg("unknown dtype");
+  if (hsl_status e = check_mx(D, HSL_MX_E2M1, "D")) return e;
+  if (batch < 0 || batch > INT32_MAX) return bad_arg("batch out of range");
+  if (batch == 0 || D->rows == 0) return HSL_OK;
+  if (!X || !Y) return bad_arg("X/Y is NULL");
+  if (hsl_status e = check_workspace(ws, ws_bytes,
+                                     workspace_bytes(HSL_MX_OP_APPLY, batch, D->rows, D->cols, 0, dtype)))
+    return e;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return mx_simt_run(operand(X, dtype, D->cols, false), operand(D, false), batch, D->rows, D->cols,
+                     add, Y, dtype, s);
+}
+
+hsl_status hsl_mx4_apply_t(const hsl_mx* D, const void* dY, const void* add, void* dX, int64_t batch,
+                           hsl_dtype dtype, void* ws, size_t ws_bytes, hsl_stream stream) {
+  set_message("");
+  if (!dtype_ok(dtype)) return bad_arg("unknown dtype");
+  if (hsl_status e = check_mx(D, HSL_MX_E2M1, "D")) return e;
+  if (batch < 0 || batch > INT32_MAX) return bad_arg("batch out of range");
+  if (batch == 0) return HSL_OK;
+  if (!dX || (D->rows > 0 && !dY)) return bad_arg("dY/dX is NULL");
+  if (hsl_status e = check_workspace(ws, ws_bytes,
+                                     workspace_bytes(HSL_MX_OP_APPLY_T, batch, D->rows, D->cols, 0, dtype)))
+    return e;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return mx_simt_run(operand(dY, dtype, D->rows, false), operand(D, true), batch, D->cols, D->rows,
+                     add, dX, dtype, s);
+}
+
+hsl_status hsl_mx4_matmul(const hsl_mx* A, const hsl_mx* B, const void* add, void* Y, hsl_dtype dtype,
+                          void* ws, size_t ws_bytes, hsl_stream stream) {
+  set_message("");
+  if (!dtype_ok(dtype)) return bad_arg("unknown dtype");
+  if (hsl_status e = check_mx(A, HSL_MX_E2M1, "A")) return e;
+  if (hsl_status e = check_mx(B, HSL_MX_E2M1, "B")) return e;
+  if (A->cols != B->cols) return bad_arg("A and B must have the same number of columns");
+  if (A->rows == 0 || B->rows == 0) return HSL_OK;
+  if (!Y) return bad_arg("Y is NULL");
+  if (hsl_status e = check_workspace(
+          ws, ws_bytes, workspace_bytes(HSL_MX_OP_MATMUL, A->rows, B->rows, A->cols, 0, dtype)))
+    return e;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return mx_simt_run(operand(A, false), operand(B, false), A->rows, B->rows, A->cols, add, Y, dtype, s);
+}
+
+hsl_status hsl_mx8_factor_grad(const hsl_mx* X, const void* dY, int64_t m, const void* U,
+                               const void* V, int32_t r, const void* add, void* dU, void* dV, void* dX,
+                               hsl_dtype dtype, void* ws, size_t ws_bytes, hsl_stream stream) {
+  set_message("");
+  if (!dtype_ok(dtype)) return bad_arg("unknown dtype");
+  if (hsl_status e = check_mx(X, HSL_MX_INT8, "X")) return e;
+  if (!size_ok(m)) return bad_arg("m out of range");
+  if (r < 1 || r > 256) return not_supported("need 1 <= r <= 256");
+  if (!U || !V || !dU || !dV) return bad_arg("U/V/dU/dV is NULL");
+  if (add && !dX) return bad_arg("add without dX");
+  const int64_t T = X->rows, n = X->cols;
+  if (T > 0 && !dY) return bad_arg("dY is NULL");
+  if (hsl_status e = check_workspace(ws, ws_bytes,
+                                     workspace_bytes(HSL_MX_OP_FACTOR_GRAD, T, m, n, r, dtype)))
+    return e;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  float* Z = static_cast<float*>(ws);
+  float* G = Z + T * r;
+  const MxOperand x = operand(X, false), xt = operand(X, true);
+  if (hsl_status e = mx_simt_run(x, operand(V, dtype, r, true), T, r, n, nullptr, Z, HSL_F32, s)) return e;
+  if (hsl_status e = mx_simt_run(operand(dY, dtype, m, false), operand(U, dtype, r, true), T, r, m,
+                                 nullptr, G, HSL_F32, s))
+    return e;
+  if (hsl_status e = mx_simt_run(operand(dY, dtype, m, true), operand(Z, HSL_F32, r, true), m, r, T,
+                                 nullptr, dU, dtype, s))
+    return e;
+  if (hsl_status e = mx_simt_run(xt, operand(G, HSL_F32, r, true), n, r, T, nullptr, dV, dtype, s))
+    return e;
+  if (!dX) return HSL_OK;
+  return mx_simt_run(operand(G, HSL_F32, r, false), operand(V, dtype, r, false), T, n, r, add, dX, dtype,
+                     s);
+}
+
+}  // extern "C"

@@ -1,0 +1,45 @@
+// Host-side internals of the microscaled operators: operands and kernel launchers.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "hsl.h"
+
+namespace hsl {
+
+// One factor of a product, stored as [i][k] (or [k][i] when trans).
+struct MxOperand {
+  enum Kind : int32_t { kF32, kBF16, kE2M1, kInt8 };
+  const void* p;
+  const uint8_t* scales;  // e2m1, int8
+  int64_t pitch;          // elements (f32, bf16) or bytes of codes per stored row
+  int64_t spitch;         // scale bytes per stored row
+  int32_t kind;
+  int32_t trans;
+};
+
+// The operand's rows i0, i0 + 1, ...; i0 a multiple of 32 for transposed blocks.
+inline MxOperand mx_operand_from(const MxOperand& o, int64_t i0) {
+  MxOperand r = o;
+  const char* p = static_cast<const char*>(o.p);
+  const int64_t esize = o.kind == MxOperand::kF32 ? 4 : o.kind == MxOperand::kBF16 ? 2 : 1;
+  if (!o.trans) {
+    r.p = p + i0 * o.pitch * esize;
+    if (o.scales) r.scales = o.scales + i0 * o.spitch;
+  } else {
+    r.p = p + (o.kind == MxOperand::kE2M1 ? i0 / 2 : i0 * esize);
+    if (o.scales) r.scales = o.scales + i0 / 32;
+  }
+  return r;
+}
+
+hsl_status mx_quantize_run(const void* X, hsl_dtype dtype, int64_t rows, int64_t cols, bool int8,
+                           void* codes, void* scales, cudaStream_t s);
+hsl_status mx_dequantize_run(const void* codes, const void* scales, int64_t rows, int64_t cols,
+                             bool int8, void* X, hsl_dtype dtype, cudaStream_t s);
+// C[M][N] (row pitch N) = add + A Bᵀ in fp32
+hsl_status mx_simt_run(const MxOperand& A, const MxOperand& B, int64_t M, int64_t N, int64_t K,
+                       const void* add, void* C, hsl_dtype cdt, cudaStream_t s);
+
+}  // namespace hsl

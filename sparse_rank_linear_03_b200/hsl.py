@@ -9,6 +9,7 @@ is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -28,8 +29,16 @@ EXPORTS = (
     "hsl_group_create", "hsl_group_apply", "hsl_group_destroy", "hsl_check",
     "hsl_status_str", "hsl_last_message", "hsl_launch_count", "hsl_split_topk_noalloc",
     "hsl_concentration", "hsl_rcm_order", "hsl_permute", "hsl_set_permutation", "hsl_factor",
-    "hsl_set_index_bits",
+    "hsl_set_index_bits", "hsl_mx_pitch", "hsl_mx_workspace", "hsl_mx_quantize",
+    "hsl_mx_dequantize", "hsl_mx4_apply", "hsl_mx4_apply_t", "hsl_mx4_matmul",
+    "hsl_mx8_factor_grad",
 )
+
+
+class _MXView(ctypes.Structure):
+    """hsl_mx."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("elem", ctypes.c_int)]
 
 
 class HslError(RuntimeError):
@@ -69,6 +78,14 @@ def _load() -> ctypes.CDLL:
         "hsl_set_permutation": [P, P, P, P],
         "hsl_factor": [P, P, ctypes.c_int, P, I32, I32, P, P, P, P],
         "hsl_set_index_bits": [P, I32],
+        "hsl_mx_pitch": [I64, I32, ctypes.POINTER(I64), ctypes.POINTER(I64)],
+        "hsl_mx_workspace": [I32, I64, I64, I64, I64, I32, ctypes.POINTER(ctypes.c_size_t)],
+        "hsl_mx_quantize": [P, I32, I64, I64, I32, P, P, P],
+        "hsl_mx_dequantize": [P, P, I32, P],
+        "hsl_mx4_apply": [P, P, P, P, I64, I32, P, ctypes.c_size_t, P],
+        "hsl_mx4_apply_t": [P, P, P, P, I64, I32, P, ctypes.c_size_t, P],
+        "hsl_mx4_matmul": [P, P, P, P, I32, P, ctypes.c_size_t, P],
+        "hsl_mx8_factor_grad": [P, P, I64, P, P, I32, P, P, P, P, I32, P, ctypes.c_size_t, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -312,3 +329,211 @@ class Group:
             self.close()
         except Exception:
             pass
+
+
+# ---- microscaled blocks -------------------------------------------------------
+
+MX_ELEM = {"e2m1": 0, "int8": 1}
+_MX_OP = {"apply": 0, "apply_t": 1, "matmul": 2, "factor_grad": 3}
+_DTYPE_NAME = {torch.float32: "f32", torch.bfloat16: "bf16"}
+
+
+def mx_pitch(cols: int, elem: str) -> tuple[int, int]:
+    """Bytes per row of the codes and of the scales (hsl_mx_pitch)."""
+    c, s = ctypes.c_int64(), ctypes.c_int64()
+    _ok(lib.hsl_mx_pitch(cols, MX_ELEM[elem], ctypes.byref(c), ctypes.byref(s)), "hsl_mx_pitch")
+    return c.value, s.value
+
+
+@functools.lru_cache(maxsize=4096)
+def _mx_workspace_bytes(op: int, batch: int, m: int, n: int, r: int, dtype: int) -> int:
+    b = ctypes.c_size_t()
+    _ok(lib.hsl_mx_workspace(op, batch, m, n, r, dtype, ctypes.byref(b)), "hsl_mx_workspace")
+    return b.value
+
+
+class MX:
+    """A matrix in microscaled blocks: codes and scales in the layout of hsl_mx.
+
+    ``codes`` is [rows][code pitch] (uint8 for e2m1; int8 or uint8 for int8),
+    ``scales`` [rows][scale pitch] uint8; both contiguous, on one CUDA device."""
+
+    __slots__ = ("codes", "scales", "rows", "cols", "elem", "_view", "_ref")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int, elem: str = "e2m1"):
+        if elem not in MX_ELEM:
+            raise ValueError(f"unknown element type {elem!r}")
+        nb = (cols + 31) // 32
+        if cols < 1 or codes.dim() != 2 or scales.dim() != 2:
+            raise ValueError("codes and scales are 2-D and cols >= 1")
+        rows = codes.shape[0]
+        if codes.shape[1] != nb * (16 if elem == "e2m1" else 32):
+            raise ValueError(f"codes have {codes.shape[1]} bytes per row, expected "
+                             f"{nb * (16 if elem == 'e2m1' else 32)}")
+        if scales.shape[0] != rows or scales.shape[1] != (nb + 15) // 16 * 16:
+            raise ValueError(f"scales must be [{rows}][{(nb + 15) // 16 * 16}]")
+        if codes.dtype not in (torch.uint8, torch.int8) or scales.dtype != torch.uint8:
+            raise ValueError("codes are uint8 (int8 for int8 blocks), scales uint8")
+        if not codes.is_cuda or scales.device != codes.device:
+            raise ValueError("codes and scales must be on one CUDA device")
+        self.codes, self.scales, self.rows, self.cols, self.elem = codes, scales, rows, cols, elem
+        self._view = _MXView(_ptr(codes), _ptr(scales), rows, cols, MX_ELEM[elem])
+        self._ref = ctypes.addressof(self._view)
+
+    @property
+    def device(self) -> torch.device:
+        return self.codes.device
+
+
+class _On:
+    """Makes the tensors' device current, and the given stream torch's current one, for the
+    allocations and the launch of one call."""
+
+    __slots__ = ("ptr", "_ctx")
+
+    def __init__(self, device: torch.device, stream):
+        self._ctx = None
+        if stream is None:
+            if device.index != torch.cuda.current_device():
+                self._ctx = torch.cuda.device(device)
+            self.ptr = torch.cuda.current_stream(device).cuda_stream
+        else:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)),
+                                                   device=device)
+            self._ctx = torch.cuda.stream(stream)
+            self.ptr = stream.cuda_stream
+
+    def __enter__(self):
+        if self._ctx is not None:
+            self._ctx.__enter__()
+        return self.ptr
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+
+
+def _operand(t: torch.Tensor, shape: tuple, dtype: torch.dtype, device: torch.device, what: str) -> int:
+    """The pointer of a contiguous tensor of this shape, type and device."""
+    if t.shape != shape:
+        raise ValueError(f"{what} is {tuple(t.shape)}, expected {shape}")
+    if t.dtype != dtype:
+        raise ValueError(f"{what} is {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def _mx_dtype(t: torch.Tensor) -> int:
+    name = _DTYPE_NAME.get(t.dtype)
+    if name is None:
+        raise ValueError(f"{t.dtype} is not supported: f32 or bf16")
+    return DTYPE[name]
+
+
+def _scratch(op: str, batch: int, m: int, n: int, r: int, dtype: int, device: torch.device):
+    b = _mx_workspace_bytes(_MX_OP[op], batch, m, n, r, dtype)
+    return (torch.empty(b, dtype=torch.uint8, device=device) if b else None), b
+
+
+def mx_quantize(X: torch.Tensor, elem: str = "e2m1", stream=None) -> MX:
+    """X [rows][cols] in blocks of 32 along its rows (hsl_mx_quantize)."""
+    if X.dim() != 2 or not X.is_cuda:
+        raise ValueError("X must be a 2-D CUDA tensor")
+    if elem not in MX_ELEM:
+        raise ValueError(f"unknown element type {elem!r}")
+    rows, cols = X.shape
+    dt = _mx_dtype(X)
+    xp = _operand(X, (rows, cols), X.dtype, X.device, "X")
+    nb = (cols + 31) // 32
+    with _On(X.device, stream) as s:
+        codes = torch.empty(rows, nb * (16 if elem == "e2m1" else 32), device=X.device,
+                            dtype=torch.uint8 if elem == "e2m1" else torch.int8)
+        scales = torch.empty(rows, (nb + 15) // 16 * 16, dtype=torch.uint8, device=X.device)
+        q = MX(codes, scales, cols, elem)
+        _ok(lib.hsl_mx_quantize(xp, dt, rows, cols, MX_ELEM[elem], codes.data_ptr(),
+                                scales.data_ptr(), s), "hsl_mx_quantize")
+    return q
+
+
+def mx_dequantize(q: MX, dtype: str = "bf16", stream=None) -> torch.Tensor:
+    """The values that the blocks stand for, [rows][cols] (hsl_mx_dequantize)."""
+    with _On(q.device, stream) as s:
+        X = torch.empty(q.rows, q.cols, dtype=TORCH_DTYPE[dtype], device=q.device)
+        _ok(lib.hsl_mx_dequantize(q._ref, X.data_ptr(), DTYPE[dtype], s), "hsl_mx_dequantize")
+    return X
+
+
+def _mx4_product(fn, name: str, op: str, D: MX, X: torch.Tensor, k: int, f: int, add, Y, stream):
+    if X.dim() != 2:
+        raise ValueError("the input must be 2-D [batch][features]")
+    dev, dt = D.codes.device, _mx_dtype(X)
+    batch = X.shape[0]
+    xp = _operand(X, (batch, k), X.dtype, dev, "the input")
+    ap = _operand(add, (batch, f), X.dtype, dev, "add") if add is not None else None
+    with _On(dev, stream) as s:
+        if Y is None:
+            Y = torch.empty(batch, f, dtype=X.dtype, device=dev)
+        yp = _operand(Y, (batch, f), X.dtype, dev, "the output")
+        ws, wb = _scratch(op, batch, D.rows, D.cols, 0, dt, dev)
+        _ok(fn(D._ref, xp, ap, yp, batch, dt, ws.data_ptr() if wb else None, wb, s), name)
+    return Y
+
+
+def mx4_apply(D: MX, X: torch.Tensor, Y: torch.Tensor | None = None,
+              add: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y [batch][m] = X [batch][n] Dᵀ (+ add), D [m][n] in e2m1 blocks (hsl_mx4_apply).
+    ``add`` may be Y, e.g. the output of the layer's sparse and low-rank part."""
+    return _mx4_product(lib.hsl_mx4_apply, "hsl_mx4_apply", "apply", D, X, D.cols, D.rows, add, Y, stream)
+
+
+def mx4_apply_t(D: MX, dY: torch.Tensor, dX: torch.Tensor | None = None,
+                add: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """dX [batch][n] = dY [batch][m] D (+ add): the gradient of mx4_apply's input
+    (hsl_mx4_apply_t)."""
+    return _mx4_product(lib.hsl_mx4_apply_t, "hsl_mx4_apply_t", "apply_t", D, dY, D.rows, D.cols, add, dX,
+                        stream)
+
+
+def mx4_matmul(A: MX, B: MX, Y: torch.Tensor | None = None, dtype: str = "bf16",
+               add: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y [A.rows][B.rows] = A Bᵀ (+ add), both in e2m1 blocks (hsl_mx4_matmul)."""
+    dev, tdt = A.device, TORCH_DTYPE[dtype]
+    if B.device != dev:
+        raise ValueError(f"B is on {B.device}, expected {dev}")
+    ap = _operand(add, (A.rows, B.rows), tdt, dev, "add") if add is not None else None
+    with _On(dev, stream) as s:
+        if Y is None:
+            Y = torch.empty(A.rows, B.rows, dtype=tdt, device=dev)
+        yp = _operand(Y, (A.rows, B.rows), tdt, dev, "Y")
+        ws, wb = _scratch("matmul", A.rows, B.rows, A.cols, 0, DTYPE[dtype], dev)
+        _ok(lib.hsl_mx4_matmul(A._ref, B._ref, ap, yp, DTYPE[dtype], ws.data_ptr() if wb else None, wb, s),
+            "hsl_mx4_matmul")
+    return Y
+
+
+def mx8_factor_grad(X: MX, dY: torch.Tensor, U: torch.Tensor, V: torch.Tensor, dx: bool = False,
+                    add: torch.Tensor | None = None, stream=None):
+    """Backward pass of x → U (Vᵀ x) from its input kept in int8 blocks (hsl_mx8_factor_grad):
+    dU [m][r] and dV [n][r], and with ``dx`` also dX [T][n] = dY U Vᵀ (+ add)."""
+    if dY.dim() != 2 or U.dim() != 2:
+        raise ValueError("dY and U must be 2-D")
+    dev, dt = X.device, _mx_dtype(dY)
+    m, r = U.shape
+    gp = _operand(dY, (X.rows, m), dY.dtype, dev, "dY")
+    up = _operand(U, (m, r), dY.dtype, dev, "U")
+    vp = _operand(V, (X.cols, r), dY.dtype, dev, "V")
+    if add is not None and not dx:
+        raise ValueError("add is for dX: pass dx=True")
+    ap = _operand(add, (X.rows, X.cols), dY.dtype, dev, "add") if add is not None else None
+    with _On(dev, stream) as s:
+        dU, dV = torch.empty_like(U), torch.empty_like(V)
+        dX = torch.empty(X.rows, X.cols, dtype=dY.dtype, device=dev) if dx else None
+        ws, wb = _scratch("factor_grad", X.rows, m, X.cols, r, dt, dev)
+        _ok(lib.hsl_mx8_factor_grad(X._ref, gp, m, up, vp, r, ap, dU.data_ptr(), dV.data_ptr(),
+                                    dX.data_ptr() if dx else None, dt, ws.data_ptr() if wb else None,
+                                    wb, s), "hsl_mx8_factor_grad")
+    return (dU, dV, dX) if dx else (dU, dV)

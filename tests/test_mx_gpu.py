@@ -1,0 +1,221 @@
+"""Microscaled operators on the GPU against the float64 oracle.
+
+Quantisation is exact: codes and scale bytes are compared bit for bit.  Products
+are held to a bound derived from their arithmetic, element by element:
+
+  |y − y*| ≤ u |y*| + c(K) Σ|a||b|,   c(K) = (64 + K/16) · 2^-23
+
+u is half a step of the output type (bf16 2^-8, f32 2^-24); a sum kept in fp32
+is folded in chains of at most 64 + K/16 additions, each off by at most 2^-23 of
+the partial sums' bound Σ|a||b| (2^-24 for rounding, 2^-23 for truncation inside
+the tensor cores).  Operands are exact: bf16 and fp32 inputs, and block values
+(at most 8 significant bits) in bf16 or fp32.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import mx
+
+pytestmark = pytest.mark.gpu
+
+TDT = {"f32": torch.float32, "bf16": torch.bfloat16}
+HALF_STEP = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}
+
+
+@pytest.fixture(scope="module")
+def hsl():
+    from sparse_rank_linear_03_b200 import hsl as mod
+    return mod
+
+
+def chain(K):
+    return (64 + K / 16) * 2.0 ** -23
+
+
+def tensor(x, dtype):
+    return torch.from_numpy(np.ascontiguousarray(x, dtype=np.float32)).to(TDT[dtype]).cuda()
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def weights(m, n, seed):
+    return 0.02 * np.random.default_rng(seed).standard_t(3, size=(m, n))
+
+
+def tokens(t, n, seed):
+    rng = np.random.default_rng(seed)
+    return rng.standard_normal((t, n)) * np.where(rng.random(n) < 0.02, 8.0, 1.0)
+
+
+def blocks(hsl, x, elem):
+    """x as blocks on the device (from the oracle's codes) and the float64 values held."""
+    c, s = mx.quantize(np.asarray(x, np.float32), elem)
+    q = hsl.MX(torch.from_numpy(c).cuda(), torch.from_numpy(s).cuda(), x.shape[1], elem)
+    return q, mx.values(c, s, x.shape[1], elem)
+
+
+def close(got, want, mag, K, dtype, extra=0.0):
+    """`mag`: Σ|a||b| (+ |add|) of each element; `extra`: error that the operands carry."""
+    err = np.abs(f64(got) - want)
+    lim = HALF_STEP[dtype] * np.abs(want) + (chain(K) * mag + extra) * (1 + HALF_STEP[dtype])
+    worst = np.max(err - lim)
+    assert np.all(np.isfinite(f64(got))) and worst <= 0, f"{worst} over the bound"
+
+
+# ---------------------------------------------------------------- quantisation
+
+@pytest.mark.parametrize("elem", ["e2m1", "int8"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 31), (3, 32), (5, 33), (7, 40), (2, 511), (9, 1001),
+                                       (33, 520), (300, 1024), (1, 70001), (4097, 8)])
+def test_quantize_bit_exact(hsl, rows, cols, elem, dtype):
+    x = tensor(weights(rows, cols, rows + cols), dtype)
+    q = hsl.mx_quantize(x, elem)
+    c, s = mx.quantize(f64(x), elem)
+    assert np.array_equal(q.codes.cpu().numpy().view(np.uint8), c)
+    assert np.array_equal(q.scales.cpu().numpy(), s)
+    back = hsl.mx_dequantize(q, dtype)
+    assert np.array_equal(f64(back), mx.values(c, s, cols, elem))
+
+
+@pytest.mark.parametrize("elem", ["e2m1", "int8"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_quantize_special_values(hsl, elem, dtype):
+    x = np.zeros((9, 64), np.float32)
+    x[0, 3] = np.nan
+    x[1, 40] = np.inf
+    x[2, 5], x[2, 6] = -np.inf, np.nan
+    x[3, :] = -0.0
+    x[4, 7] = 2.0 ** -133                      # a subnormal of both types
+    x[4, 40] = 2.0 ** -127
+    x[5, :] = 2.0 ** 127 * 1.9921875           # the largest bf16
+    x[6, :] = np.float32(2.0 ** -126) * np.linspace(0, 3, 64, dtype=np.float32)
+    x[7, :32] = [0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0] * 4   # ties
+    x[7, 31] = 7.5
+    x[8, ::2] = 2.0 ** 100
+    x[8, 1::2] = 2.0 ** -100
+    t = tensor(x, dtype)
+    q = hsl.mx_quantize(t, elem)
+    c, s = mx.quantize(f64(t), elem)
+    assert np.array_equal(q.codes.cpu().numpy().view(np.uint8), c)
+    assert np.array_equal(q.scales.cpu().numpy(), s)
+    for out in ("f32", "bf16"):
+        want = mx.values(c, s, 64, elem)
+        got = f64(hsl.mx_dequantize(q, out))
+        assert np.array_equal(np.isnan(got), np.isnan(want))
+        assert np.array_equal(got[~np.isnan(want)], want[~np.isnan(want)])
+
+
+def test_quantize_unaligned_input(hsl):
+    base = tensor(weights(1, 8 * 64 + 1, 5), "bf16").view(-1)
+    x = base[1:].view(8, 64)
+    q = hsl.mx_quantize(x)
+    c, s = mx.quantize(f64(x), "e2m1")
+    assert np.array_equal(q.codes.cpu().numpy(), c) and np.array_equal(q.scales.cpu().numpy(), s)
+
+
+def test_quantize_no_rows(hsl):
+    q = hsl.mx_quantize(torch.empty(0, 40, device="cuda"))
+    assert q.rows == 0 and hsl.mx_dequantize(q, "f32").shape == (0, 40)
+
+
+# ---------------------------------------------------------------- products
+
+SIZES = [(1, 1, 1), (1, 1, 32), (1, 64, 64), (2, 65, 96), (3, 128, 40), (5, 1000, 777), (8, 256, 512),
+         (9, 129, 33), (16, 1024, 1024), (17, 300, 2048), (33, 1001, 777), (64, 257, 520),
+         (65, 640, 1056), (130, 511, 1023), (200, 1100, 544), (257, 256, 256), (300, 777, 4096)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,m,n", SIZES)
+def test_apply(hsl, T, m, n, dtype):
+    D, d = blocks(hsl, weights(m, n, m + n), "e2m1")
+    x = tensor(tokens(T, n, T), dtype)
+    want, mag = mx.apply(d, f64(x)), mx.apply(np.abs(d), np.abs(f64(x)))
+    close(hsl.mx4_apply(D, x), want, mag, n, dtype)
+    add = tensor(tokens(T, m, 7), dtype)
+    close(hsl.mx4_apply(D, x, add=add), want + f64(add), mag + np.abs(f64(add)), n, dtype)
+    kept = f64(add)
+    close(hsl.mx4_apply(D, x, Y=add, add=add), want + kept, mag + np.abs(kept), n, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,m,n", SIZES)
+def test_apply_t(hsl, T, m, n, dtype):
+    D, d = blocks(hsl, weights(m, n, m + n), "e2m1")
+    dy = tensor(tokens(T, m, T), dtype)
+    want, mag = mx.apply_t(d, f64(dy)), mx.apply_t(np.abs(d), np.abs(f64(dy)))
+    close(hsl.mx4_apply_t(D, dy), want, mag, m, dtype)
+    add = tensor(tokens(T, n, 7), dtype)
+    kept = f64(add)
+    close(hsl.mx4_apply_t(D, dy, add=add), want + kept, mag + np.abs(kept), m, dtype)
+    close(hsl.mx4_apply_t(D, dy, dX=add, add=add), want + kept, mag + np.abs(kept), m, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,m,n", SIZES)
+def test_matmul(hsl, T, m, n, dtype):
+    A, a = blocks(hsl, tokens(T, n, T), "e2m1")
+    B, b = blocks(hsl, weights(m, n, m + n), "e2m1")
+    want, mag = mx.apply(b, a), mx.apply(np.abs(b), np.abs(a))
+    close(hsl.mx4_matmul(A, B, dtype=dtype), want, mag, n, dtype)
+    add = tensor(tokens(T, m, 7), dtype)
+    kept = f64(add)
+    close(hsl.mx4_matmul(A, B, dtype=dtype, add=add), want + kept, mag + np.abs(kept), n, dtype)
+    close(hsl.mx4_matmul(A, B, Y=add, dtype=dtype, add=add), want + kept, mag + np.abs(kept), n, dtype)
+
+
+GRAD_SIZES = [(1, 1, 1, 1), (1, 40, 64, 8), (2, 64, 65, 3), (31, 128, 96, 16), (33, 300, 200, 17),
+              (64, 256, 512, 64), (77, 1001, 777, 100), (128, 512, 256, 128), (200, 640, 1056, 256),
+              (500, 257, 300, 40), (1000, 384, 1100, 33)]
+
+
+def grad_check(hsl, T, m, n, r, dtype, seed):
+    X, x = blocks(hsl, tokens(T, n, seed), "int8")
+    rng = np.random.default_rng(seed + 1)
+    dY, U, V = (tensor(a, dtype) for a in (0.01 * rng.standard_normal((T, m)),
+                                           0.05 * rng.standard_normal((m, r)),
+                                           0.05 * rng.standard_normal((n, r))))
+    add = tensor(0.01 * rng.standard_normal((T, n)), dtype)
+    dy, u, v, ad = f64(dY), f64(U), f64(V), f64(add)
+    wU, wV, wX = mx.factor_grad(x, dy, u, v, ad)
+    # Z and G carry their own sums' error and 2^-16 from being held as two bf16 parts
+    # (f32: 2^-24, within the same bound); it passes through the second products
+    a = np.abs
+    eZ = chain(n) * (a(x) @ a(v)) + 2.0 ** -16 * a(x @ v)
+    eG = chain(m) * (a(dy) @ a(u)) + 2.0 ** -16 * a(dy @ u)
+    dU, dV, dX = hsl.mx8_factor_grad(X, dY, U, V, dx=True, add=add)
+    close(dU, wU, a(dy).T @ a(x @ v), T, dtype, a(dy).T @ eZ * 1.01)
+    close(dV, wV, a(x).T @ a(dy @ u), T, dtype, a(x).T @ eG * 1.01)
+    close(dX, wX, a(dy @ u) @ a(v).T + a(ad), r, dtype, eG @ a(v).T * 1.01)
+    two = hsl.mx8_factor_grad(X, dY, U, V)
+    assert len(two) == 2 and torch.equal(two[0], dU) and torch.equal(two[1], dV)
+    plain = hsl.mx8_factor_grad(X, dY, U, V, dx=True)[2]
+    close(plain, wX - ad, a(dy @ u) @ a(v).T, r, dtype, eG @ a(v).T * 1.01)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,m,n,r", GRAD_SIZES)
+def test_factor_grad(hsl, T, m, n, r, dtype):
+    grad_check(hsl, T, m, n, r, dtype, T + m)
+
+
+def test_no_tokens(hsl):
+    D, _ = blocks(hsl, weights(5, 40, 1), "e2m1")
+    for dt in (torch.float32, torch.bfloat16):
+        assert hsl.mx4_apply(D, torch.empty(0, 40, dtype=dt, device="cuda")).shape == (0, 5)
+        assert hsl.mx4_apply_t(D, torch.empty(0, 5, dtype=dt, device="cuda")).shape == (0, 40)
+        X = hsl.mx_quantize(torch.empty(0, 40, dtype=dt, device="cuda"), "int8")
+        U, V = torch.ones(5, 3, dtype=dt, device="cuda"), torch.ones(40, 3, dtype=dt, device="cuda")
+        dU, dV, dX = hsl.mx8_factor_grad(X, torch.empty(0, 5, dtype=dt, device="cuda"), U, V, dx=True)
+        assert not dU.any() and not dV.any() and dX.shape == (0, 40)
+    E = hsl.mx_quantize(torch.empty(0, 40, device="cuda"))
+    assert hsl.mx4_matmul(E, D).shape == (0, 5) and hsl.mx4_matmul(D, E).shape == (5, 0)
+    # a D of no rows: the gradient is add, or zero
+    dY = torch.empty(3, 0, dtype=torch.bfloat16, device="cuda")
+    assert not hsl.mx4_apply_t(E, dY).any()
+    one = torch.ones(3, 40, dtype=torch.bfloat16, device="cuda")
+    assert torch.equal(hsl.mx4_apply_t(E, dY, add=one), one)
