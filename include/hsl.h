@@ -321,7 +321,7 @@ hsl_status hsl_set_permutation(hsl_handle h, const int32_t* row_order, const int
  * the sizes of a call (16-byte aligned; contents need not survive the call, and
  * calls that may overlap need one each).  The device of the pointers and the
  * stream must be current.  All are asynchronous on s, allocate nothing and can
- * be captured. */
+ * be captured.  Rows, columns and batches are at most 2^30. */
 typedef enum { HSL_MX_E2M1 = 0, HSL_MX_INT8 = 1 } hsl_mx_elem;
 typedef struct {
   const void* codes;
@@ -395,6 +395,12 @@ hsl_status hsl_mx4_matmul(const hsl_mx* A, const hsl_mx* B, const void* add, voi
 hsl_status hsl_mx8_factor_grad(const hsl_mx* X, const void* dY, int64_t m, const void* U,
                                const void* V, int32_t r, const void* add, void* dU, void* dV, void* dX,
                                hsl_dtype dtype, void* ws, size_t ws_bytes, hsl_stream s);
+
+/* Synchronise s and return, then clear, the device-side error of the microscaled
+ * operators on the current device: HSL_ERR_TIMEOUT if a bounded device wait of
+ * any of them gave up (its output is then incomplete), HSL_OK if none did.
+ * [HSS] §Risks and mitigations, risk 1, as hsl_check. */
+hsl_status hsl_mx_check(hsl_stream s);
 
 /* Synchronise s and return, then clear, the device-side error of the handle
  * (HSL_ERR_NAN_INPUT, HSL_ERR_TIMEOUT) — HSL_OK if none.

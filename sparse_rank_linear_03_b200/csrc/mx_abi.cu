@@ -23,7 +23,8 @@ hsl_status not_supported(const char* why) {
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 bool dtype_ok(hsl_dtype d) { return d == HSL_F32 || d == HSL_BF16; }
-bool size_ok(int64_t v) { return v >= 1 && v <= INT32_MAX; }
+constexpr int64_t kMaxSize = int64_t(1) << 30;  // rows, columns, tokens: indices stay in 32 bits
+bool size_ok(int64_t v) { return v >= 1 && v <= kMaxSize; }
 
 // The checks that every operator makes of a matrix in blocks.
 hsl_status check_mx(const hsl_mx* q, int elem, const char* what) {
@@ -33,7 +34,7 @@ hsl_status check_mx(const hsl_mx* q, int elem, const char* what) {
   if (elem >= 0 && int(q->elem) != elem)
     return not_supported((std::string(what) + (elem == HSL_MX_E2M1 ? " must hold e2m1 blocks"
                                                                      : " must hold int8 blocks")).c_str());
-  if (q->rows < 0 || q->rows > INT32_MAX || !size_ok(q->cols))
+  if (q->rows < 0 || q->rows > kMaxSize || !size_ok(q->cols))
     return bad_arg((std::string(what) + ": rows or cols out of range").c_str());
   if (q->rows > 0 && (!q->codes || !q->scales))
     return bad_arg((std::string(what) + ": codes/scales is NULL").c_str());
@@ -64,10 +65,13 @@ MxOperand operand(const void* p, hsl_dtype dt, int64_t pitch, bool trans) {
 }
 
 size_t workspace_bytes(hsl_mx_op op, int64_t T, int64_t m, int64_t n, int64_t r, hsl_dtype dt) {
-  switch (op) {
-    case HSL_MX_OP_FACTOR_GRAD: return size_t(2 * T * r * 4);
-    default: return 0;
-  }
+  const size_t simt = op == HSL_MX_OP_FACTOR_GRAD ? size_t(2 * T * r * 4) : 0;
+  if (dt == HSL_F32 || T == 0 || m == 0) return simt;
+  size_t tc = 0;
+  if (op == HSL_MX_OP_APPLY || op == HSL_MX_OP_APPLY_T)
+    tc = mx_gemm_apply_workspace(op == HSL_MX_OP_APPLY_T, T, m, n);
+  if (op == HSL_MX_OP_FACTOR_GRAD && r > 0) tc = mx_gemm_grad_workspace(T, m, n, r);
+  return simt > tc ? simt : tc;
 }
 
 hsl_status check_workspace(const void* ws, size_t have, size_t need) {
@@ -123,7 +127,7 @@ hsl_status hsl_mx_workspace(hsl_mx_op op, int64_t batch, int64_t m, int64_t n, i
   if (!bytes) return bad_arg("bytes is NULL");
   if (op < HSL_MX_OP_APPLY || op > HSL_MX_OP_FACTOR_GRAD) return bad_arg("unknown operator");
   if (!dtype_ok(dtype)) return bad_arg("unknown dtype");
-  if (batch < 0 || batch > INT32_MAX || m < 0 || m > INT32_MAX || !size_ok(n) || r < 0 || r > 256)
+  if (batch < 0 || batch > kMaxSize || m < 0 || m > kMaxSize || !size_ok(n) || r < 0 || r > 256)
     return bad_arg("a size is out of range");
   *bytes = workspace_bytes(op, batch, m, n, r, dtype);
   return HSL_OK;
@@ -134,13 +138,15 @@ hsl_status hsl_mx4_apply(const hsl_mx* D, const void* X, const void* add, void* 
   set_message("");
   if (!dtype_ok(dtype)) return bad_arg("unknown dtype");
   if (hsl_status e = check_mx(D, HSL_MX_E2M1, "D")) return e;
-  if (batch < 0 || batch > INT32_MAX) return bad_arg("batch out of range");
+  if (batch < 0 || batch > kMaxSize) return bad_arg("batch out of range");
   if (batch == 0 || D->rows == 0) return HSL_OK;
   if (!X || !Y) return bad_arg("X/Y is NULL");
   if (hsl_status e = check_workspace(ws, ws_bytes,
                                      workspace_bytes(HSL_MX_OP_APPLY, batch, D->rows, D->cols, 0, dtype)))
     return e;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dtype == HSL_BF16 && mx_gemm_supported(X))
+    return mx_gemm_apply_run(false, operand(D, false), D->rows, D->cols, X, add, Y, batch, ws, s);
   return mx_simt_run(operand(X, dtype, D->cols, false), operand(D, false), batch, D->rows, D->cols,
                      add, Y, dtype, s);
 }
@@ -150,13 +156,15 @@ hsl_status hsl_mx4_apply_t(const hsl_mx* D, const void* dY, const void* add, voi
   set_message("");
   if (!dtype_ok(dtype)) return bad_arg("unknown dtype");
   if (hsl_status e = check_mx(D, HSL_MX_E2M1, "D")) return e;
-  if (batch < 0 || batch > INT32_MAX) return bad_arg("batch out of range");
+  if (batch < 0 || batch > kMaxSize) return bad_arg("batch out of range");
   if (batch == 0) return HSL_OK;
   if (!dX || (D->rows > 0 && !dY)) return bad_arg("dY/dX is NULL");
   if (hsl_status e = check_workspace(ws, ws_bytes,
                                      workspace_bytes(HSL_MX_OP_APPLY_T, batch, D->rows, D->cols, 0, dtype)))
     return e;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dtype == HSL_BF16 && D->rows > 0 && mx_gemm_supported(dY))
+    return mx_gemm_apply_run(true, operand(D, true), D->rows, D->cols, dY, add, dX, batch, ws, s);
   return mx_simt_run(operand(dY, dtype, D->rows, false), operand(D, true), batch, D->cols, D->rows,
                      add, dX, dtype, s);
 }
@@ -193,6 +201,8 @@ hsl_status hsl_mx8_factor_grad(const hsl_mx* X, const void* dY, int64_t m, const
                                      workspace_bytes(HSL_MX_OP_FACTOR_GRAD, T, m, n, r, dtype)))
     return e;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dtype == HSL_BF16 && T > 0 && mx_gemm_supported(dY) && mx_gemm_supported(U) && mx_gemm_supported(V))
+    return mx_gemm_grad_run(operand(X, false), T, n, dY, m, U, V, r, add, dU, dV, dX, ws, s);
   float* Z = static_cast<float*>(ws);
   float* G = Z + T * r;
   const MxOperand x = operand(X, false), xt = operand(X, true);
@@ -208,6 +218,25 @@ hsl_status hsl_mx8_factor_grad(const hsl_mx* X, const void* dY, int64_t m, const
   if (!dX) return HSL_OK;
   return mx_simt_run(operand(G, HSL_F32, r, false), operand(V, dtype, r, false), T, n, r, add, dX, dtype,
                      s);
+}
+
+hsl_status hsl_mx_check(hsl_stream stream) {
+  set_message("");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (cudaError_t e = cudaStreamSynchronize(s)) return cuda_fail(e, "stream synchronize");
+  uint32_t* words[] = {nullptr};
+  if (cudaError_t e = mx_gemm_error_word(&words[0])) return cuda_fail(e, "error word address");
+  uint32_t all = 0;
+  for (uint32_t* p : words) {
+    uint32_t v = 0;
+    if (cudaError_t e = cudaMemcpy(&v, p, 4, cudaMemcpyDeviceToHost)) return cuda_fail(e, "error word read");
+    if (v == 0) continue;
+    all |= v;
+    if (cudaError_t e = cudaMemset(p, 0, 4)) return cuda_fail(e, "error word clear");
+  }
+  if (all == 0) return HSL_OK;
+  set_message("a bounded device wait gave up");
+  return HSL_ERR_TIMEOUT;
 }
 
 }  // extern "C"

@@ -1,0 +1,768 @@
+// Products on the tensor cores with one factor held in microscaled blocks.
+//
+//   C = A · (B0 + B1)ᵀ (+ add),   A [M][K], B [N][K], fp32 sums in TMEM
+//
+// A is the large factor: a 4-bit weight matrix, an 8-bit checkpoint, or a bf16
+// matrix, each either stored as [M][K] or used transposed from [K][M].  B is a bf16
+// matrix (tokens, factors), stored as [N][K] or [K][N]; B1 is the low part of a
+// value held as a bf16 pair.  The same kernel is the forward product (M = features,
+// N = tokens), its input gradient (the same matrix, transposed) and the four
+// skinny products of the factors' gradients (N = r).
+//
+// Blocks are widened to bf16 on their way into shared memory.  That is exact: an
+// e2m1 value has 2 significant bits and an int8 value 7, the block's scale is a
+// power of two, and bf16 has 8 significant bits and fp32's exponents (values
+// down to 2^−133 are bf16 subnormals).  So the products differ from the definition
+// by the rounding of the fp32 sums only.
+//
+// Both storage orders use the same shared-memory tile: rows of 64 values (128
+// bytes) in the 128-byte swizzle.  For [M][K] a tile row is a row of A and the 64
+// values run along K; for [K][M] a tile row is a k and the 64 values run along M,
+// which the MMA reads as an M-major operand.  Widening is the same either way: a
+// thread turns the one or two blocks of its tile row into 128 bytes.
+//
+//   warp 0 lane 0   TMA of the B tile(s), and of A when it is bf16
+//   warp 1 lane 0   tcgen05.mma, M = 128 per accumulator, N up to 256, K = 16
+//   warps 2-9       widen A's blocks (codes of the next K-block already in
+//                   registers); then the epilogue: tcgen05.ld, add, round, store
+//
+// MH = 2 gives the CTA two 128-row accumulators that share every B tile: a K-block
+// of 256 × 256 × 64 takes the MMAs about 1024 cycles, in which 32 KB of B and
+// 8 KB of codes arrive and the eight warps spend about 400 issue cycles widening.
+// Every wait is bounded.
+#include <cuda.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "common.cuh"
+#include "internal.h"
+#include "mx.cuh"
+#include "mx_ops.h"
+#include "tc.cuh"
+
+namespace hsl {
+namespace {
+
+__device__ uint32_t g_mx_gemm_err;
+
+constexpr int G_BK = 64;
+constexpr int G_THREADS = 320;
+constexpr int G_MAX_STAGES = 8;
+constexpr int G_SMEM_BUDGET = 200 * 1024;  // stages; the barriers and alignment take under 2 KB more
+
+enum AKind { A_BF16_K, A_BF16_M, A_E2M1_K, A_E2M1_M, A_INT8_K, A_INT8_M };
+enum OutKind { OUT_T, OUT_R, OUT_T_PART, OUT_R_PART };  // C[n][m] or C[m][n]; bf16 or fp32 partials
+
+constexpr bool a_is_blocks(int a) { return a >= A_E2M1_K; }
+constexpr bool a_is_mmajor(int a) { return a == A_BF16_M || a == A_E2M1_M || a == A_INT8_M; }
+constexpr bool a_is_int8(int a) { return a == A_INT8_K || a == A_INT8_M; }
+
+struct GemmMaps {
+  CUtensorMap a;   // bf16 A: box {64, 128} (K-major) or {64, 64}
+  CUtensorMap b0;  // B: box {64, BN} (K-major) or {64, 64}
+  CUtensorMap b1;  // low part
+  CUtensorMap c;   // OUT_T: box {128·MH, BN}
+};
+struct GemmArgs {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  int64_t cpitch, spitch;
+  int nb;            // blocks per stored row of A
+  int arows;         // stored rows of A
+  int M, N, nk;      // nk: K-blocks of 64
+  int BN, stages, splits;
+  int cstore;        // OUT_T: tiled store possible
+  const __nv_bfloat16* add;
+  __nv_bfloat16* C;
+  float* part;       // [splits][N][M] or [splits][M][N]
+};
+
+__device__ __forceinline__ bool g_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (*abort_flag) return false;
+  if (tc::mbar_wait(bar, parity, &g_mx_gemm_err)) return true;
+  *abort_flag = 1;
+  return false;
+}
+
+// M- or N-major operand in the 128-byte swizzle: 64 values along the row, 8 k per
+// 1024-byte atom; the next 64 values of the row dimension 8192 bytes on.
+__device__ __forceinline__ uint64_t desc_mn_sw128(const void* tile) {
+  const uint64_t addr = tc::smem_u32(tile);
+  uint64_t d = 0;
+  d |= (addr >> 4) & 0x3FFFull;
+  d |= uint64_t(8192 >> 4) << 16;  // leading byte offset: the next 64 values
+  d |= uint64_t(1024 >> 4) << 32;  // stride byte offset: the next 8 k
+  d |= uint64_t(1) << 46;
+  d |= uint64_t(2) << 61;          // SWIZZLE_128B
+  return d;
+}
+
+// ---- widening -----------------------------------------------------------------
+__device__ __forceinline__ uint32_t mul_bf2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t sub_bf2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// 2^(e − 127) as a pair of bf16 (2^−127 is a subnormal; 255 stands for NaN).
+__device__ __forceinline__ uint32_t e2m1_scale(uint32_t e) {
+  const uint32_t b = e == 255u ? 0x7FC0u : e == 0u ? 0x0040u : e << 7;
+  return b | (b << 16);
+}
+// 2^(e − 127) / 64 (down to the subnormal 2^−133).
+__device__ __forceinline__ uint32_t int8_scale(uint32_t e) {
+  const uint32_t b = e == 255u ? 0x7FC0u : e > 6u ? (e - 6u) << 7 : 1u << e;
+  return b | (b << 16);
+}
+
+// Eight e2m1 codes (one word) → eight bf16.  The high and the low byte of the
+// eight magnitudes are looked up by byte permutes (a code's three low bits are
+// the selector), the sign bits gathered by a third.
+__device__ __forceinline__ uint4 widen_e2m1(uint32_t w, uint32_t scale) {
+  const uint32_t mag = w & 0x77777777u, w4 = w << 4;
+  uint32_t hi = __byte_perm(0x3F3F3F00u, 0x40404040u, mag);
+  uint32_t lo = __byte_perm(0xC0800000u, 0xC0804000u, mag);
+  hi |= __byte_perm(w4, w, 0x5140) & 0x80808080u;
+  uint4 v;
+  v.x = mul_bf2(__byte_perm(lo, hi, 0x5140), scale);
+  v.y = mul_bf2(__byte_perm(lo, hi, 0x7362), scale);
+  const uint32_t mag2 = mag >> 16;
+  hi = __byte_perm(0x3F3F3F00u, 0x40404040u, mag2);
+  lo = __byte_perm(0xC0800000u, 0xC0804000u, mag2);
+  hi |= __byte_perm(w4, w, 0x7362) & 0x80808080u;
+  v.z = mul_bf2(__byte_perm(lo, hi, 0x5140), scale);
+  v.w = mul_bf2(__byte_perm(lo, hi, 0x7362), scale);
+  return v;
+}
+// Four int8 (one word) → four bf16: 128 + (low 7 bits) is 0x4300 | bits, from which
+// 128 (0x4300) or, for a negative value, 256 (0x4380) is taken away.
+__device__ __forceinline__ uint2 widen_int8(uint32_t w, uint32_t scale) {
+  const uint32_t m = w & 0x7F7F7F7Fu, n = w & 0x80808080u;
+  uint2 v;
+  v.x = mul_bf2(sub_bf2(__byte_perm(m, 0x43434343u, 0x4140), __byte_perm(n, 0x43434343u, 0x4140)), scale);
+  v.y = mul_bf2(sub_bf2(__byte_perm(m, 0x43434343u, 0x4342), __byte_perm(n, 0x43434343u, 0x4342)), scale);
+  return v;
+}
+
+// The codes and scale of one block of 32.
+template <bool kInt8>
+struct Block {
+  uint4 c[kInt8 ? 2 : 1];
+  uint32_t e;
+};
+template <bool kInt8>
+__device__ __forceinline__ void fetch(Block<kInt8>& b, const GemmArgs& g, int row, int blk) {
+  if (row < g.arows && blk < g.nb) {
+    const uint8_t* p = g.codes + int64_t(row) * g.cpitch + int64_t(blk) * (kInt8 ? 32 : 16);
+    b.c[0] = ld_stream16(p);
+    if (kInt8) b.c[1] = ld_stream16(p + 16);
+    b.e = __ldg(g.scales + int64_t(row) * g.spitch + blk);
+  } else {
+    b.c[0] = make_uint4(0, 0, 0, 0);
+    if (kInt8) b.c[1] = make_uint4(0, 0, 0, 0);
+    b.e = 0;
+  }
+}
+// Writes the block's 32 bf16 to chunks 4·half .. 4·half + 3 of tile row `row`.
+template <bool kInt8>
+__device__ __forceinline__ void widen(const Block<kInt8>& b, unsigned char* tile, int row, int half) {
+  unsigned char* r = tile + row * 128;
+  const int x = row & 7;
+  if (kInt8) {
+    const uint32_t s = int8_scale(b.e);
+    const uint32_t w[8] = {b.c[0].x, b.c[0].y, b.c[0].z, b.c[0].w,
+                           b.c[kInt8 ? 1 : 0].x, b.c[kInt8 ? 1 : 0].y, b.c[kInt8 ? 1 : 0].z,
+                           b.c[kInt8 ? 1 : 0].w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint2 lo = widen_int8(w[2 * q], s), hi = widen_int8(w[2 * q + 1], s);
+      *reinterpret_cast<uint4*>(r + (((half * 4 + q) ^ x) << 4)) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    }
+  } else {
+    const uint32_t s = e2m1_scale(b.e);
+    const uint32_t w[4] = {b.c[0].x, b.c[0].y, b.c[0].z, b.c[0].w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<uint4*>(r + (((half * 4 + q) ^ x) << 4)) = widen_e2m1(w[q], s);
+  }
+}
+
+template <int AK, bool BMN, int TERMS, int MH, int OUT>
+__global__ void __launch_bounds__(G_THREADS, 1)
+    k_mx_gemm(const __grid_constant__ GemmMaps maps, const GemmArgs g) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t full[G_MAX_STAGES], empty[G_MAX_STAGES], accf;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ntn = (g.N + g.BN - 1) / g.BN;
+  const int tile = blockIdx.x / g.splits, split = blockIdx.x % g.splits;
+  const int i0 = (tile / ntn) * (128 * MH), j0 = (tile % ntn) * g.BN;
+  const int kb0 = int(int64_t(g.nk) * split / g.splits);
+  const int nk = int(int64_t(g.nk) * (split + 1) / g.splits) - kb0;
+  constexpr int kA = MH * 128 * 128;  // bytes of the A tile
+  const int bgroups = (g.BN + 63) / 64;
+  const int kB = BMN ? bgroups * 8192 : g.BN * 128;
+  const int kStage = kA + TERMS * kB;
+  uint32_t cols = MH == 2 ? 64 : 32;  // whole 32-column reads past 2 × 16 columns stay inside
+  while (cols < uint32_t(MH * g.BN)) cols *= 2;
+
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int s = 0; s < g.stages; ++s) {
+      tc::mbar_init(&full[s], a_is_blocks(AK) ? 1 + 8 : 1);  // copies, and the eight widening warps
+      tc::mbar_init(&empty[s], 1);
+    }
+    tc::mbar_init(&accf, 1);
+    tc::fence_mbar_init();
+    tc::prefetch_tmap(&maps.b0);
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(&tmem_slot, cols);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  volatile int* abrt = &abort_flag;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int s = 0, issued = 0;
+      uint32_t ph = 1;
+      for (int kb = 0; kb < nk; ++kb) {
+        if (!g_wait(&empty[s], ph, abrt)) break;
+        unsigned char* a = smem + s * kStage;
+        unsigned char* b = a + kA;
+        const int k0 = (kb0 + kb) * G_BK;
+        tc::mbar_expect_tx(&full[s], (a_is_blocks(AK) ? 0 : kA) + TERMS * kB);
+        if (AK == A_BF16_K) {
+#pragma unroll
+          for (int h = 0; h < MH; ++h)
+            tc::tma_load_2d(a + h * 16384, &maps.a, k0, i0 + h * 128, &full[s]);
+        } else if (AK == A_BF16_M) {
+#pragma unroll
+          for (int h = 0; h < 2 * MH; ++h)
+            tc::tma_load_2d(a + h * 8192, &maps.a, i0 + h * 64, k0, &full[s]);
+        }
+#pragma unroll
+        for (int t = 0; t < TERMS; ++t) {
+          const CUtensorMap* map = t ? &maps.b1 : &maps.b0;
+          if (BMN) {
+            for (int q = 0; q < bgroups; ++q)
+              tc::tma_load_2d(b + t * kB + q * 8192, map, j0 + q * 64, k0, &full[s]);
+          } else {
+            tc::tma_load_2d(b + t * kB, map, k0, j0, &full[s]);
+          }
+        }
+        ++issued;
+        if (++s == g.stages) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+      // the copies in flight have landed before the CTA's shared memory is given up
+      for (int q = 0; q < g.stages && q < issued; ++q) {
+        const int last = (issued - 1 - q) / g.stages;  // uses of stage q before its last one
+        if (*abrt) tc::mbar_wait(&full[q], uint32_t(last) & 1, &g_mx_gemm_err);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = tc::idesc_bf16(128, g.BN) | (a_is_mmajor(AK) ? 1u << 15 : 0u) |
+                             (BMN ? 1u << 16 : 0u);
+      int s = 0;
+      uint32_t ph = 0;
+      for (int kb = 0; kb < nk; ++kb) {
+        if (!g_wait(&full[s], ph, abrt)) break;
+        tc::tc_fence_after();
+        unsigned char* a = smem + s * kStage;
+#pragma unroll
+        for (int t = 0; t < TERMS; ++t) {
+          const uint64_t bd = BMN ? desc_mn_sw128(a + kA + t * kB) : tc::desc_sw128(a + kA + t * kB);
+#pragma unroll
+          for (int h = 0; h < MH; ++h) {
+            const uint64_t ad =
+                a_is_mmajor(AK) ? desc_mn_sw128(a + h * 16384) : tc::desc_sw128(a + h * 16384);
+#pragma unroll
+            for (int k = 0; k < G_BK / 16; ++k)
+              tc::mma_bf16(tmem + h * g.BN, tc::desc_advance(ad, k * (a_is_mmajor(AK) ? 2048 : 32)),
+                           tc::desc_advance(bd, k * (BMN ? 2048 : 32)), idesc,
+                           (kb > 0 || k > 0 || t > 0) ? 1u : 0u);
+          }
+        }
+        tc::mma_commit(&empty[s]);
+        if (++s == g.stages) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+      tc::mma_commit(&accf);
+    }
+    __syncwarp();
+  } else {
+    const int tid = threadIdx.x - 64;
+    if (a_is_blocks(AK)) {
+      constexpr bool kInt8 = a_is_int8(AK);
+      // MH = 2: tile row tid, both blocks; MH = 1: two threads share a tile row
+      const int trow = MH == 2 ? tid : (tid & 127);
+      const int half0 = MH == 2 ? 0 : (tid >> 7);
+      // stored row and block of this tile row at K-block kb
+      const int row0 = a_is_mmajor(AK) ? (trow & 63) : i0 + trow;
+      const int blk0 = (a_is_mmajor(AK) ? i0 / 32 + (trow >> 6) * 2 : 0) + half0;
+      Block<kInt8> cur[MH], nxt[MH];
+      auto get = [&](Block<kInt8>(&b)[MH], int kb) {
+        const int row = a_is_mmajor(AK) ? row0 + kb * G_BK : row0;
+        const int blk = a_is_mmajor(AK) ? blk0 : blk0 + kb * 2;
+#pragma unroll
+        for (int q = 0; q < MH; ++q) fetch(b[q], g, row, blk + q);
+      };
+      if (nk > 0) get(cur, kb0);
+      int s = 0;
+      uint32_t ph = 1;
+      for (int kb = 0; kb < nk; ++kb) {
+        if (kb + 1 < nk) get(nxt, kb0 + kb + 1);
+        if (!g_wait(&empty[s], ph, abrt)) break;
+        unsigned char* a = smem + s * kStage;
+#pragma unroll
+        for (int q = 0; q < MH; ++q) widen(cur[q], a, trow, half0 + q);
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&full[s]);
+#pragma unroll
+        for (int q = 0; q < MH; ++q) cur[q] = nxt[q];
+        if (++s == g.stages) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    // epilogue: warp w reaches TMEM lanes 32 (w mod 4) onwards; with two
+    // accumulators warps 2-5 take the first, 6-9 the second; with one, 6-9 take
+    // the upper half of the columns
+    __syncwarp();
+    const bool ok = tc::mbar_wait(&accf, 0, &g_mx_gemm_err) && !*abrt;
+    __nv_bfloat16* stg = reinterpret_cast<__nv_bfloat16*>(smem);
+    if (ok) {
+      tc::tc_fence_after();
+      const int grp = warp >= 6 ? 1 : 0;
+      const int L = ((warp & 3) << 5) | lane;
+      const int R = (MH == 2 ? grp * 128 : 0) + L;
+      const int i = i0 + R;
+      const uint32_t tb =
+          tmem + (uint32_t((warp & 3) * 32) << 16) + (MH == 2 ? uint32_t(grp * g.BN) : 0u);
+      // columns in steps of 32 (the last step may reach past BN, inside the allocation)
+      const int steps = (g.BN + 31) / 32;
+      const int c_lo = MH == 2 ? 0 : (grp ? (steps + 1) / 2 : 0);
+      const int c_hi = MH == 2 ? steps : (grp ? steps : (steps + 1) / 2);
+#pragma unroll 1
+      for (int c = c_lo; c < c_hi; ++c) {
+        const int c0 = c * 32;
+        float v[32];
+        tc::tmem_ld32(tb + c0, v);
+        if (nk == 0) {
+#pragma unroll
+          for (int q = 0; q < 32; ++q) v[q] = 0.f;
+        }
+        const int jn = min(32, min(g.BN - c0, g.N - j0 - c0));  // columns of this step in the tile
+        if (OUT == OUT_T || OUT == OUT_T_PART) {
+          if (OUT == OUT_T_PART) {
+            float* p = g.part + (int64_t(split) * g.N + j0 + c0) * g.M + i;
+            if (i < g.M) {
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                if (q < jn) p[int64_t(q) * g.M] = v[q];
+            }
+          } else {
+            if (g.add && i < g.M) {
+              const __nv_bfloat16* p = g.add + int64_t(j0 + c0) * g.M + i;
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                if (q < jn) v[q] += __bfloat162float(p[int64_t(q) * g.M]);
+            }
+            if (g.cstore) {
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                if (c0 + q < g.BN) stg[(c0 + q) * (128 * MH) + R] = __float2bfloat16_rn(v[q]);
+            } else if (i < g.M) {
+              __nv_bfloat16* p = g.C + int64_t(j0 + c0) * g.M + i;
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                if (q < jn) p[int64_t(q) * g.M] = __float2bfloat16_rn(v[q]);
+            }
+          }
+        } else if (i < g.M && jn > 0) {
+          if (OUT == OUT_R_PART) {
+            float* p = g.part + (int64_t(split) * g.M + i) * g.N + j0 + c0;
+            if (jn == 32 && g.N % 4 == 0) {
+#pragma unroll
+              for (int q = 0; q < 32; q += 4)
+                *reinterpret_cast<float4*>(p + q) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
+            } else {
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                if (q < jn) p[q] = v[q];
+            }
+          } else {
+            __nv_bfloat16* p = g.C + int64_t(i) * g.N + j0 + c0;
+            if (jn == 32 && g.cstore) {  // rows of C start on 16 bytes
+#pragma unroll
+              for (int q = 0; q < 32; q += 8) {
+                uint4 o;
+                uint32_t* w = &o.x;
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                  const __nv_bfloat162 h = __floats2bfloat162_rn(v[q + 2 * z], v[q + 2 * z + 1]);
+                  w[z] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+                *reinterpret_cast<uint4*>(p + q) = o;
+              }
+            } else {
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                if (q < jn) p[q] = __float2bfloat16_rn(v[q]);
+            }
+          }
+        }
+      }
+    } else {
+      *abrt = 1;
+    }
+    if (OUT == OUT_T && g.cstore) {
+      // the rounded tile [column][row] lies in the idle ring: one tiled store.  All eight
+      // warps meet here, whether or not a wait gave up before.
+      tc::fence_async_smem();
+      asm volatile("barrier.sync 1, 256;" ::: "memory");
+      if (tid == 0 && ok && !*abrt) {
+        tc::tma_store_2d(&maps.c, stg, i0, j0);
+        tc::bulk_commit();
+        tc::bulk_wait_read_all();
+      }
+    }
+  }
+  tc::tc_fence_before();
+  tc::cta_sync();
+  if (warp == 1) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, cols);
+  }
+}
+
+// Σ over the splits' partials in split order, then add and round: to bf16, or to a bf16 pair
+// (hi + lo carries 16 significant bits) whose rows are padded to `pitch` with zeros.
+__global__ void __launch_bounds__(256)
+    k_mx_reduce(const float* __restrict__ part, int splits, int64_t count, const __nv_bfloat16* add,
+                __nv_bfloat16* C) {
+  const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (e >= count) return;
+  float v = part[e];
+  for (int s = 1; s < splits; ++s) v += part[int64_t(s) * count + e];
+  if (add) v += __bfloat162float(add[e]);
+  C[e] = __float2bfloat16_rn(v);
+}
+__global__ void __launch_bounds__(256)
+    k_mx_reduce_pair(const float* __restrict__ part, int splits, int64_t rows, int n, int pitch,
+                     __nv_bfloat16* __restrict__ hi, __nv_bfloat16* __restrict__ lo) {
+  const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (e >= rows * pitch) return;
+  const int64_t row = e / pitch;
+  const int c = int(e - row * pitch);
+  float v = 0.f;
+  if (c < n)
+    for (int s = 0; s < splits; ++s) v += part[(int64_t(s) * rows + row) * n + c];
+  const __nv_bfloat16 h = __float2bfloat16_rn(v);
+  hi[e] = h;
+  lo[e] = __float2bfloat16_rn(v - __bfloat162float(h));
+}
+// Rows of n bf16 to rows of `pitch` (a multiple of 8, so that a tile copy can read them).
+__global__ void __launch_bounds__(256)
+    k_mx_pad_rows(const uint16_t* __restrict__ src, int64_t rows, int n, int pitch,
+                  uint16_t* __restrict__ dst) {
+  const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (e >= rows * pitch) return;
+  const int64_t row = e / pitch;
+  const int c = int(e - row * pitch);
+  dst[e] = c < n ? src[row * n + c] : uint16_t(0);
+}
+
+unsigned blocks_of(int64_t count) { return unsigned((count + 255) / 256); }
+
+// ---- host ---------------------------------------------------------------------
+struct GemmShape {
+  int BN, MH, splits, stages;
+};
+
+int stage_bytes(bool bmn, int terms, int mh, int bn) {
+  return mh * 16384 + terms * (bmn ? (bn + 63) / 64 * 8192 : bn * 128);
+}
+
+// Tile and split of an M × N × K product.
+GemmShape shape_of(int64_t M, int64_t N, int64_t K, bool bmn, int terms, bool may_split) {
+  GemmShape s;
+  const int64_t ntn = (N + 255) / 256;
+  s.BN = int(round_up((N + ntn - 1) / ntn, 16));
+  const int64_t t2 = (M + 255) / 256 * ntn;
+  s.MH = t2 >= 148 ? 2 : 1;
+  const int64_t tiles = s.MH == 2 ? t2 : (M + 127) / 128 * ntn;
+  const int64_t nk = (K + 63) / 64;
+  s.splits = 1;
+  if (may_split && tiles < 148)
+    s.splits = int(std::max<int64_t>(1, std::min<int64_t>(148 / tiles, nk / 4)));
+  s.stages = std::min(G_MAX_STAGES, G_SMEM_BUDGET / stage_bytes(bmn, terms, s.MH, s.BN));
+  return s;
+}
+
+template <int AK, bool BMN, int TERMS, int MH, int OUT>
+hsl_status launch_gemm(const GemmMaps& maps, const GemmArgs& g, cudaStream_t s) {
+  void (*fn)(const GemmMaps, const GemmArgs) = k_mx_gemm<AK, BMN, TERMS, MH, OUT>;
+  int bytes = g.stages * stage_bytes(BMN, TERMS, MH, g.BN);
+  if (OUT == OUT_T) bytes = std::max(bytes, MH * 128 * g.BN * 2);  // the epilogue's tile
+  bytes += 1024;
+  if (cudaError_t e = allow_dyn_smem(reinterpret_cast<const void*>(fn), bytes))
+    return cuda_fail(e, "block product smem attribute");
+  const int64_t tiles = int64_t((g.M + 128 * MH - 1) / (128 * MH)) * ((g.N + g.BN - 1) / g.BN);
+  note_launch();
+  fn<<<unsigned(tiles * g.splits), G_THREADS, size_t(bytes), s>>>(maps, g);
+  return cuda_fail(cudaGetLastError(), "block product launch");
+}
+template <int AK, bool BMN, int TERMS, int OUT>
+hsl_status launch_gemm(int mh, const GemmMaps& maps, const GemmArgs& g, cudaStream_t s) {
+  return mh == 2 ? launch_gemm<AK, BMN, TERMS, 2, OUT>(maps, g, s)
+                 : launch_gemm<AK, BMN, TERMS, 1, OUT>(maps, g, s);
+}
+
+const auto kBF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+const auto kSW = CU_TENSOR_MAP_SWIZZLE_128B;
+
+hsl_status map_failed() {
+  set_message("tensor map encoding failed");
+  return HSL_ERR_CUDA;
+}
+
+int64_t up16(int64_t b) { return (b + 255) / 256 * 256; }
+
+hsl_status pad_rows(const void* src, int64_t rows, int64_t n, int64_t pitch, void* dst, cudaStream_t s) {
+  note_launch();
+  k_mx_pad_rows<<<blocks_of(rows * pitch), 256, 0, s>>>(static_cast<const uint16_t*>(src), rows, int(n),
+                                                        int(pitch), static_cast<uint16_t*>(dst));
+  return cuda_fail(cudaGetLastError(), "row padding launch");
+}
+
+}  // namespace
+
+// ---- Y = X Dᵀ and dX = dY D -----------------------------------------------------
+size_t mx_gemm_apply_workspace(bool trans, int64_t T, int64_t m, int64_t n) {
+  const int64_t M = trans ? n : m, K = trans ? m : n;
+  const GemmShape sh = shape_of(M, T, K, false, 1, true);
+  size_t b = 0;
+  if (K % 8) b += up16(T * round_up(K, 8) * 2);
+  if (sh.splits > 1) b += up16(int64_t(sh.splits) * T * M * 4);
+  return b;
+}
+
+bool mx_gemm_supported(const void* X) {
+  return reinterpret_cast<uintptr_t>(X) % 16 == 0 && tmap_available();
+}
+
+hsl_status mx_gemm_apply_run(bool trans, const MxOperand& D, int64_t m, int64_t n, const void* X,
+                             const void* add, void* Y, int64_t T, void* ws, cudaStream_t s) {
+  const int64_t M = trans ? n : m, K = trans ? m : n;
+  const GemmShape sh = shape_of(M, T, K, false, 1, true);
+  unsigned char* w = static_cast<unsigned char*>(ws);
+  int64_t kp = K;
+  if (K % 8) {
+    kp = round_up(K, 8);
+    if (hsl_status e = pad_rows(X, T, K, kp, w, s)) return e;
+    X = w;
+    w += up16(T * kp * 2);
+  }
+  GemmMaps maps;
+  memset(&maps, 0, sizeof(maps));
+  GemmArgs g = {};
+  g.codes = static_cast<const uint8_t*>(D.p);
+  g.scales = D.scales;
+  g.cpitch = D.pitch;
+  g.spitch = D.spitch;
+  g.nb = int(mx::blocks(n));
+  g.arows = int(m);
+  g.M = int(M);
+  g.N = int(T);
+  g.nk = int((K + G_BK - 1) / G_BK);
+  g.BN = sh.BN;
+  g.stages = sh.stages;
+  g.splits = sh.splits;
+  g.add = static_cast<const __nv_bfloat16*>(add);
+  g.C = static_cast<__nv_bfloat16*>(Y);
+  g.part = reinterpret_cast<float*>(w);
+  if (!make_tmap_2d(&maps.b0, kBF, 2, X, T, K, kp, 64, sh.BN, kSW)) return map_failed();
+  if (sh.splits > 1) {
+    if (hsl_status e = trans ? launch_gemm<A_E2M1_M, false, 1, OUT_T_PART>(sh.MH, maps, g, s)
+                             : launch_gemm<A_E2M1_K, false, 1, OUT_T_PART>(sh.MH, maps, g, s))
+      return e;
+    note_launch();
+    k_mx_reduce<<<blocks_of(T * M), 256, 0, s>>>(g.part, sh.splits, T * M, g.add, g.C);
+    return cuda_fail(cudaGetLastError(), "split sum launch");
+  }
+  g.cstore = (M % 8 == 0 && reinterpret_cast<uintptr_t>(Y) % 16 == 0) ? 1 : 0;
+  if (g.cstore && !make_tmap_2d(&maps.c, kBF, 2, Y, T, M, M, 128 * sh.MH, sh.BN,
+                                CU_TENSOR_MAP_SWIZZLE_NONE))
+    return map_failed();
+  return trans ? launch_gemm<A_E2M1_M, false, 1, OUT_T>(sh.MH, maps, g, s)
+               : launch_gemm<A_E2M1_K, false, 1, OUT_T>(sh.MH, maps, g, s);
+}
+
+// ---- gradients of the factors ----------------------------------------------------
+namespace {
+struct GradPlan {
+  int64_t rp, mp;             // padded pitches of r- and m-wide rows
+  GemmShape z, g, u, v, x;
+  size_t off_dy, off_u, off_v, off_zh, off_zl, off_gh, off_gl, off_part, total;
+};
+GradPlan grad_plan(int64_t T, int64_t m, int64_t n, int64_t r) {
+  GradPlan p;
+  p.rp = round_up(r, 8);
+  p.mp = round_up(m, 8);
+  p.z = shape_of(T, r, n, true, 1, true);
+  p.g = shape_of(T, r, m, true, 1, true);
+  p.u = shape_of(m, r, T, true, 2, true);
+  p.v = shape_of(n, r, T, true, 2, true);
+  p.x = shape_of(n, T, r, false, 2, false);
+  size_t o = 0;
+  auto take = [&](int64_t bytes) {
+    const size_t at = o;
+    o += size_t(up16(bytes));
+    return at;
+  };
+  p.off_dy = take(m % 8 ? T * p.mp * 2 : 0);
+  p.off_u = take(r % 8 ? m * p.rp * 2 : 0);
+  p.off_v = take(r % 8 ? n * p.rp * 2 : 0);
+  p.off_zh = take(T * p.rp * 2);
+  p.off_zl = take(T * p.rp * 2);
+  p.off_gh = take(T * p.rp * 2);
+  p.off_gl = take(T * p.rp * 2);
+  int64_t part = int64_t(std::max(p.z.splits, p.g.splits)) * T * r * 4;
+  if (p.u.splits > 1) part = std::max(part, int64_t(p.u.splits) * m * r * 4);
+  if (p.v.splits > 1) part = std::max(part, int64_t(p.v.splits) * n * r * 4);
+  p.off_part = take(part);
+  p.total = o;
+  return p;
+}
+}  // namespace
+
+size_t mx_gemm_grad_workspace(int64_t T, int64_t m, int64_t n, int64_t r) {
+  return grad_plan(T, m, n, r).total;
+}
+
+hsl_status mx_gemm_grad_run(const MxOperand& X, int64_t T, int64_t n, const void* dY, int64_t m,
+                            const void* U, const void* V, int64_t r, const void* add, void* dU, void* dV,
+                            void* dX, void* ws, cudaStream_t s) {
+  const GradPlan p = grad_plan(T, m, n, r);
+  unsigned char* w = static_cast<unsigned char*>(ws);
+  if (m % 8) {
+    if (hsl_status e = pad_rows(dY, T, m, p.mp, w + p.off_dy, s)) return e;
+    dY = w + p.off_dy;
+  }
+  if (r % 8) {
+    if (hsl_status e = pad_rows(U, m, r, p.rp, w + p.off_u, s)) return e;
+    if (hsl_status e = pad_rows(V, n, r, p.rp, w + p.off_v, s)) return e;
+    U = w + p.off_u;
+    V = w + p.off_v;
+  }
+  __nv_bfloat16* zh = reinterpret_cast<__nv_bfloat16*>(w + p.off_zh);
+  __nv_bfloat16* zl = reinterpret_cast<__nv_bfloat16*>(w + p.off_zl);
+  __nv_bfloat16* gh = reinterpret_cast<__nv_bfloat16*>(w + p.off_gh);
+  __nv_bfloat16* gl = reinterpret_cast<__nv_bfloat16*>(w + p.off_gl);
+  float* part = reinterpret_cast<float*>(w + p.off_part);
+
+  GemmArgs base = {};
+  base.codes = static_cast<const uint8_t*>(X.p);
+  base.scales = X.scales;
+  base.cpitch = X.pitch;
+  base.spitch = X.spitch;
+  base.nb = int(mx::blocks(n));
+  base.arows = int(T);
+  base.part = part;
+  auto args = [&](const GemmShape& sh, int64_t M, int64_t N, int64_t K) {
+    GemmArgs g = base;
+    g.M = int(M);
+    g.N = int(N);
+    g.nk = int((K + G_BK - 1) / G_BK);
+    g.BN = sh.BN;
+    g.stages = sh.stages;
+    g.splits = sh.splits;
+    return g;
+  };
+  auto pair = [&](const GemmShape& sh, __nv_bfloat16* hi, __nv_bfloat16* lo) {
+    note_launch();
+    k_mx_reduce_pair<<<blocks_of(T * p.rp), 256, 0, s>>>(part, sh.splits, T, int(r), int(p.rp), hi, lo);
+    return cuda_fail(cudaGetLastError(), "split sum launch");
+  };
+  GemmMaps maps;
+  memset(&maps, 0, sizeof(maps));
+  {  // G = dY U
+    GemmArgs g = args(p.g, T, r, m);
+    if (!make_tmap_2d(&maps.a, kBF, 2, dY, T, m, p.mp, 64, 128, kSW) ||
+        !make_tmap_2d(&maps.b0, kBF, 2, U, m, r, p.rp, 64, 64, kSW))
+      return map_failed();
+    if (hsl_status e = launch_gemm<A_BF16_K, true, 1, OUT_R_PART>(p.g.MH, maps, g, s)) return e;
+    if (hsl_status e = pair(p.g, gh, gl)) return e;
+  }
+  {  // Z = X V
+    GemmArgs g = args(p.z, T, r, n);
+    if (!make_tmap_2d(&maps.b0, kBF, 2, V, n, r, p.rp, 64, 64, kSW)) return map_failed();
+    if (hsl_status e = launch_gemm<A_INT8_K, true, 1, OUT_R_PART>(p.z.MH, maps, g, s)) return e;
+    if (hsl_status e = pair(p.z, zh, zl)) return e;
+  }
+  auto second = [&](bool of_u, const GemmShape& sh, int64_t M, __nv_bfloat16* hi, __nv_bfloat16* lo,
+                    void* out) {
+    GemmArgs g = args(sh, M, r, T);
+    if (!make_tmap_2d(&maps.b0, kBF, 2, hi, T, r, p.rp, 64, 64, kSW) ||
+        !make_tmap_2d(&maps.b1, kBF, 2, lo, T, r, p.rp, 64, 64, kSW))
+      return map_failed();
+    if (of_u && !make_tmap_2d(&maps.a, kBF, 2, dY, T, m, p.mp, 64, 64, kSW)) return map_failed();
+    g.C = static_cast<__nv_bfloat16*>(out);
+    g.cstore = (r % 8 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0) ? 1 : 0;
+    if (sh.splits == 1)
+      return of_u ? launch_gemm<A_BF16_M, true, 2, OUT_R>(sh.MH, maps, g, s)
+                  : launch_gemm<A_INT8_M, true, 2, OUT_R>(sh.MH, maps, g, s);
+    if (hsl_status e = of_u ? launch_gemm<A_BF16_M, true, 2, OUT_R_PART>(sh.MH, maps, g, s)
+                            : launch_gemm<A_INT8_M, true, 2, OUT_R_PART>(sh.MH, maps, g, s))
+      return e;
+    note_launch();
+    k_mx_reduce<<<blocks_of(M * r), 256, 0, s>>>(part, sh.splits, M * r, nullptr, g.C);
+    return cuda_fail(cudaGetLastError(), "split sum launch");
+  };
+  if (hsl_status e = second(true, p.u, m, zh, zl, dU)) return e;
+  if (hsl_status e = second(false, p.v, n, gh, gl, dV)) return e;
+  if (!dX) return HSL_OK;
+  // dX = add + G Vᵀ: rows of V are A, tokens are B
+  GemmArgs g = args(p.x, n, T, r);
+  if (!make_tmap_2d(&maps.a, kBF, 2, V, n, r, p.rp, 64, 128, kSW) ||
+      !make_tmap_2d(&maps.b0, kBF, 2, gh, T, r, p.rp, 64, p.x.BN, kSW) ||
+      !make_tmap_2d(&maps.b1, kBF, 2, gl, T, r, p.rp, 64, p.x.BN, kSW))
+    return map_failed();
+  g.add = static_cast<const __nv_bfloat16*>(add);
+  g.C = static_cast<__nv_bfloat16*>(dX);
+  g.cstore = (n % 8 == 0 && reinterpret_cast<uintptr_t>(dX) % 16 == 0) ? 1 : 0;
+  if (g.cstore && !make_tmap_2d(&maps.c, kBF, 2, dX, T, n, n, 128 * p.x.MH, p.x.BN,
+                                CU_TENSOR_MAP_SWIZZLE_NONE))
+    return map_failed();
+  return launch_gemm<A_BF16_K, false, 2, OUT_T>(p.x.MH, maps, g, s);
+}
+
+cudaError_t mx_gemm_error_word(uint32_t** p) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_mx_gemm_err);
+}
+
+}  // namespace hsl

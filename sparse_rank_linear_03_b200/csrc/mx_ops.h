@@ -42,4 +42,15 @@ hsl_status mx_dequantize_run(const void* codes, const void* scales, int64_t rows
 hsl_status mx_simt_run(const MxOperand& A, const MxOperand& B, int64_t M, int64_t N, int64_t K,
                        const void* add, void* C, hsl_dtype cdt, cudaStream_t s);
 
+// Tensor-core products (mx_gemm.cu), bf16: X, dY, U, V on 16 bytes (mx_gemm_supported)
+bool mx_gemm_supported(const void* X);
+size_t mx_gemm_apply_workspace(bool trans, int64_t T, int64_t m, int64_t n);
+hsl_status mx_gemm_apply_run(bool trans, const MxOperand& D, int64_t m, int64_t n, const void* X,
+                             const void* add, void* Y, int64_t T, void* ws, cudaStream_t s);
+size_t mx_gemm_grad_workspace(int64_t T, int64_t m, int64_t n, int64_t r);
+hsl_status mx_gemm_grad_run(const MxOperand& X, int64_t T, int64_t n, const void* dY, int64_t m,
+                            const void* U, const void* V, int64_t r, const void* add, void* dU, void* dV,
+                            void* dX, void* ws, cudaStream_t s);
+cudaError_t mx_gemm_error_word(uint32_t** p);
+
 }  // namespace hsl

@@ -31,7 +31,7 @@ EXPORTS = (
     "hsl_concentration", "hsl_rcm_order", "hsl_permute", "hsl_set_permutation", "hsl_factor",
     "hsl_set_index_bits", "hsl_mx_pitch", "hsl_mx_workspace", "hsl_mx_quantize",
     "hsl_mx_dequantize", "hsl_mx4_apply", "hsl_mx4_apply_t", "hsl_mx4_matmul",
-    "hsl_mx8_factor_grad",
+    "hsl_mx8_factor_grad", "hsl_mx_check",
 )
 
 
@@ -85,6 +85,7 @@ def _load() -> ctypes.CDLL:
         "hsl_mx4_apply": [P, P, P, P, I64, I32, P, ctypes.c_size_t, P],
         "hsl_mx4_apply_t": [P, P, P, P, I64, I32, P, ctypes.c_size_t, P],
         "hsl_mx4_matmul": [P, P, P, P, I32, P, ctypes.c_size_t, P],
+        "hsl_mx_check": [P],
         "hsl_mx8_factor_grad": [P, P, I64, P, P, I32, P, P, P, P, I32, P, ctypes.c_size_t, P],
     }
     for name, args in sig.items():
@@ -537,3 +538,11 @@ def mx8_factor_grad(X: MX, dY: torch.Tensor, U: torch.Tensor, V: torch.Tensor, d
                                     dX.data_ptr() if dx else None, dt, ws.data_ptr() if wb else None,
                                     wb, s), "hsl_mx8_factor_grad")
     return (dU, dV, dX) if dx else (dU, dV)
+
+
+def mx_check(device=None, stream=None) -> None:
+    """Synchronise the stream and raise if a device wait of the microscaled operators gave up
+    on the device (hsl_mx_check)."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    with _On(dev, stream) as s:
+        _ok(lib.hsl_mx_check(s), "hsl_mx_check")
