@@ -182,6 +182,8 @@ hsl_status hsl_mx4_matmul(const hsl_mx* A, const hsl_mx* B, const void* add, voi
           ws, ws_bytes, workspace_bytes(HSL_MX_OP_MATMUL, A->rows, B->rows, A->cols, 0, dtype)))
     return e;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (mx_matmul_supported())
+    return mx_matmul_run(operand(A, false), A->rows, operand(B, false), B->rows, A->cols, add, Y, dtype, s);
   return mx_simt_run(operand(A, false), operand(B, false), A->rows, B->rows, A->cols, add, Y, dtype, s);
 }
 
@@ -224,8 +226,9 @@ hsl_status hsl_mx_check(hsl_stream stream) {
   set_message("");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cudaError_t e = cudaStreamSynchronize(s)) return cuda_fail(e, "stream synchronize");
-  uint32_t* words[] = {nullptr};
+  uint32_t* words[2] = {};
   if (cudaError_t e = mx_gemm_error_word(&words[0])) return cuda_fail(e, "error word address");
+  if (cudaError_t e = mx_matmul_error_word(&words[1])) return cuda_fail(e, "error word address");
   uint32_t all = 0;
   for (uint32_t* p : words) {
     uint32_t v = 0;

@@ -52,5 +52,10 @@ hsl_status mx_gemm_grad_run(const MxOperand& X, int64_t T, int64_t n, const void
                             const void* U, const void* V, int64_t r, const void* add, void* dU, void* dV,
                             void* dX, void* ws, cudaStream_t s);
 cudaError_t mx_gemm_error_word(uint32_t** p);
+// Both factors in e2m1 blocks (mx_matmul.cu): Y[T][m] = A Bᵀ (+ add)
+bool mx_matmul_supported();
+hsl_status mx_matmul_run(const MxOperand& A, int64_t T, const MxOperand& B, int64_t m, int64_t n,
+                         const void* add, void* Y, hsl_dtype dtype, cudaStream_t s);
+cudaError_t mx_matmul_error_word(uint32_t** p);
 
 }  // namespace hsl
