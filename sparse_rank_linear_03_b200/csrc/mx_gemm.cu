@@ -23,8 +23,8 @@
 //
 //   warp 0 lane 0   TMA of the B tile(s), and of A when it is bf16
 //   warp 1 lane 0   tcgen05.mma, M = 128 per accumulator, N up to 256, K = 16
-//   warps 2-9       widen A's blocks (codes of the next K-block already in
-//                   registers); then the epilogue: tcgen05.ld, add, round, store
+//   warps 2-17      widen A's blocks, two groups of eight taking turns at the K-blocks;
+//                   then the epilogue: tcgen05.ld, add, round, store
 //
 // MH = 2 gives the CTA two 128-row accumulators that share every B tile: a K-block
 // of 256 × 256 × 64 takes the MMAs about 1024 cycles, in which 32 KB of B and
@@ -47,9 +47,9 @@ namespace {
 __device__ uint32_t g_mx_gemm_err;
 
 constexpr int G_BK = 64;
-constexpr int G_THREADS = 320;
+constexpr int G_THREADS = 576;   // 18 warps: copies, MMA, 2 × 8 widening (all 16 in the epilogue)
 constexpr int G_MAX_STAGES = 8;
-constexpr int G_SMEM_BUDGET = 200 * 1024;  // stages; the barriers and alignment take under 2 KB more
+constexpr int G_SMEM_BUDGET = 222 * 1024;  // stages; the barriers and alignment take under 3 KB more
 
 enum AKind { A_BF16_K, A_BF16_M, A_E2M1_K, A_E2M1_M, A_INT8_K, A_INT8_M };
 enum OutKind { OUT_T, OUT_R, OUT_T_PART, OUT_R_PART };  // C[n][m] or C[m][n]; bf16 or fp32 partials
@@ -63,13 +63,13 @@ struct GemmMaps {
   CUtensorMap b0;  // B: box {64, BN} (K-major) or {64, 64}
   CUtensorMap b1;  // low part
   CUtensorMap c;   // OUT_T: box {128·MH, BN}
+  CUtensorMap q;   // codes: box {CodeTile::kInner bytes, CodeTile::kRows}
+  CUtensorMap qs;  // scales of [K][M] blocks: box {16 bytes, 64}
 };
 struct GemmArgs {
-  const uint8_t* codes;
-  const uint8_t* scales;
-  int64_t cpitch, spitch;
-  int nb;            // blocks per stored row of A
-  int arows;         // stored rows of A
+  const uint8_t* scales;  // [M][K] blocks: read 16 at a time per row
+  int64_t spitch;
+  int arows, nb;          // stored rows of A, blocks per row
   int M, N, nk;      // nk: K-blocks of 64
   int BN, stages, splits;
   int cstore;        // OUT_T: tiled store possible
@@ -79,10 +79,18 @@ struct GemmArgs {
 };
 
 __device__ __forceinline__ bool g_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (tc::mbar_try(bar, parity)) return true;
   if (*abort_flag) return false;
   if (tc::mbar_wait(bar, parity, &g_mx_gemm_err)) return true;
   *abort_flag = 1;
   return false;
+}
+
+// One lane of a converged warp, chosen so that the compiler knows the choice is uniform.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 // M- or N-major operand in the 128-byte swizzle: 64 values along the row, 8 k per
@@ -150,25 +158,34 @@ __device__ __forceinline__ uint2 widen_int8(uint32_t w, uint32_t scale) {
   return v;
 }
 
+// The code tile of a K-block in shared memory, as copied: kBoxes boxes of kRows rows of
+// kInner bytes in the swizzle of that width, so that the threads of a warp, a row
+// each, read their 16-byte chunks without bank conflicts.
+template <int AK, int MH>
+struct CodeTile {
+  static constexpr int kElem = a_is_int8(AK) ? 2 : 1;  // half-bytes per value
+  static constexpr int kRowBytes = (a_is_mmajor(AK) ? 128 * MH : 64) * kElem / 2;
+  static constexpr int kRows = a_is_mmajor(AK) ? 64 : 128 * MH;
+  static constexpr int kInner = kRowBytes < 128 ? kRowBytes : 128;
+  static constexpr int kBoxes = kRowBytes / kInner;
+  static constexpr int kCodes = kRows * kRowBytes;
+  static constexpr int kScales = a_is_mmajor(AK) ? 64 * 16 : 0;
+  static constexpr int kBytes = a_is_blocks(AK) ? kCodes + kScales : 0;
+  // address of 16-byte chunk c of row r
+  __device__ static __forceinline__ uint32_t at(int r, int c) {
+    constexpr int per = kInner / 16;
+    const int box = c / per, in = c % per;
+    const int x = kInner == 128 ? r & 7 : kInner == 64 ? (r >> 1) & 3 : (r >> 2) & 1;
+    return uint32_t(box * kRows * kInner + r * kInner + ((in ^ x) << 4));
+  }
+};
+
 // The codes and scale of one block of 32.
 template <bool kInt8>
 struct Block {
   uint4 c[kInt8 ? 2 : 1];
   uint32_t e;
 };
-template <bool kInt8>
-__device__ __forceinline__ void fetch(Block<kInt8>& b, const GemmArgs& g, int row, int blk) {
-  if (row < g.arows && blk < g.nb) {
-    const uint8_t* p = g.codes + int64_t(row) * g.cpitch + int64_t(blk) * (kInt8 ? 32 : 16);
-    b.c[0] = ld_stream16(p);
-    if (kInt8) b.c[1] = ld_stream16(p + 16);
-    b.e = __ldg(g.scales + int64_t(row) * g.spitch + blk);
-  } else {
-    b.c[0] = make_uint4(0, 0, 0, 0);
-    if (kInt8) b.c[1] = make_uint4(0, 0, 0, 0);
-    b.e = 0;
-  }
-}
 // Writes the block's 32 bf16 to chunks 4·half .. 4·half + 3 of tile row `row`.
 template <bool kInt8>
 __device__ __forceinline__ void widen(const Block<kInt8>& b, unsigned char* tile, int row, int half) {
@@ -199,7 +216,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t full[G_MAX_STAGES], empty[G_MAX_STAGES], accf;
+  __shared__ uint64_t full[G_MAX_STAGES], empty[G_MAX_STAGES], raw[G_MAX_STAGES], accf;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
 
@@ -212,7 +229,9 @@ __global__ void __launch_bounds__(G_THREADS, 1)
   constexpr int kA = MH * 128 * 128;  // bytes of the A tile
   const int bgroups = (g.BN + 63) / 64;
   const int kB = BMN ? bgroups * 8192 : g.BN * 128;
-  const int kStage = kA + TERMS * kB;
+  using Code = CodeTile<AK, MH>;
+  const int kRaw = kA + TERMS * kB;  // the code tile's place in a stage
+  const int kStage = kRaw + Code::kBytes;
   uint32_t cols = MH == 2 ? 64 : 32;  // whole 32-column reads past 2 × 16 columns stay inside
   while (cols < uint32_t(MH * g.BN)) cols *= 2;
 
@@ -221,6 +240,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     for (int s = 0; s < g.stages; ++s) {
       tc::mbar_init(&full[s], a_is_blocks(AK) ? 1 + 8 : 1);  // copies, and the eight widening warps
       tc::mbar_init(&empty[s], 1);
+      tc::mbar_init(&raw[s], 1);
     }
     tc::mbar_init(&accf, 1);
     tc::fence_mbar_init();
@@ -245,6 +265,15 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         unsigned char* a = smem + s * kStage;
         unsigned char* b = a + kA;
         const int k0 = (kb0 + kb) * G_BK;
+        if (a_is_blocks(AK)) {
+          unsigned char* q = a + kRaw;
+          tc::mbar_expect_tx(&raw[s], Code::kBytes);
+          const int qx = (a_is_mmajor(AK) ? i0 : k0) * Code::kElem / 2, qy = a_is_mmajor(AK) ? k0 : i0;
+#pragma unroll
+          for (int x = 0; x < Code::kBoxes; ++x)
+            tc::tma_load_2d(q + x * Code::kRows * Code::kInner, &maps.q, qx + x * Code::kInner, qy, &raw[s]);
+          if (a_is_mmajor(AK)) tc::tma_load_2d(q + Code::kCodes, &maps.qs, (i0 / 32) & ~15, k0, &raw[s]);
+        }
         tc::mbar_expect_tx(&full[s], (a_is_blocks(AK) ? 0 : kA) + TERMS * kB);
         if (AK == A_BF16_K) {
 #pragma unroll
@@ -274,12 +303,14 @@ __global__ void __launch_bounds__(G_THREADS, 1)
       // the copies in flight have landed before the CTA's shared memory is given up
       for (int q = 0; q < g.stages && q < issued; ++q) {
         const int last = (issued - 1 - q) / g.stages;  // uses of stage q before its last one
-        if (*abrt) tc::mbar_wait(&full[q], uint32_t(last) & 1, &g_mx_gemm_err);
+        if (!*abrt) continue;
+        if (a_is_blocks(AK)) tc::mbar_wait(&raw[q], uint32_t(last) & 1, &g_mx_gemm_err);
+        tc::mbar_wait(&full[q], uint32_t(last) & 1, &g_mx_gemm_err);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t idesc = tc::idesc_bf16(128, g.BN) | (a_is_mmajor(AK) ? 1u << 15 : 0u) |
                              (BMN ? 1u << 16 : 0u);
       int s = 0;
@@ -312,60 +343,86 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     }
     __syncwarp();
   } else {
-    const int tid = threadIdx.x - 64;
+    const int tid = (threadIdx.x - 64) & 255, group = (warp - 2) >> 3;
     if (a_is_blocks(AK)) {
       constexpr bool kInt8 = a_is_int8(AK);
       // MH = 2: tile row tid, both blocks; MH = 1: two threads share a tile row
       const int trow = MH == 2 ? tid : (tid & 127);
       const int half0 = MH == 2 ? 0 : (tid >> 7);
-      // stored row and block of this tile row at K-block kb
-      const int row0 = a_is_mmajor(AK) ? (trow & 63) : i0 + trow;
-      const int blk0 = (a_is_mmajor(AK) ? i0 / 32 + (trow >> 6) * 2 : 0) + half0;
-      Block<kInt8> cur[MH], nxt[MH];
-      auto get = [&](Block<kInt8>(&b)[MH], int kb) {
-        const int row = a_is_mmajor(AK) ? row0 + kb * G_BK : row0;
-        const int blk = a_is_mmajor(AK) ? blk0 : blk0 + kb * 2;
-#pragma unroll
-        for (int q = 0; q < MH; ++q) fetch(b[q], g, row, blk + q);
-      };
-      if (nk > 0) get(cur, kb0);
-      int s = 0;
-      uint32_t ph = 1;
-      for (int kb = 0; kb < nk; ++kb) {
-        if (kb + 1 < nk) get(nxt, kb0 + kb + 1);
-        if (!g_wait(&empty[s], ph, abrt)) break;
+      // The two groups of eight warps take the K-blocks in turn, so that one group's wait for
+      // its codes and its hand-over overlap the other's arithmetic.
+      // [M][K]: the row's scales, 16 blocks (8 K-blocks) at a time, one load ahead
+      const bool row_ok = i0 + trow < g.arows;
+      const uint4* srow = reinterpret_cast<const uint4*>(g.scales + int64_t(i0 + trow) * g.spitch);
+      const int sgroups = int(g.spitch / 16);
+      int sgrp = (kb0 + group) >> 3;
+      uint4 sc = make_uint4(0, 0, 0, 0), sn = sc;
+      if (!a_is_mmajor(AK) && row_ok) {
+        if (sgrp < sgroups) sc = __ldg(srow + sgrp);
+        if (sgrp + 1 < sgroups) sn = __ldg(srow + sgrp + 1);
+      }
+      int s = group;
+      uint32_t ph = 0;
+      for (int kb = group; kb < nk; kb += 2) {
         unsigned char* a = smem + s * kStage;
+        Block<kInt8> blk[MH];
+        if (!g_wait(&raw[s], ph, abrt)) break;  // (the stage's last MMAs are done: its copies waited)
+        const unsigned char* q = a + kRaw;
 #pragma unroll
-        for (int q = 0; q < MH; ++q) widen(cur[q], a, trow, half0 + q);
+        for (int b = 0; b < MH; ++b) {
+          const int r = a_is_mmajor(AK) ? (trow & 63) : trow;
+          const int n0 = (a_is_mmajor(AK) ? (trow >> 6) * 2 : 0) + half0 + b;  // block in the row
+          if (kInt8) {
+            blk[b].c[0] = *reinterpret_cast<const uint4*>(q + Code::at(r, 2 * n0));
+            blk[b].c[kInt8 ? 1 : 0] = *reinterpret_cast<const uint4*>(q + Code::at(r, 2 * n0 + 1));
+          } else {
+            blk[b].c[0] = *reinterpret_cast<const uint4*>(q + Code::at(r, n0));
+          }
+          if (a_is_mmajor(AK)) blk[b].e = q[Code::kCodes + r * 16 + ((i0 / 32) & 15) + n0];
+        }
+        if (!a_is_mmajor(AK)) {
+          const int kk = kb0 + kb;
+          if ((kk >> 3) != sgrp) {  // steps of 2: the next group of 8 K-blocks
+            sgrp = kk >> 3;
+            sc = sn;
+            if (row_ok && sgrp + 1 < sgroups) sn = __ldg(srow + sgrp + 1);
+          }
+          const uint32_t w = (kk & 4) ? ((kk & 2) ? sc.w : sc.z) : ((kk & 2) ? sc.y : sc.x);
+          const uint32_t pair = (kk & 1) ? w >> 16 : w;
+#pragma unroll
+          for (int b = 0; b < MH; ++b)  // padding bytes after the last block count as 0
+            blk[b].e = kk * 2 + half0 + b < g.nb ? (pair >> (8 * (half0 + b))) & 0xFFu : 0u;
+        }
+#pragma unroll
+        for (int b = 0; b < MH; ++b) widen(blk[b], a, trow, half0 + b);
         tc::fence_async_smem();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&full[s]);
-#pragma unroll
-        for (int q = 0; q < MH; ++q) cur[q] = nxt[q];
-        if (++s == g.stages) {
-          s = 0;
+        s += 2;
+        if (s >= g.stages) {
+          s -= g.stages;
           ph ^= 1;
         }
       }
     }
-    // epilogue: warp w reaches TMEM lanes 32 (w mod 4) onwards; with two
-    // accumulators warps 2-5 take the first, 6-9 the second; with one, 6-9 take
-    // the upper half of the columns
+    // epilogue: warp w reaches TMEM lanes 32 (w mod 4) onwards; the four groups of four
+    // warps divide the accumulators and their columns
     __syncwarp();
     const bool ok = tc::mbar_wait(&accf, 0, &g_mx_gemm_err) && !*abrt;
     __nv_bfloat16* stg = reinterpret_cast<__nv_bfloat16*>(smem);
     if (ok) {
       tc::tc_fence_after();
-      const int grp = warp >= 6 ? 1 : 0;
+      const int grp = (warp - 2) >> 2;
+      const int acc = MH == 2 ? grp & 1 : 0;
       const int L = ((warp & 3) << 5) | lane;
-      const int R = (MH == 2 ? grp * 128 : 0) + L;
+      const int R = acc * 128 + L;
       const int i = i0 + R;
-      const uint32_t tb =
-          tmem + (uint32_t((warp & 3) * 32) << 16) + (MH == 2 ? uint32_t(grp * g.BN) : 0u);
+      const uint32_t tb = tmem + (uint32_t((warp & 3) * 32) << 16) + uint32_t(acc * g.BN);
       // columns in steps of 32 (the last step may reach past BN, inside the allocation)
       const int steps = (g.BN + 31) / 32;
-      const int c_lo = MH == 2 ? 0 : (grp ? (steps + 1) / 2 : 0);
-      const int c_hi = MH == 2 ? steps : (grp ? steps : (steps + 1) / 2);
+      constexpr int kShare = 4 / MH;  // groups of four warps per accumulator
+      const int part = grp / MH;
+      const int c_lo = steps * part / kShare, c_hi = steps * (part + 1) / kShare;
 #pragma unroll 1
       for (int c = c_lo; c < c_hi; ++c) {
         const int c0 = c * 32;
@@ -440,11 +497,11 @@ __global__ void __launch_bounds__(G_THREADS, 1)
       *abrt = 1;
     }
     if (OUT == OUT_T && g.cstore) {
-      // the rounded tile [column][row] lies in the idle ring: one tiled store.  All eight
+      // the rounded tile [column][row] lies in the idle ring: one tiled store.  All sixteen
       // warps meet here, whether or not a wait gave up before.
       tc::fence_async_smem();
-      asm volatile("barrier.sync 1, 256;" ::: "memory");
-      if (tid == 0 && ok && !*abrt) {
+      asm volatile("barrier.sync 1, 512;" ::: "memory");
+      if (threadIdx.x == 64 && ok && !*abrt) {
         tc::tma_store_2d(&maps.c, stg, i0, j0);
         tc::bulk_commit();
         tc::bulk_wait_read_all();
@@ -503,30 +560,53 @@ struct GemmShape {
   int BN, MH, splits, stages;
 };
 
-int stage_bytes(bool bmn, int terms, int mh, int bn) {
-  return mh * 16384 + terms * (bmn ? (bn + 63) / 64 * 8192 : bn * 128);
+int code_bytes(int ak, int mh) {
+  if (!a_is_blocks(ak)) return 0;
+  return 128 * mh * (a_is_int8(ak) ? 64 : 32) + (a_is_mmajor(ak) ? 1024 : 0);
+}
+int stage_bytes(int ak, bool bmn, int terms, int mh, int bn) {
+  return mh * 16384 + terms * (bmn ? (bn + 63) / 64 * 8192 : bn * 128) + code_bytes(ak, mh);
 }
 
 // Tile and split of an M × N × K product.
-GemmShape shape_of(int64_t M, int64_t N, int64_t K, bool bmn, int terms, bool may_split) {
+GemmShape shape_of(int ak, int64_t M, int64_t N, int64_t K, bool bmn, int terms, bool may_split) {
   GemmShape s;
-  const int64_t ntn = (N + 255) / 256;
+  // With at least a tile per SM, 256-row tiles whose width makes the last round of
+  // CTAs as full as it can be: time goes as rounds × columns (a K-block of fewer than
+  // 160 columns costs the widening, not the MMAs).  2048 tokens × 11008 rows: 208
+  // columns (2.9 rounds) against 256 (2.3 rounds, the third mostly idle).
+  int64_t ntn = (N + 255) / 256;
+  const int64_t t2 = (M + 255) / 256;
+  s.MH = t2 * ntn >= 148 ? 2 : 1;
+  if (s.MH == 2) {
+    int64_t best = INT64_MAX, at = ntn;
+    for (int64_t c = ntn; c <= 2 * ntn; ++c) {
+      const int64_t bn = round_up((N + c - 1) / c, 16);
+      const int64_t cost = (t2 * c + 147) / 148 * std::max<int64_t>(bn, 160);
+      if (cost < best) {
+        best = cost;
+        at = c;
+      }
+    }
+    ntn = at;
+  }
   s.BN = int(round_up((N + ntn - 1) / ntn, 16));
-  const int64_t t2 = (M + 255) / 256 * ntn;
-  s.MH = t2 >= 148 ? 2 : 1;
-  const int64_t tiles = s.MH == 2 ? t2 : (M + 127) / 128 * ntn;
+  const int64_t tiles = s.MH == 2 ? t2 * ntn : (M + 127) / 128 * ntn;
   const int64_t nk = (K + 63) / 64;
   s.splits = 1;
   if (may_split && tiles < 148)
     s.splits = int(std::max<int64_t>(1, std::min<int64_t>(148 / tiles, nk / 4)));
-  s.stages = std::min(G_MAX_STAGES, G_SMEM_BUDGET / stage_bytes(bmn, terms, s.MH, s.BN));
+  // two stages at least: a pair of terms with an 8-bit factor leaves room for them only
+  // with one accumulator
+  if (s.MH == 2 && G_SMEM_BUDGET / stage_bytes(ak, bmn, terms, 2, s.BN) < 2) s.MH = 1;
+  s.stages = std::min(G_MAX_STAGES, G_SMEM_BUDGET / stage_bytes(ak, bmn, terms, s.MH, s.BN));
   return s;
 }
 
 template <int AK, bool BMN, int TERMS, int MH, int OUT>
 hsl_status launch_gemm(const GemmMaps& maps, const GemmArgs& g, cudaStream_t s) {
   void (*fn)(const GemmMaps, const GemmArgs) = k_mx_gemm<AK, BMN, TERMS, MH, OUT>;
-  int bytes = g.stages * stage_bytes(BMN, TERMS, MH, g.BN);
+  int bytes = g.stages * stage_bytes(AK, BMN, TERMS, MH, g.BN);
   if (OUT == OUT_T) bytes = std::max(bytes, MH * 128 * g.BN * 2);  // the epilogue's tile
   bytes += 1024;
   if (cudaError_t e = allow_dyn_smem(reinterpret_cast<const void*>(fn), bytes))
@@ -544,6 +624,19 @@ hsl_status launch_gemm(int mh, const GemmMaps& maps, const GemmArgs& g, cudaStre
 
 const auto kBF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
 const auto kSW = CU_TENSOR_MAP_SWIZZLE_128B;
+
+// The tensor maps of a factor in blocks (stored rows × cols).
+bool block_maps(GemmMaps* maps, int ak, int mh, const MxOperand& o, int64_t rows) {
+  const auto U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const int row_bytes = (a_is_mmajor(ak) ? 128 * mh : 64) / (a_is_int8(ak) ? 1 : 2);
+  const int inner = std::min(row_bytes, 128);
+  const auto sw = inner == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                  : inner == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                : CU_TENSOR_MAP_SWIZZLE_32B;
+  return make_tmap_2d(&maps->q, U8, 1, o.p, rows, o.pitch, o.pitch, inner, a_is_mmajor(ak) ? 64 : 128 * mh, sw) &&
+         (!a_is_mmajor(ak) || make_tmap_2d(&maps->qs, U8, 1, o.scales, rows, o.spitch, o.spitch, 16, 64,
+                                           CU_TENSOR_MAP_SWIZZLE_NONE));
+}
 
 hsl_status map_failed() {
   set_message("tensor map encoding failed");
@@ -564,7 +657,7 @@ hsl_status pad_rows(const void* src, int64_t rows, int64_t n, int64_t pitch, voi
 // ---- Y = X Dᵀ and dX = dY D -----------------------------------------------------
 size_t mx_gemm_apply_workspace(bool trans, int64_t T, int64_t m, int64_t n) {
   const int64_t M = trans ? n : m, K = trans ? m : n;
-  const GemmShape sh = shape_of(M, T, K, false, 1, true);
+  const GemmShape sh = shape_of(trans ? A_E2M1_M : A_E2M1_K, M, T, K, false, 1, true);
   size_t b = 0;
   if (K % 8) b += up16(T * round_up(K, 8) * 2);
   if (sh.splits > 1) b += up16(int64_t(sh.splits) * T * M * 4);
@@ -578,7 +671,7 @@ bool mx_gemm_supported(const void* X) {
 hsl_status mx_gemm_apply_run(bool trans, const MxOperand& D, int64_t m, int64_t n, const void* X,
                              const void* add, void* Y, int64_t T, void* ws, cudaStream_t s) {
   const int64_t M = trans ? n : m, K = trans ? m : n;
-  const GemmShape sh = shape_of(M, T, K, false, 1, true);
+  const GemmShape sh = shape_of(trans ? A_E2M1_M : A_E2M1_K, M, T, K, false, 1, true);
   unsigned char* w = static_cast<unsigned char*>(ws);
   int64_t kp = K;
   if (K % 8) {
@@ -590,12 +683,10 @@ hsl_status mx_gemm_apply_run(bool trans, const MxOperand& D, int64_t m, int64_t 
   GemmMaps maps;
   memset(&maps, 0, sizeof(maps));
   GemmArgs g = {};
-  g.codes = static_cast<const uint8_t*>(D.p);
   g.scales = D.scales;
-  g.cpitch = D.pitch;
   g.spitch = D.spitch;
-  g.nb = int(mx::blocks(n));
   g.arows = int(m);
+  g.nb = int(mx::blocks(n));
   g.M = int(M);
   g.N = int(T);
   g.nk = int((K + G_BK - 1) / G_BK);
@@ -605,7 +696,9 @@ hsl_status mx_gemm_apply_run(bool trans, const MxOperand& D, int64_t m, int64_t 
   g.add = static_cast<const __nv_bfloat16*>(add);
   g.C = static_cast<__nv_bfloat16*>(Y);
   g.part = reinterpret_cast<float*>(w);
-  if (!make_tmap_2d(&maps.b0, kBF, 2, X, T, K, kp, 64, sh.BN, kSW)) return map_failed();
+  if (!make_tmap_2d(&maps.b0, kBF, 2, X, T, K, kp, 64, sh.BN, kSW) ||
+      !block_maps(&maps, trans ? A_E2M1_M : A_E2M1_K, sh.MH, D, m))
+    return map_failed();
   if (sh.splits > 1) {
     if (hsl_status e = trans ? launch_gemm<A_E2M1_M, false, 1, OUT_T_PART>(sh.MH, maps, g, s)
                              : launch_gemm<A_E2M1_K, false, 1, OUT_T_PART>(sh.MH, maps, g, s))
@@ -633,11 +726,11 @@ GradPlan grad_plan(int64_t T, int64_t m, int64_t n, int64_t r) {
   GradPlan p;
   p.rp = round_up(r, 8);
   p.mp = round_up(m, 8);
-  p.z = shape_of(T, r, n, true, 1, true);
-  p.g = shape_of(T, r, m, true, 1, true);
-  p.u = shape_of(m, r, T, true, 2, true);
-  p.v = shape_of(n, r, T, true, 2, true);
-  p.x = shape_of(n, T, r, false, 2, false);
+  p.z = shape_of(A_INT8_K, T, r, n, true, 1, true);
+  p.g = shape_of(A_BF16_K, T, r, m, true, 1, true);
+  p.u = shape_of(A_BF16_M, m, r, T, true, 2, true);
+  p.v = shape_of(A_INT8_M, n, r, T, true, 2, true);
+  p.x = shape_of(A_BF16_K, n, T, r, false, 2, false);
   size_t o = 0;
   auto take = [&](int64_t bytes) {
     const size_t at = o;
@@ -686,12 +779,10 @@ hsl_status mx_gemm_grad_run(const MxOperand& X, int64_t T, int64_t n, const void
   float* part = reinterpret_cast<float*>(w + p.off_part);
 
   GemmArgs base = {};
-  base.codes = static_cast<const uint8_t*>(X.p);
   base.scales = X.scales;
-  base.cpitch = X.pitch;
   base.spitch = X.spitch;
-  base.nb = int(mx::blocks(n));
   base.arows = int(T);
+  base.nb = int(mx::blocks(n));
   base.part = part;
   auto args = [&](const GemmShape& sh, int64_t M, int64_t N, int64_t K) {
     GemmArgs g = base;
@@ -720,7 +811,9 @@ hsl_status mx_gemm_grad_run(const MxOperand& X, int64_t T, int64_t n, const void
   }
   {  // Z = X V
     GemmArgs g = args(p.z, T, r, n);
-    if (!make_tmap_2d(&maps.b0, kBF, 2, V, n, r, p.rp, 64, 64, kSW)) return map_failed();
+    if (!make_tmap_2d(&maps.b0, kBF, 2, V, n, r, p.rp, 64, 64, kSW) ||
+        !block_maps(&maps, A_INT8_K, p.z.MH, X, T))
+      return map_failed();
     if (hsl_status e = launch_gemm<A_INT8_K, true, 1, OUT_R_PART>(p.z.MH, maps, g, s)) return e;
     if (hsl_status e = pair(p.z, zh, zl)) return e;
   }
@@ -730,7 +823,9 @@ hsl_status mx_gemm_grad_run(const MxOperand& X, int64_t T, int64_t n, const void
     if (!make_tmap_2d(&maps.b0, kBF, 2, hi, T, r, p.rp, 64, 64, kSW) ||
         !make_tmap_2d(&maps.b1, kBF, 2, lo, T, r, p.rp, 64, 64, kSW))
       return map_failed();
-    if (of_u && !make_tmap_2d(&maps.a, kBF, 2, dY, T, m, p.mp, 64, 64, kSW)) return map_failed();
+    if (of_u ? !make_tmap_2d(&maps.a, kBF, 2, dY, T, m, p.mp, 64, 64, kSW)
+             : !block_maps(&maps, A_INT8_M, sh.MH, X, T))
+      return map_failed();
     g.C = static_cast<__nv_bfloat16*>(out);
     g.cstore = (r % 8 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0) ? 1 : 0;
     if (sh.splits == 1)
