@@ -23,6 +23,7 @@
 //
 //   warp 0 lane 0   TMA of the B tile(s), and of A when it is bf16
 //   warp 1 lane 0   tcgen05.mma, M = 128 per accumulator, N up to 256, K = 16
+//   warp 18 lane 0  TMA of the code tiles, into a ring of their own
 //   warps 2-17      widen A's blocks, two groups of eight taking turns at the K-blocks;
 //                   then the epilogue: tcgen05.ld, add, round, store
 //
@@ -47,7 +48,7 @@ namespace {
 __device__ uint32_t g_mx_gemm_err;
 
 constexpr int G_BK = 64;
-constexpr int G_THREADS = 576;   // 18 warps: copies, MMA, 2 × 8 widening (all 16 in the epilogue)
+constexpr int G_THREADS = 608;   // 19 warps: copies, MMA, 2 × 8 widening (all 16 in the epilogue), code copies
 constexpr int G_MAX_STAGES = 8;
 constexpr int G_SMEM_BUDGET = 222 * 1024;  // stages; the barriers and alignment take under 3 KB more
 
@@ -72,6 +73,7 @@ struct GemmArgs {
   int arows, nb;          // stored rows of A, blocks per row
   int M, N, nk;      // nk: K-blocks of 64
   int BN, stages, splits;
+  int codes;         // code tiles in flight
   int cstore;        // OUT_T: tiled store possible
   const __nv_bfloat16* add;
   __nv_bfloat16* C;
@@ -216,7 +218,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t full[G_MAX_STAGES], empty[G_MAX_STAGES], raw[G_MAX_STAGES], accf;
+  __shared__ uint64_t full[G_MAX_STAGES], empty[G_MAX_STAGES], accf;
+  __shared__ uint64_t raw[G_MAX_STAGES], taken[G_MAX_STAGES];  // code tile landed, read
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
 
@@ -230,8 +233,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
   const int bgroups = (g.BN + 63) / 64;
   const int kB = BMN ? bgroups * 8192 : g.BN * 128;
   using Code = CodeTile<AK, MH>;
-  const int kRaw = kA + TERMS * kB;  // the code tile's place in a stage
-  const int kStage = kRaw + Code::kBytes;
+  const int kStage = kA + TERMS * kB;
+  unsigned char* cring = smem + g.stages * kStage;
   uint32_t cols = MH == 2 ? 64 : 32;  // whole 32-column reads past 2 × 16 columns stay inside
   while (cols < uint32_t(MH * g.BN)) cols *= 2;
 
@@ -240,7 +243,10 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     for (int s = 0; s < g.stages; ++s) {
       tc::mbar_init(&full[s], a_is_blocks(AK) ? 1 + 8 : 1);  // copies, and the eight widening warps
       tc::mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < g.codes; ++s) {
       tc::mbar_init(&raw[s], 1);
+      tc::mbar_init(&taken[s], 8);
     }
     tc::mbar_init(&accf, 1);
     tc::fence_mbar_init();
@@ -265,15 +271,6 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         unsigned char* a = smem + s * kStage;
         unsigned char* b = a + kA;
         const int k0 = (kb0 + kb) * G_BK;
-        if (a_is_blocks(AK)) {
-          unsigned char* q = a + kRaw;
-          tc::mbar_expect_tx(&raw[s], Code::kBytes);
-          const int qx = (a_is_mmajor(AK) ? i0 : k0) * Code::kElem / 2, qy = a_is_mmajor(AK) ? k0 : i0;
-#pragma unroll
-          for (int x = 0; x < Code::kBoxes; ++x)
-            tc::tma_load_2d(q + x * Code::kRows * Code::kInner, &maps.q, qx + x * Code::kInner, qy, &raw[s]);
-          if (a_is_mmajor(AK)) tc::tma_load_2d(q + Code::kCodes, &maps.qs, (i0 / 32) & ~15, k0, &raw[s]);
-        }
         tc::mbar_expect_tx(&full[s], (a_is_blocks(AK) ? 0 : kA) + TERMS * kB);
         if (AK == A_BF16_K) {
 #pragma unroll
@@ -303,10 +300,32 @@ __global__ void __launch_bounds__(G_THREADS, 1)
       // the copies in flight have landed before the CTA's shared memory is given up
       for (int q = 0; q < g.stages && q < issued; ++q) {
         const int last = (issued - 1 - q) / g.stages;  // uses of stage q before its last one
-        if (!*abrt) continue;
-        if (a_is_blocks(AK)) tc::mbar_wait(&raw[q], uint32_t(last) & 1, &g_mx_gemm_err);
-        tc::mbar_wait(&full[q], uint32_t(last) & 1, &g_mx_gemm_err);
+        if (*abrt) tc::mbar_wait(&full[q], uint32_t(last) & 1, &g_mx_gemm_err);
       }
+    }
+    __syncwarp();
+  } else if (warp == 18) {
+    if (lane == 0 && a_is_blocks(AK)) {
+      int s = 0, issued = 0;
+      uint32_t ph = 1;
+      for (int kb = 0; kb < nk; ++kb) {
+        if (!g_wait(&taken[s], ph, abrt)) break;
+        unsigned char* q = cring + s * Code::kBytes;
+        const int k0 = (kb0 + kb) * G_BK;
+        const int qx = (a_is_mmajor(AK) ? i0 : k0) * Code::kElem / 2, qy = a_is_mmajor(AK) ? k0 : i0;
+        tc::mbar_expect_tx(&raw[s], Code::kBytes);
+#pragma unroll
+        for (int x = 0; x < Code::kBoxes; ++x)
+          tc::tma_load_2d(q + x * Code::kRows * Code::kInner, &maps.q, qx + x * Code::kInner, qy, &raw[s]);
+        if (a_is_mmajor(AK)) tc::tma_load_2d(q + Code::kCodes, &maps.qs, (i0 / 32) & ~15, k0, &raw[s]);
+        ++issued;
+        if (++s == g.codes) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+      for (int q = 0; q < g.codes && q < issued; ++q)
+        if (*abrt) tc::mbar_wait(&raw[q], uint32_t((issued - 1 - q) / g.codes) & 1, &g_mx_gemm_err);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -361,13 +380,13 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         if (sgrp < sgroups) sc = __ldg(srow + sgrp);
         if (sgrp + 1 < sgroups) sn = __ldg(srow + sgrp + 1);
       }
-      int s = group;
-      uint32_t ph = 0;
+      int s = group, cs = group;
+      uint32_t ph = 1, cph = 0;
       for (int kb = group; kb < nk; kb += 2) {
         unsigned char* a = smem + s * kStage;
         Block<kInt8> blk[MH];
-        if (!g_wait(&raw[s], ph, abrt)) break;  // (the stage's last MMAs are done: its copies waited)
-        const unsigned char* q = a + kRaw;
+        if (!g_wait(&raw[cs], cph, abrt)) break;
+        const unsigned char* q = cring + cs * Code::kBytes;
 #pragma unroll
         for (int b = 0; b < MH; ++b) {
           const int r = a_is_mmajor(AK) ? (trow & 63) : trow;
@@ -393,6 +412,14 @@ __global__ void __launch_bounds__(G_THREADS, 1)
           for (int b = 0; b < MH; ++b)  // padding bytes after the last block count as 0
             blk[b].e = kk * 2 + half0 + b < g.nb ? (pair >> (8 * (half0 + b))) & 0xFFu : 0u;
         }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&taken[cs]);
+        cs += 2;
+        if (cs >= g.codes) {
+          cs -= g.codes;
+          cph ^= 1;
+        }
+        if (!g_wait(&empty[s], ph, abrt)) break;
 #pragma unroll
         for (int b = 0; b < MH; ++b) widen(blk[b], a, trow, half0 + b);
         tc::fence_async_smem();
@@ -557,15 +584,15 @@ unsigned blocks_of(int64_t count) { return unsigned((count + 255) / 256); }
 
 // ---- host ---------------------------------------------------------------------
 struct GemmShape {
-  int BN, MH, splits, stages;
+  int BN, MH, splits, stages, codes;
 };
 
 int code_bytes(int ak, int mh) {
   if (!a_is_blocks(ak)) return 0;
   return 128 * mh * (a_is_int8(ak) ? 64 : 32) + (a_is_mmajor(ak) ? 1024 : 0);
 }
-int stage_bytes(int ak, bool bmn, int terms, int mh, int bn) {
-  return mh * 16384 + terms * (bmn ? (bn + 63) / 64 * 8192 : bn * 128) + code_bytes(ak, mh);
+int stage_bytes(bool bmn, int terms, int mh, int bn) {
+  return mh * 16384 + terms * (bmn ? (bn + 63) / 64 * 8192 : bn * 128);
 }
 
 // Tile and split of an M × N × K product.
@@ -596,17 +623,25 @@ GemmShape shape_of(int ak, int64_t M, int64_t N, int64_t K, bool bmn, int terms,
   s.splits = 1;
   if (may_split && tiles < 148)
     s.splits = int(std::max<int64_t>(1, std::min<int64_t>(148 / tiles, nk / 4)));
-  // two stages at least: a pair of terms with an 8-bit factor leaves room for them only
-  // with one accumulator
-  if (s.MH == 2 && G_SMEM_BUDGET / stage_bytes(ak, bmn, terms, 2, s.BN) < 2) s.MH = 1;
-  s.stages = std::min(G_MAX_STAGES, G_SMEM_BUDGET / stage_bytes(ak, bmn, terms, s.MH, s.BN));
+  // Code tiles are small and come from farther away than anything else: four of them in
+  // flight at least, then as many stages as fit (two at least: a pair of terms with an
+  // 8-bit factor leaves room for them only with one accumulator), then more code tiles.
+  auto fit = [&](int mh) {
+    const int code = code_bytes(ak, mh), stage = stage_bytes(bmn, terms, mh, s.BN);
+    s.codes = code ? 4 : 0;
+    if (G_SMEM_BUDGET - s.codes * code < 3 * stage) s.codes = code ? 3 : 0;
+    s.stages = std::min(G_MAX_STAGES, (G_SMEM_BUDGET - s.codes * code) / stage);
+    if (code) s.codes = std::min(G_MAX_STAGES, (G_SMEM_BUDGET - s.stages * stage) / code);
+  };
+  fit(s.MH);
+  if (s.MH == 2 && s.stages < 2) fit(s.MH = 1);
   return s;
 }
 
 template <int AK, bool BMN, int TERMS, int MH, int OUT>
 hsl_status launch_gemm(const GemmMaps& maps, const GemmArgs& g, cudaStream_t s) {
   void (*fn)(const GemmMaps, const GemmArgs) = k_mx_gemm<AK, BMN, TERMS, MH, OUT>;
-  int bytes = g.stages * stage_bytes(AK, BMN, TERMS, MH, g.BN);
+  int bytes = g.stages * stage_bytes(BMN, TERMS, MH, g.BN) + g.codes * code_bytes(AK, MH);
   if (OUT == OUT_T) bytes = std::max(bytes, MH * 128 * g.BN * 2);  // the epilogue's tile
   bytes += 1024;
   if (cudaError_t e = allow_dyn_smem(reinterpret_cast<const void*>(fn), bytes))
@@ -692,6 +727,7 @@ hsl_status mx_gemm_apply_run(bool trans, const MxOperand& D, int64_t m, int64_t 
   g.nk = int((K + G_BK - 1) / G_BK);
   g.BN = sh.BN;
   g.stages = sh.stages;
+  g.codes = sh.codes;
   g.splits = sh.splits;
   g.add = static_cast<const __nv_bfloat16*>(add);
   g.C = static_cast<__nv_bfloat16*>(Y);
@@ -791,6 +827,8 @@ hsl_status mx_gemm_grad_run(const MxOperand& X, int64_t T, int64_t n, const void
     g.nk = int((K + G_BK - 1) / G_BK);
     g.BN = sh.BN;
     g.stages = sh.stages;
+    g.codes = sh.codes;
+  g.codes = sh.codes;
     g.splits = sh.splits;
     return g;
   };
