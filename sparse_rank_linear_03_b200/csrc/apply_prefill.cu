@@ -986,6 +986,18 @@ bool make_tmap_kblocks(CUtensorMap* map, const void* base, int64_t rows, int64_t
             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+bool make_tmap_3d_bytes(CUtensorMap* map, const void* base, const int64_t (&dims)[3], int64_t stride1,
+                        int64_t stride2, const int (&box)[3], CUtensorMapSwizzle sw) {
+  const EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t d[3] = {cuuint64_t(dims[0]), cuuint64_t(dims[1]), cuuint64_t(dims[2])};
+  cuuint64_t st[2] = {cuuint64_t(stride1), cuuint64_t(stride2)};
+  cuuint32_t b[3] = {cuuint32_t(box[0]), cuuint32_t(box[1]), cuuint32_t(box[2])};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), d, st, b, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 bool tmap_available() { return encode_fn() != nullptr; }
 
 // Z workspace and Vt come from the handle (Vt built when the factors are packed).

@@ -176,6 +176,10 @@ bool make_tmap_2d(CUtensorMap* map, CUtensorMapDataType dt, int esize, const voi
 // contiguous (128-byte swizzle), in one copy (apply_prefill.cu).
 bool make_tmap_kblocks(CUtensorMap* map, const void* base, int64_t rows, int64_t cols,
                        int box_rows, int box_kblocks);
+// 3-D map of bytes: dims {inner, d1, d2} with byte strides of the outer two, box
+// likewise (apply_prefill.cu).
+bool make_tmap_3d_bytes(CUtensorMap* map, const void* base, const int64_t (&dims)[3], int64_t stride1,
+                        int64_t stride2, const int (&box)[3], CUtensorMapSwizzle sw);
 bool tmap_available();
 
 }  // namespace hsl

@@ -68,6 +68,7 @@ size_t workspace_bytes(hsl_mx_op op, int64_t T, int64_t m, int64_t n, int64_t r,
   const size_t simt = op == HSL_MX_OP_FACTOR_GRAD ? size_t(2 * T * r * 4) : 0;
   if (dt == HSL_F32 || T == 0 || m == 0) return simt;
   size_t tc = 0;
+  if (op == HSL_MX_OP_APPLY && mx_decode_fits(T, m, n)) return 0;
   if (op == HSL_MX_OP_APPLY || op == HSL_MX_OP_APPLY_T)
     tc = mx_gemm_apply_workspace(op == HSL_MX_OP_APPLY_T, T, m, n);
   if (op == HSL_MX_OP_FACTOR_GRAD && r > 0) tc = mx_gemm_grad_workspace(T, m, n, r);
@@ -145,8 +146,12 @@ hsl_status hsl_mx4_apply(const hsl_mx* D, const void* X, const void* add, void* 
                                      workspace_bytes(HSL_MX_OP_APPLY, batch, D->rows, D->cols, 0, dtype)))
     return e;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dtype == HSL_BF16 && mx_decode_fits(batch, D->rows, D->cols))
+    return mx_decode_run(operand(D, false), D->rows, D->cols, X, add, Y, batch, s);
   if (dtype == HSL_BF16 && mx_gemm_supported(X))
     return mx_gemm_apply_run(false, operand(D, false), D->rows, D->cols, X, add, Y, batch, ws, s);
+  if (dtype == HSL_F32 && batch <= kMxDecodeF32Max)
+    return mx_decode_f32_run(operand(D, false), D->rows, D->cols, X, add, Y, batch, s);
   return mx_simt_run(operand(X, dtype, D->cols, false), operand(D, false), batch, D->rows, D->cols,
                      add, Y, dtype, s);
 }
@@ -226,9 +231,10 @@ hsl_status hsl_mx_check(hsl_stream stream) {
   set_message("");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cudaError_t e = cudaStreamSynchronize(s)) return cuda_fail(e, "stream synchronize");
-  uint32_t* words[2] = {};
+  uint32_t* words[3] = {};
   if (cudaError_t e = mx_gemm_error_word(&words[0])) return cuda_fail(e, "error word address");
   if (cudaError_t e = mx_matmul_error_word(&words[1])) return cuda_fail(e, "error word address");
+  if (cudaError_t e = mx_decode_error_word(&words[2])) return cuda_fail(e, "error word address");
   uint32_t all = 0;
   for (uint32_t* p : words) {
     uint32_t v = 0;

@@ -1,0 +1,578 @@
+// Y = X Dᵀ (+ add) for a few tokens, D in e2m1 blocks: one pass over the codes.
+//
+// bf16 (k_mx_decode): bound by the bytes of D, 17 per 32 values.  At 6.5 TB/s that is
+// 44 values per SM and cycle, so a value may cost 2.9 instructions, of which 1.45 on the
+// integer pipe (64 lanes per cycle).  Byte permutes that build bf16 values take 2.8
+// integer instructions per value (28672 × 8192, one token: 60 µs).  What this kernel
+// does takes about half an integer instruction:
+//
+//   cvt turns two codes into two fp16 values, which mma.sync (m16n8k16, fp32 sums)
+//   multiplies with the tokens, 16 rows of D × 8 columns.  Each block has its own
+//   MMAs, and its scale multiplies their 4 sums per lane (fp32 FMA).
+//
+//   The tokens become fp16 without losing a bit: a token's values are sorted into
+//   windows of 32 binades below its largest, and each window, scaled by its own
+//   power of two, is a column of its own (8 significant bits over 32 binades end at
+//   2^−23, fp16 reaches 2^−24).  Activations fit one window nearly always; there is room
+//   for two columns per token up to 4 tokens, and what does not fit takes
+//   another pass over D.  At the end each column is scaled back.  Infinities
+//   and NaN go to the first window as they are.  Block scales enter as 2^(e − 142), so
+//   that a column's sums lie as if its largest value were about 1.
+//
+//   One CTA per SM keeps the columns in shared memory and walks over tiles of 16 rows.
+//   Codes and scales come in tiled copies, one of each per stage, a ring of stages ahead of
+//   the arithmetic: at 1.5 to 2 µs of latency 65 to 90 KB per SM have to be in flight.
+//   Sixteen warps divide a stage in units of 256 values of K.  Lane (g, t) takes word t
+//   (8 codes) of each block of rows g and g + 8, and the same 8 values of column g:
+//   the order of the terms of a dot product is free.  The warps' sums are added
+//   up in warp order, several row tiles at a time.  Where the columns do not fit, K is taken in slices; the rows'
+//   sums stay in shared memory from slice to slice and pass to pass.
+//
+// f32 (k_mx_decode_f32): a lane per row, tokens broadcast from shared memory, fp32 FMA.
+#include <cuda.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "common.cuh"
+#include "internal.h"
+#include "mx.cuh"
+#include "mx_ops.h"
+#include "tc.cuh"
+
+namespace hsl {
+namespace {
+
+constexpr int DC_WARPS = 16;
+constexpr int DC_UNIT = 256;                 // values of K per warp and step
+constexpr int DC_SMEM_MAX = 224 * 1024;
+
+// Eight codes (one word) → four fp16 pairs.
+__device__ __forceinline__ void widen_word(uint32_t w, uint32_t (&v)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+      : "r"(w));
+}
+// 2^(e − 142) for any scale byte: fp32 subnormals below e = 16; 255 stands for NaN.
+__device__ __forceinline__ float any_scale(uint32_t e) {
+  return __uint_as_float(e == 255u ? 0x7FC00000u : e >= 16u ? (e - 15u) << 23 : 1u << (e + 7u));
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+struct DcMaps {
+  CUtensorMap c3;  // codes as [unit][row][128 bytes]: box {128, 16·tps, su}
+  CUtensorMap c2;  // codes as [row][bytes]: box {128, 16·tps} (stages with the row's ragged end)
+  CUtensorMap s;   // scales: box {128, 16·tps}
+};
+struct DcArgs {
+  const __nv_bfloat16* X;
+  const __nv_bfloat16* add;
+  __nv_bfloat16* Y;
+  int m, n, nb, T;
+  int vec;     // rows of X start on 16 bytes
+  int wcols;   // columns per token, at most
+  int slice;   // units of K whose columns are in shared memory at a time
+  int su;      // units per stage and row tile
+  int tps;     // row tiles per stage
+  int stages;
+  int ysum, ring;  // offsets in shared memory: the kept sums, the stages
+};
+
+// A stage: su units of codes, each `rows` rows of 128 bytes, then 128 scale bytes per row
+// (two units in 16 bytes), all in the 128-byte swizzle: 16-byte chunk c of row r lies at
+// chunk c ^ (r & 7), so that the eight rows of a warp's access lie in different banks.
+__host__ __device__ constexpr int dc_stage_bytes(int su, int rows) { return (su + 1) * rows * 128; }
+
+// 16-byte piece c (eight values) of a column in shared memory: the eight lanes of an access
+// (two columns × four neighbouring pieces) meet eight different bank groups.
+__device__ __forceinline__ int xs_at(int col, int c, int pieces) { return col * pieces + (c ^ ((col & 1) << 2)); }
+
+__device__ __forceinline__ uint4 load_piece(const DcArgs& a, int tok, int col) {
+  uint4 v = make_uint4(0, 0, 0, 0);
+  const __nv_bfloat16* p = a.X + int64_t(tok) * a.n + col;
+  if (a.vec && col + 8 <= a.n) {
+    v = __ldg(reinterpret_cast<const uint4*>(p));
+  } else {
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (col + j < a.n)
+        w[j >> 1] |= uint32_t(__ldg(reinterpret_cast<const uint16_t*>(p) + j)) << ((j & 1) * 16);
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return v;
+}
+// The values of a piece that belong to window `win` of a token whose largest exponent field is
+// `top`, scaled by 2^(142 − top + 32 win) to fp16; zeros elsewhere.
+__device__ __forceinline__ uint4 window_piece(const uint4& v, int top, int win) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const int k = 142 - top + 32 * win;  // in two factors: 2^k alone may not be an fp32 value
+  const float f0 = __uint_as_float(uint32_t(127 + k / 2) << 23);
+  const float f1 = __uint_as_float(uint32_t(127 + k - k / 2) << 23);
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float x[2] = {bf_lo(w[j]), bf_hi(w[j])};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int b = int((w[j] >> (h * 16 + 7)) & 0xFFu);
+      const int at = b == 255 ? 0 : (top - b) >> 5;
+      x[h] = at == win ? x[h] * f0 * f1 : 0.f;
+    }
+    const __half2 p = __floats2half2_rn(x[0], x[1]);
+    o[j] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+__device__ uint32_t g_mx_decode_err;
+
+constexpr int DC_MAX_STAGES = 8;
+constexpr int DC_THREADS = (DC_WARPS + 1) * 32;
+// Room for the warps' sums: of two row tiles with 8 columns, of more with fewer columns.
+constexpr int DC_RED = 2 * DC_WARPS * 16 * 8 * 4;
+
+__device__ __forceinline__ void dc_sync() { asm volatile("barrier.sync 1, 512;" ::: "memory"); }  // the 16 warps
+
+__global__ void __launch_bounds__(DC_THREADS, 1)
+    k_mx_decode(const __grid_constant__ DcMaps maps, const DcArgs a) {
+  constexpr int kRows = 16;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t full[DC_MAX_STAGES], empty[DC_MAX_STAGES];
+  __shared__ int abort_flag, emax[8], emin[8];
+  float* red = reinterpret_cast<float*>(smem);  // [slot][DC_WARPS][kRows][columns]
+  const int pieces = a.slice * (DC_UNIT / 8);
+  uint4* xs = reinterpret_cast<uint4*>(smem + DC_RED);
+  unsigned char* ring = smem + a.ring;
+  float* ysum = reinterpret_cast<float*>(smem + a.ysum);  // [row tile of this CTA][token][kRows]
+  const int srows = a.tps * kRows;
+  const int sbytes = dc_stage_bytes(a.su, srows);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int units = (a.nb + 7) / 8, tiles = (a.m + kRows - 1) / kRows;
+  const int groups = (tiles + a.tps - 1) / a.tps;  // row tiles are taken tps at a time
+  volatile int* abrt = &abort_flag;
+
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int i = 0; i < a.stages; ++i) {
+      tc::mbar_init(&full[i], 1);
+      tc::mbar_init(&empty[i], DC_WARPS);
+    }
+    tc::fence_mbar_init();
+  }
+  __syncthreads();
+
+  if (warp == DC_WARPS) {
+    const uint64_t policy = tc::make_policy_evict_first();
+    const int whole = a.nb / 8;  // units that a row has in full
+    int s = 0, issued = 0;
+    uint32_t ph = 1;
+    for (int u0 = 0; u0 < units; u0 += a.slice) {
+      const int uend = min(u0 + a.slice, units);
+      int passes = 1;
+      bool told = false;
+      for (int pass = 0; pass < passes; ++pass) {
+        int step = 0;
+        for (int grp = blockIdx.x; grp < groups; grp += gridDim.x) {
+          const int row0 = grp * srows;
+          for (int u = u0; u < uend; u += a.su, ++step) {
+            if (!told && step == a.stages) {  // as far as the ring goes without knowing the passes
+              told = true;
+              __syncthreads();
+            }
+            if (lane == 0) {
+              if (!tc::mbar_try(&empty[s], ph) && (*abrt || !tc::mbar_wait(&empty[s], ph, &g_mx_decode_err)))
+                *abrt = 1;
+              // after a wait that gave up nothing more is copied, but the barriers are still met
+              if (!*abrt) {
+                unsigned char* c = ring + s * sbytes;
+                const bool ragged = u + a.su > whole && whole < units;
+                const int nu = ragged ? min(a.su, units - u) : a.su;
+                tc::mbar_expect_tx(&full[s], uint32_t((nu + 1) * srows * 128));
+                if (!ragged) {
+                  tc::tma_load_3d_hint(c, &maps.c3, 0, row0, u, &full[s], policy);
+                } else {
+                  for (int q = 0; q < nu; ++q)
+                    tc::tma_load_2d_hint(c + q * srows * 128, &maps.c2, (u + q) * 128, row0, &full[s], policy);
+                }
+                tc::tma_load_2d_hint(c + a.su * srows * 128, &maps.s, u * 8, row0, &full[s], policy);
+                ++issued;
+              }
+            }
+            __syncwarp();
+            if (++s == a.stages) {
+              s = 0;
+              ph ^= 1;
+            }
+          }
+        }
+        if (!told) {
+          told = true;
+          __syncthreads();
+        }
+        if (pass == 0)
+          for (int t = 0; t < a.T; ++t) passes = max(passes, ((emax[t] - emin[t]) / 32 + a.wcols) / a.wcols);
+      }
+      __syncthreads();  // (the exponents may be written again)
+    }
+    if (lane == 0 && *abrt)
+      for (int q = 0; q < a.stages && q < issued; ++q)  // copies in flight land first
+        tc::mbar_wait(&full[q], uint32_t((issued - 1 - q) / a.stages) & 1, &g_mx_decode_err);
+    return;
+  }
+
+  const int g = lane >> 2, t = lane & 3;
+  // this warp's row tile within a stage and its unit there
+  const int sub = warp / a.su, my = warp - sub * a.su;
+  int s = 0;
+  uint32_t ph = 0;
+  for (int u0 = 0; u0 < units; u0 += a.slice) {
+    const int uend = min(u0 + a.slice, units);
+    // the tokens' largest and smallest exponent fields (of finite values that are not zero)
+    if (threadIdx.x < a.T) {
+      emax[threadIdx.x] = -1;
+      emin[threadIdx.x] = 255;
+    }
+    dc_sync();  // (and the columns of the last slice are read)
+    for (int e = threadIdx.x; e < a.T * pieces; e += DC_WARPS * 32) {
+      const int tok = e / pieces, c = e - tok * pieces;  // one token per warp: pieces % 32 == 0
+      const uint4 v = load_piece(a, tok, u0 * DC_UNIT + c * 8);
+      xs[xs_at(tok, c, pieces)] = v;  // as it is; one column per token replaces it in place
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      int hi = -1, lo = 255;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t bits = (w[j >> 1] >> ((j & 1) * 16)) & 0x7FFFu;
+        const int b = int(bits >> 7);
+        if (bits != 0 && b != 255) {
+          hi = max(hi, b);
+          lo = min(lo, b);
+        }
+      }
+      hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+      lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+      if (lane == 0 && hi >= 0) {
+        atomicMax(&emax[tok], hi);
+        atomicMin(&emin[tok], lo);
+      }
+    }
+    dc_sync();
+    if (threadIdx.x < a.T && emax[threadIdx.x] < 0) emax[threadIdx.x] = emin[threadIdx.x] = 127;
+    __syncthreads();
+    int windows = 1;
+    for (int k = 0; k < a.T; ++k) windows = max(windows, (emax[k] - emin[k]) / 32 + 1);
+    const int per_tok = min(windows, a.wcols), cols = a.T * per_tok;
+    const int passes = (windows + a.wcols - 1) / a.wcols;
+
+    for (int pass = 0; pass < passes; ++pass) {
+      if (pass || per_tok > 1) dc_sync();  // the last pass's columns, or the tokens, are read
+      for (int e = threadIdx.x; e < cols * pieces; e += DC_WARPS * 32) {
+        const int col = e / pieces, c = e - col * pieces;
+        const int tok = col / per_tok, win = pass * a.wcols + col - tok * per_tok;
+        uint4* x = &xs[xs_at(col, c, pieces)];
+        // (the same thread wrote the same piece when one column per token is kept)
+        const uint4 v = passes == 1 && per_tok == 1 ? *x : load_piece(a, tok, u0 * DC_UNIT + c * 8);
+        *x = window_piece(v, emax[tok], win);
+      }
+      dc_sync();
+      const bool first = u0 == 0 && pass == 0, last = uend == units && pass == passes - 1;
+      // The warps' sums of several row tiles are kept before they are added up together: a
+      // meeting of the warps per tile costs more than the tile's copies.
+      const int slots = DC_RED / (DC_WARPS * kRows * 4 * cols);
+      int slot = 0, local = 0;
+      // Column g (or any other, where there are fewer: those sums are not used) at this lane's
+      // words; pieces of odd columns are swapped in fours.
+      const int mycol = min(g, cols - 1), flip = (mycol & 1) * 4;
+      const uint4* xb = xs + mycol * pieces + t;
+      for (int grp = blockIdx.x; grp < groups; grp += gridDim.x) {
+        float acc[4] = {};
+        for (int u = u0; u < uend; u += a.su) {
+          const bool got = tc::mbar_try(&full[s], ph) ||
+                           (!*abrt && tc::mbar_wait(&full[s], ph, &g_mx_decode_err));
+          if (!got) *abrt = 1;
+          const int unit = u + my;
+          if (got && sub < a.tps && unit < uend) {
+            const unsigned char* cbase = ring + s * sbytes + (my * srows + sub * kRows + g) * 128 + t * 4;
+            const unsigned char* ebase = ring + s * sbytes + (a.su * srows + sub * kRows + g) * 128 +
+                                         (((my >> 1) ^ g) << 4) + (my & 1) * 8;
+            const uint2 e0 = *reinterpret_cast<const uint2*>(ebase);
+            const uint2 e1 = *reinterpret_cast<const uint2*>(ebase + 1024);
+            uint32_t w0[8], w1[8];
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+              const unsigned char* cb = cbase + ((b ^ g) << 4);
+              w0[b] = *reinterpret_cast<const uint32_t*>(cb);
+              w1[b] = *reinterpret_cast<const uint32_t*>(cb + 1024);
+            }
+            // scales whose power is an fp32 normal by a shift; lane t looks over one of the
+            // four words for a byte below 16, or 255
+            const uint2 eh = (t & 2) ? e1 : e0;
+            const uint32_t w = (t & 1) ? eh.y : eh.x, low = w & 0xF0F0F0F0u, inv = ~w;
+            const uint32_t odd = ((low - 0x01010101u) & ~low & 0x80808080u) |
+                                 ((inv - 0x01010101u) & w & 0x80808080u);
+            float s0[8], s1[8];
+            if (!__any_sync(0xFFFFFFFFu, odd != 0) && unit * 8 + 8 <= a.nb) {
+#pragma unroll
+              for (int b = 0; b < 8; ++b) {
+                s0[b] = __uint_as_float((__byte_perm(b < 4 ? e0.x : e0.y, 0, 0x4440 | (b & 3)) << 23) - (15u << 23));
+                s1[b] = __uint_as_float((__byte_perm(b < 4 ? e1.x : e1.y, 0, 0x4440 | (b & 3)) << 23) - (15u << 23));
+              }
+            } else {  // padding after the row's last block counts as 0
+#pragma unroll
+              for (int b = 0; b < 8; ++b) {
+                const bool in = unit * 8 + b < a.nb;
+                s0[b] = in ? any_scale(((b < 4 ? e0.x : e0.y) >> (8 * (b & 3))) & 0xFFu) : 0.f;
+                s1[b] = in ? any_scale(((b < 4 ? e1.x : e1.y) >> (8 * (b & 3))) & 0xFFu) : 0.f;
+              }
+            }
+            const uint4* xe = xb + (unit - u0) * 32 + flip;
+            const uint4* xo = xb + (unit - u0) * 32 - flip;
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+              uint32_t v0[4], v1[4];
+              widen_word(w0[b], v0);
+              widen_word(w1[b], v1);
+              const uint4 x = (b & 1) ? xo[b * 4] : xe[b * 4];
+              float c[4] = {0.f, 0.f, 0.f, 0.f};
+              mma16816(c, v0[0], v1[0], v0[1], v1[1], x.x, x.y);
+              mma16816(c, v0[2], v1[2], v0[3], v1[3], x.z, x.w);
+              acc[0] = fmaf(s0[b], c[0], acc[0]);
+              acc[1] = fmaf(s0[b], c[1], acc[1]);
+              acc[2] = fmaf(s1[b], c[2], acc[2]);
+              acc[3] = fmaf(s1[b], c[3], acc[3]);
+            }
+          }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&empty[s]);
+          if (++s == a.stages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+        float* out = red + ((slot * DC_WARPS + warp) * kRows + g) * cols;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          if (2 * t + q < cols) {
+            out[2 * t + q] = acc[q];
+            out[8 * cols + 2 * t + q] = acc[2 + q];
+          }
+        ++slot;
+        if (slot < slots && grp + int(gridDim.x) < groups) continue;
+        dc_sync();
+        const int per = kRows * a.T, per_grp = per * a.tps;
+        for (int e = threadIdx.x; e < per_grp * slot; e += DC_WARPS * 32) {
+          const int q = e / per_grp, ts = (e - q * per_grp) / per, rest = e - q * per_grp - ts * per;
+          const int i = rest % kRows, tok = rest / kRows;
+          const int row = ((grp - (slot - 1 - q) * int(gridDim.x)) * a.tps + ts) * kRows + i;
+          if (row >= a.m) continue;
+          const float* p = red + ((q * DC_WARPS + ts * a.su) * kRows + i) * cols + tok * per_tok;
+          float v = 0.f;
+          for (int c = per_tok - 1; c >= 0; --c) {
+            float col = p[c];
+#pragma unroll 4
+            for (int w = 1; w < a.su; ++w) col += p[w * kRows * cols + c];
+            v += ldexpf(col, emax[tok] - 127 - 32 * (pass * a.wcols + c));
+          }
+          float* keep = ysum + ((int64_t(local + q) * a.tps + ts) * a.T + tok) * kRows + i;
+          if (!first) v += *keep;
+          if (!last) {
+            *keep = v;
+            continue;
+          }
+          const int64_t at = int64_t(tok) * a.m + row;
+          if (a.add) v += __bfloat162float(a.add[at]);
+          a.Y[at] = __float2bfloat16_rn(v);
+        }
+        dc_sync();
+        local += slot;
+        slot = 0;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ---- f32 ------------------------------------------------------------------------
+constexpr int DF_WARPS = 8;
+constexpr int DF_TOK = 8;      // tokens of a pass
+constexpr int DF_SLAB = 1024;  // values of K staged at a time: 128 per warp
+
+// A CTA takes 32 rows (a lane each) × up to 8 tokens; its eight warps divide each slab of K.
+// A row's 16 bytes of codes are read by one lane; four blocks later the
+// lane has used the whole 64 bytes, which stay in L1 meanwhile.
+__global__ void __launch_bounds__(DF_WARPS * 32)
+    k_mx_decode_f32(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t cpitch,
+                    int64_t spitch, const float* __restrict__ X, const float* add, float* Y, int m, int n,
+                    int nb, int T) {
+  __shared__ __align__(16) float xs[DF_TOK][DF_SLAB];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int i = blockIdx.x * 32 + lane, row = min(i, m - 1);
+  const int t0 = blockIdx.y * DF_TOK, nt = min(DF_TOK, T - t0);
+  float acc[DF_TOK] = {};
+  for (int k0 = 0; k0 < n; k0 += DF_SLAB) {
+    uint4 c[4];
+    uint32_t s = 0;
+    const int b0 = k0 / 32 + warp * 4;
+    if (b0 < nb) s = __ldg(reinterpret_cast<const uint32_t*>(scales + int64_t(row) * spitch + b0));
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      c[q] = b0 + q < nb ? __ldg(reinterpret_cast<const uint4*>(codes + int64_t(row) * cpitch + int64_t(b0 + q) * 16))
+                         : make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    for (int e = threadIdx.x; e < nt * DF_SLAB; e += DF_WARPS * 32) {
+      const int tok = e / DF_SLAB, k = e % DF_SLAB;
+      xs[tok][k] = k0 + k < n ? X[int64_t(t0 + tok) * n + k0 + k] : 0.f;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (b0 + q >= nb) break;
+      const float scale = mx::scale_f32((s >> (8 * q)) & 0xFFu);
+      const uint32_t w[4] = {c[q].x, c[q].y, c[q].z, c[q].w};
+      float part[DF_TOK] = {};
+#pragma unroll
+      for (int z = 0; z < 8; ++z) {
+        float d[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) d[p] = mx::e2m1_f32((w[z >> 1] >> ((z & 1) * 16 + p * 4)) & 15u) * scale;
+#pragma unroll
+        for (int tok = 0; tok < DF_TOK; ++tok) {
+          if (tok >= nt) break;
+          const float4 x = *reinterpret_cast<const float4*>(&xs[tok][warp * 128 + q * 32 + z * 4]);
+          part[tok] = fmaf(d[0], x.x, part[tok]);
+          part[tok] = fmaf(d[1], x.y, part[tok]);
+          part[tok] = fmaf(d[2], x.z, part[tok]);
+          part[tok] = fmaf(d[3], x.w, part[tok]);
+        }
+      }
+#pragma unroll
+      for (int tok = 0; tok < DF_TOK; ++tok) acc[tok] += part[tok];
+    }
+  }
+  __syncthreads();
+  float* red = &xs[0][0];  // [warp][token][row]
+#pragma unroll
+  for (int tok = 0; tok < DF_TOK; ++tok) red[(warp * DF_TOK + tok) * 32 + lane] = acc[tok];
+  __syncthreads();
+  // warp w adds up token w
+  if (warp < nt && i < m) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < DF_WARPS; ++w) v += red[(w * DF_TOK + warp) * 32 + lane];
+    const int64_t at = int64_t(t0 + warp) * m + i;
+    if (add) v += add[at];
+    Y[at] = v;
+  }
+}
+static_assert(DF_WARPS * DF_TOK * 32 <= DF_TOK * DF_SLAB, "the sums fit where the tokens were");
+
+// How a call is laid out in shared memory; stages = 0 where it does not fit.
+struct DcPlan {
+  int wcols, slice, su, tps, stages, ysum, ring, bytes, grid;
+};
+DcPlan decode_plan(int64_t T, int64_t m, int64_t n) {
+  DcPlan p = {};
+  p.wcols = 2 * T <= 8 ? 2 : 1;
+  const int rows = 16;
+  const int units = int((mx::blocks(n) + 7) / 8);
+  const int64_t tiles = (m + rows - 1) / rows;
+  const int red = DC_RED;
+  // the widest slice (all of K at best) that leaves room for two stages at least; with
+  // more than one, slices of whole stages of 16 units, or of an even number of units (a
+  // copy of scales starts on 16 bytes)
+  for (int count = 1; count <= units; ++count) {
+    p.slice = (units + count - 1) / count;
+    if (count > 1) p.slice = p.slice >= 16 ? p.slice / 16 * 16 : (p.slice + 1) / 2 * 2;
+    p.su = std::min(p.slice, DC_WARPS);
+    p.tps = DC_WARPS / p.su;
+    const int64_t groups = (tiles + p.tps - 1) / p.tps;
+    p.grid = int(std::min<int64_t>(groups, 148));
+    const int64_t ysum = (groups + p.grid - 1) / p.grid * p.tps * T * rows * 4;
+    const int64_t xs = T * p.wcols * p.slice * (DC_UNIT * 2);
+    const int stage = dc_stage_bytes(p.su, p.tps * rows);
+    const int64_t left = DC_SMEM_MAX - round_up(red + xs, 1024) - ysum;
+    if (left < 2 * stage) continue;
+    p.stages = int(std::min<int64_t>(DC_MAX_STAGES, left / stage));
+    p.ring = int(round_up(red + xs, 1024));
+    p.ysum = p.ring + p.stages * stage;
+    p.bytes = p.ysum + int(ysum) + 1024;
+    return p;
+  }
+  p.stages = 0;
+  return p;
+}
+
+}  // namespace
+
+bool mx_decode_fits(int64_t T, int64_t m, int64_t n) {
+  return T <= kMxDecodeMax && tmap_available() && decode_plan(T, m, n).stages >= 2;
+}
+
+hsl_status mx_decode_run(const MxOperand& D, int64_t m, int64_t n, const void* X, const void* add, void* Y,
+                         int64_t T, cudaStream_t s) {
+  const DcPlan p = decode_plan(T, m, n);
+  DcArgs a;
+  DcMaps maps;
+  memset(&maps, 0, sizeof(maps));
+  const int rows = 16 * p.tps;
+  const auto U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const auto SW = CU_TENSOR_MAP_SWIZZLE_128B;
+  const int64_t whole = D.pitch / 128;
+  if ((whole > 0 && !make_tmap_3d_bytes(&maps.c3, D.p, {128, m, whole}, D.pitch, 128, {128, rows, p.su}, SW)) ||
+      !make_tmap_2d(&maps.c2, U8, 1, D.p, m, D.pitch, D.pitch, 128, rows, SW) ||
+      !make_tmap_2d(&maps.s, U8, 1, D.scales, m, D.spitch, D.spitch, 128, rows, SW)) {
+    set_message("tensor map encoding failed");
+    return HSL_ERR_CUDA;
+  }
+  a.X = static_cast<const __nv_bfloat16*>(X);
+  a.add = static_cast<const __nv_bfloat16*>(add);
+  a.Y = static_cast<__nv_bfloat16*>(Y);
+  a.m = int(m);
+  a.n = int(n);
+  a.nb = int(mx::blocks(n));
+  a.T = int(T);
+  a.vec = n % 8 == 0 && reinterpret_cast<uintptr_t>(X) % 16 == 0 ? 1 : 0;
+  a.wcols = p.wcols;
+  a.ring = p.ring;
+  a.slice = p.slice;
+  a.su = p.su;
+  a.tps = p.tps;
+  a.stages = p.stages;
+  a.ysum = p.ysum;
+  if (cudaError_t e = allow_dyn_smem(reinterpret_cast<const void*>(k_mx_decode), p.bytes))
+    return cuda_fail(e, "4-bit decode smem attribute");
+  note_launch();
+  k_mx_decode<<<unsigned(p.grid), DC_THREADS, size_t(p.bytes), s>>>(maps, a);
+  return cuda_fail(cudaGetLastError(), "4-bit decode launch");
+}
+
+cudaError_t mx_decode_error_word(uint32_t** p) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_mx_decode_err);
+}
+
+hsl_status mx_decode_f32_run(const MxOperand& D, int64_t m, int64_t n, const void* X, const void* add,
+                             void* Y, int64_t T, cudaStream_t s) {
+  const dim3 grid(unsigned((m + 31) / 32), unsigned((T + DF_TOK - 1) / DF_TOK));
+  note_launch();
+  k_mx_decode_f32<<<grid, DF_WARPS * 32, 0, s>>>(static_cast<const uint8_t*>(D.p), D.scales, D.pitch, D.spitch,
+                                                 static_cast<const float*>(X), static_cast<const float*>(add),
+                                                 static_cast<float*>(Y), int(m), int(n), int(mx::blocks(n)),
+                                                 int(T));
+  return cuda_fail(cudaGetLastError(), "4-bit f32 decode launch");
+}
+
+}  // namespace hsl

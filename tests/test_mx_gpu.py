@@ -219,3 +219,63 @@ def test_no_tokens(hsl):
     assert not hsl.mx4_apply_t(E, dY).any()
     one = torch.ones(3, 40, dtype=torch.bfloat16, device="cuda")
     assert torch.equal(hsl.mx4_apply_t(E, dY, add=one), one)
+
+
+@pytest.mark.parametrize("T,m,n", [(1, 65, 300), (2, 64, 512), (4, 33, 1000), (5, 96, 777), (16, 40, 2048)])
+def test_apply_tokens_of_any_range(hsl, T, m, n):
+    """Tokens whose values span far more binades than one scaled 16-bit operand holds, with the
+    small ones alone deciding the outputs of half the rows; all zeros; a single value."""
+    rng = np.random.default_rng(T + m)
+    d0 = weights(m, n, 3)
+    x = rng.standard_normal((T, n)) * np.exp2(rng.integers(-100, 40, size=(T, n)))
+    big = rng.random(n) < 0.1
+    x[:, big] *= 2.0 ** 70
+    d0[::2, big] = 0.0               # these rows see only the small values
+    if T > 1:
+        x[1] = 0.0
+    if T > 2:
+        x[2] = 0.0
+        x[2, n // 2] = 2.0 ** -130    # a bf16 subnormal
+    D, d = blocks(hsl, d0, "e2m1")
+    t = tensor(x, "bf16")
+    want, mag = mx.apply(d, f64(t)), mx.apply(np.abs(d), np.abs(f64(t)))
+    # (fp32 products below 2^-126 may lose bits: 2^-149 for each of the n terms)
+    close(hsl.mx4_apply(D, t), want, mag, n, "bf16", n * 2.0 ** -140)
+    hsl.mx_check()
+
+
+@pytest.mark.parametrize("T", [1, 3, 17, 70])
+def test_apply_infinities_and_nan(hsl, T):
+    """An infinity or a NaN in a token reaches its outputs and no other token's; a NaN block
+    of D reaches its row."""
+    m, n = 130, 352
+    D, d = blocks(hsl, weights(m, n, 1), "e2m1")
+    x = tokens(T, n, 2)
+    x[0, 5], x[T - 1, 7] = np.inf, (np.nan if T > 1 else 1.0)
+    t = tensor(x, "bf16")
+    with np.errstate(invalid="ignore"):
+        want = mx.apply(d, f64(t))
+    got = f64(hsl.mx4_apply(D, t))
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    assert np.array_equal(np.isinf(got), np.isinf(want))
+    both = np.isinf(want)
+    assert np.array_equal(got[both], want[both])
+    w = weights(m, n, 1)
+    w[3, 40] = np.nan
+    q = hsl.mx_quantize(tensor(w, "bf16"))
+    y = f64(hsl.mx4_apply(q, tensor(tokens(T, n, 2), "bf16")))
+    assert np.isnan(y[:, 3]).all() and np.isfinite(np.delete(y, 3, axis=1)).all()
+
+
+@pytest.mark.parametrize("T", [1, 6, 40])
+def test_apply_scales_at_the_ends(hsl, T):
+    """Blocks whose power of two is very small or very large."""
+    m, n = 48, 320
+    w = weights(m, n, 4)
+    w[::3] *= 2.0 ** -121
+    w[1::3] *= 2.0 ** 60
+    w[5, :32] = 0.0
+    D, d = blocks(hsl, w, "e2m1")
+    t = tensor(tokens(T, n, 5), "bf16")
+    want, mag = mx.apply(d, f64(t)), mx.apply(np.abs(d), np.abs(f64(t)))
+    close(hsl.mx4_apply(D, t), want, mag, n, "bf16", n * 2.0 ** -140)
