@@ -59,9 +59,21 @@ __device__ __forceinline__ void widen_word(uint32_t w, uint32_t (&v)[4]) {
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
       : "r"(w));
 }
-// 2^(e − 142) for any scale byte: fp32 subnormals below e = 16; 255 stands for NaN.
-__device__ __forceinline__ float any_scale(uint32_t e) {
-  return __uint_as_float(e == 255u ? 0x7FC00000u : e >= 16u ? (e - 15u) << 23 : 1u << (e + 7u));
+// Four scale bytes (one word) → 2^(e − 142) in fp32: the conversion gives 2^(e − 127) as bf16 pairs
+// (2^−127 a subnormal, 255 a NaN), which widen by shifts.
+__device__ __forceinline__ void widen_scales(uint32_t w, float* s) {
+  uint32_t p[2];
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.bf16x2.ue8m0x2 %0, a;\n\t"
+      "cvt.rn.bf16x2.ue8m0x2 %1, b;\n\t}"
+      : "=r"(p[0]), "=r"(p[1])
+      : "r"(w));
+  constexpr float k = 1.0f / 32768.0f;
+  s[0] = bf_lo(p[0]) * k;
+  s[1] = bf_hi(p[0]) * k;
+  s[2] = bf_lo(p[1]) * k;
+  s[3] = bf_hi(p[1]) * k;
 }
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -116,7 +128,8 @@ __device__ __forceinline__ uint4 load_piece(const DcArgs& a, int tok, int col) {
 }
 // The values of a piece that belong to window `win` of a token whose largest exponent field is
 // `top`, scaled by 2^(142 − top + 32 win) to fp16; zeros elsewhere.
-__device__ __forceinline__ uint4 window_piece(const uint4& v, int top, int win) {
+// (`all`: there is one window, with every value in it).
+__device__ __forceinline__ uint4 window_piece(const uint4& v, int top, int win, bool all) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   const int k = 142 - top + 32 * win;  // in two factors: 2^k alone may not be an fp32 value
   const float f0 = __uint_as_float(uint32_t(127 + k / 2) << 23);
@@ -124,17 +137,25 @@ __device__ __forceinline__ uint4 window_piece(const uint4& v, int top, int win) 
   uint32_t o[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    float x[2] = {bf_lo(w[j]), bf_hi(w[j])};
+    float x[2] = {bf_lo(w[j]) * f0 * f1, bf_hi(w[j]) * f0 * f1};
+    if (!all) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int b = int((w[j] >> (h * 16 + 7)) & 0xFFu);
-      const int at = b == 255 ? 0 : (top - b) >> 5;
-      x[h] = at == win ? x[h] * f0 * f1 : 0.f;
+      for (int h = 0; h < 2; ++h) {
+        const int b = int((w[j] >> (h * 16 + 7)) & 0xFFu);
+        const int at = b == 255 ? 0 : (top - b) >> 5;
+        if (at != win) x[h] = 0.f;
+      }
     }
     const __half2 p = __floats2half2_rn(x[0], x[1]);
     o[j] = *reinterpret_cast<const uint32_t*>(&p);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
 }
 
 __device__ uint32_t g_mx_decode_err;
@@ -150,8 +171,8 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     k_mx_decode(const __grid_constant__ DcMaps maps, const DcArgs a) {
   constexpr int kRows = 16;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  unsigned char* smem = reinterpret_cast<unsigned char*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (an offset, not a rounded integer: the compiler still knows that this is shared memory)
+  unsigned char* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ uint64_t full[DC_MAX_STAGES], empty[DC_MAX_STAGES];
   __shared__ int abort_flag, emax[8], emin[8];
   float* red = reinterpret_cast<float*>(smem);  // [slot][DC_WARPS][kRows][columns]
@@ -286,7 +307,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         uint4* x = &xs[xs_at(col, c, pieces)];
         // (the same thread wrote the same piece when one column per token is kept)
         const uint4 v = passes == 1 && per_tok == 1 ? *x : load_piece(a, tok, u0 * DC_UNIT + c * 8);
-        *x = window_piece(v, emax[tok], win);
+        *x = window_piece(v, emax[tok], win, windows == 1);
       }
       dc_sync();
       const bool first = u0 == 0 && pass == 0, last = uend == units && pass == passes - 1;
@@ -306,39 +327,29 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
           if (!got) *abrt = 1;
           const int unit = u + my;
           if (got && sub < a.tps && unit < uend) {
-            const unsigned char* cbase = ring + s * sbytes + (my * srows + sub * kRows + g) * 128 + t * 4;
+            // (rows start on 128 bytes: chunk b ^ g by an exclusive or)
+            const uint32_t cbase = tc::smem_u32(ring) + s * sbytes + (my * srows + sub * kRows + g) * 128 +
+                                   (g << 4) + t * 4;
             const unsigned char* ebase = ring + s * sbytes + (a.su * srows + sub * kRows + g) * 128 +
                                          (((my >> 1) ^ g) << 4) + (my & 1) * 8;
-            const uint2 e0 = *reinterpret_cast<const uint2*>(ebase);
-            const uint2 e1 = *reinterpret_cast<const uint2*>(ebase + 1024);
+            uint2 e0 = *reinterpret_cast<const uint2*>(ebase);
+            uint2 e1 = *reinterpret_cast<const uint2*>(ebase + 1024);
+            if (unit * 8 + 8 > a.nb) {  // padding after the row's last block counts as 0
+              const int k = a.nb - unit * 8;
+              const uint32_t mx = k >= 4 ? ~0u : (1u << (8 * k)) - 1, my4 = k <= 4 ? 0u : (1u << (8 * (k - 4))) - 1;
+              e0.x &= mx; e1.x &= mx; e0.y &= my4; e1.y &= my4;
+            }
             uint32_t w0[8], w1[8];
 #pragma unroll
             for (int b = 0; b < 8; ++b) {
-              const unsigned char* cb = cbase + ((b ^ g) << 4);
-              w0[b] = *reinterpret_cast<const uint32_t*>(cb);
-              w1[b] = *reinterpret_cast<const uint32_t*>(cb + 1024);
+              w0[b] = lds32(cbase ^ (b << 4));
+              w1[b] = lds32((cbase ^ (b << 4)) + 1024);
             }
-            // scales whose power is an fp32 normal by a shift; lane t looks over one of the
-            // four words for a byte below 16, or 255
-            const uint2 eh = (t & 2) ? e1 : e0;
-            const uint32_t w = (t & 1) ? eh.y : eh.x, low = w & 0xF0F0F0F0u, inv = ~w;
-            const uint32_t odd = ((low - 0x01010101u) & ~low & 0x80808080u) |
-                                 ((inv - 0x01010101u) & w & 0x80808080u);
             float s0[8], s1[8];
-            if (!__any_sync(0xFFFFFFFFu, odd != 0) && unit * 8 + 8 <= a.nb) {
-#pragma unroll
-              for (int b = 0; b < 8; ++b) {
-                s0[b] = __uint_as_float((__byte_perm(b < 4 ? e0.x : e0.y, 0, 0x4440 | (b & 3)) << 23) - (15u << 23));
-                s1[b] = __uint_as_float((__byte_perm(b < 4 ? e1.x : e1.y, 0, 0x4440 | (b & 3)) << 23) - (15u << 23));
-              }
-            } else {  // padding after the row's last block counts as 0
-#pragma unroll
-              for (int b = 0; b < 8; ++b) {
-                const bool in = unit * 8 + b < a.nb;
-                s0[b] = in ? any_scale(((b < 4 ? e0.x : e0.y) >> (8 * (b & 3))) & 0xFFu) : 0.f;
-                s1[b] = in ? any_scale(((b < 4 ? e1.x : e1.y) >> (8 * (b & 3))) & 0xFFu) : 0.f;
-              }
-            }
+            widen_scales(e0.x, s0);
+            widen_scales(e0.y, s0 + 4);
+            widen_scales(e1.x, s1);
+            widen_scales(e1.y, s1 + 4);
             const uint4* xe = xb + (unit - u0) * 32 + flip;
             const uint4* xo = xb + (unit - u0) * 32 - flip;
 #pragma unroll

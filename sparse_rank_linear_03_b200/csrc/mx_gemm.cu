@@ -216,8 +216,8 @@ template <int AK, bool BMN, int TERMS, int MH, int OUT>
 __global__ void __launch_bounds__(G_THREADS, 1)
     k_mx_gemm(const __grid_constant__ GemmMaps maps, const GemmArgs g) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  unsigned char* smem = reinterpret_cast<unsigned char*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (an offset, not a rounded integer: the compiler still knows that this is shared memory)
+  unsigned char* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ uint64_t full[G_MAX_STAGES], empty[G_MAX_STAGES], accf;
   __shared__ uint64_t raw[G_MAX_STAGES], taken[G_MAX_STAGES];  // code tile landed, read
   __shared__ uint32_t tmem_slot;

@@ -83,8 +83,8 @@ template <typename TO, int MH>
 __global__ void __launch_bounds__(F_THREADS, 1)
     k_mx_matmul(const __grid_constant__ MmMaps maps, const MmArgs g) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  unsigned char* smem = reinterpret_cast<unsigned char*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (an offset, not a rounded integer: the compiler still knows that this is shared memory)
+  unsigned char* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ uint64_t full[F_MAX_STAGES], empty[F_MAX_STAGES], sfull[F_SRING], sempty[F_SRING], accf;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
