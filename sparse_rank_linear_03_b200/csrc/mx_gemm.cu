@@ -109,56 +109,10 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(const void* tile) {
 }
 
 // ---- widening -----------------------------------------------------------------
-__device__ __forceinline__ uint32_t mul_bf2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-__device__ __forceinline__ uint32_t sub_bf2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
-// 2^(e − 127) as a pair of bf16 (2^−127 is a subnormal; 255 stands for NaN).
-__device__ __forceinline__ uint32_t e2m1_scale(uint32_t e) {
-  const uint32_t b = e == 255u ? 0x7FC0u : e == 0u ? 0x0040u : e << 7;
-  return b | (b << 16);
-}
-// 2^(e − 127) / 64 (down to the subnormal 2^−133).
-__device__ __forceinline__ uint32_t int8_scale(uint32_t e) {
-  const uint32_t b = e == 255u ? 0x7FC0u : e > 6u ? (e - 6u) << 7 : 1u << e;
-  return b | (b << 16);
-}
-
-// Eight e2m1 codes (one word) → eight bf16.  The high and the low byte of the
-// eight magnitudes are looked up by byte permutes (a code's three low bits are
-// the selector), the sign bits gathered by a third.
-__device__ __forceinline__ uint4 widen_e2m1(uint32_t w, uint32_t scale) {
-  const uint32_t mag = w & 0x77777777u, w4 = w << 4;
-  uint32_t hi = __byte_perm(0x3F3F3F00u, 0x40404040u, mag);
-  uint32_t lo = __byte_perm(0xC0800000u, 0xC0804000u, mag);
-  hi |= __byte_perm(w4, w, 0x5140) & 0x80808080u;
-  uint4 v;
-  v.x = mul_bf2(__byte_perm(lo, hi, 0x5140), scale);
-  v.y = mul_bf2(__byte_perm(lo, hi, 0x7362), scale);
-  const uint32_t mag2 = mag >> 16;
-  hi = __byte_perm(0x3F3F3F00u, 0x40404040u, mag2);
-  lo = __byte_perm(0xC0800000u, 0xC0804000u, mag2);
-  hi |= __byte_perm(w4, w, 0x7362) & 0x80808080u;
-  v.z = mul_bf2(__byte_perm(lo, hi, 0x5140), scale);
-  v.w = mul_bf2(__byte_perm(lo, hi, 0x7362), scale);
-  return v;
-}
-// Four int8 (one word) → four bf16: 128 + (low 7 bits) is 0x4300 | bits, from which
-// 128 (0x4300) or, for a negative value, 256 (0x4380) is taken away.
-__device__ __forceinline__ uint2 widen_int8(uint32_t w, uint32_t scale) {
-  const uint32_t m = w & 0x7F7F7F7Fu, n = w & 0x80808080u;
-  uint2 v;
-  v.x = mul_bf2(sub_bf2(__byte_perm(m, 0x43434343u, 0x4140), __byte_perm(n, 0x43434343u, 0x4140)), scale);
-  v.y = mul_bf2(sub_bf2(__byte_perm(m, 0x43434343u, 0x4342), __byte_perm(n, 0x43434343u, 0x4342)), scale);
-  return v;
-}
+using mx::e2m1_scale;
+using mx::int8_scale;
+using mx::widen_e2m1;
+using mx::widen_int8;
 
 // The code tile of a K-block in shared memory, as copied: kBoxes boxes of kRows rows of
 // kInner bytes in the swizzle of that width, so that the threads of a warp, a row
