@@ -335,7 +335,6 @@ class Group:
 # ---- microscaled blocks -------------------------------------------------------
 
 MX_ELEM = {"e2m1": 0, "int8": 1}
-_MX_OP = {"apply": 0, "apply_t": 1, "matmul": 2, "factor_grad": 3}
 _DTYPE_NAME = {torch.float32: "f32", torch.bfloat16: "bf16"}
 
 
@@ -353,66 +352,109 @@ def _mx_workspace_bytes(op: int, batch: int, m: int, n: int, r: int, dtype: int)
     return b.value
 
 
+# the pointer of torch's current stream on a device, without the Stream object around it
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 class MX:
     """A matrix in microscaled blocks: codes and scales in the layout of hsl_mx.
 
     ``codes`` is [rows][code pitch] (uint8 for e2m1; int8 or uint8 for int8),
     ``scales`` [rows][scale pitch] uint8; both contiguous, on one CUDA device."""
 
-    __slots__ = ("codes", "scales", "rows", "cols", "elem", "_view", "_ref")
+    __slots__ = ("_codes", "_scales", "_buf", "rows", "cols", "elem", "device", "_view", "_ref")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int, elem: str = "e2m1"):
-        if elem not in MX_ELEM:
+        code = MX_ELEM.get(elem)
+        if code is None:
             raise ValueError(f"unknown element type {elem!r}")
-        nb = (cols + 31) // 32
         if cols < 1 or codes.dim() != 2 or scales.dim() != 2:
             raise ValueError("codes and scales are 2-D and cols >= 1")
-        rows = codes.shape[0]
-        if codes.shape[1] != nb * (16 if elem == "e2m1" else 32):
-            raise ValueError(f"codes have {codes.shape[1]} bytes per row, expected "
-                             f"{nb * (16 if elem == 'e2m1' else 32)}")
-        if scales.shape[0] != rows or scales.shape[1] != (nb + 15) // 16 * 16:
-            raise ValueError(f"scales must be [{rows}][{(nb + 15) // 16 * 16}]")
+        rows, cp = codes.shape
+        want_c, want_s = _pitches(cols, code)
+        if cp != want_c:
+            raise ValueError(f"codes have {cp} bytes per row, expected {want_c}")
+        if scales.shape != (rows, want_s):
+            raise ValueError(f"scales must be [{rows}][{want_s}]")
         if codes.dtype not in (torch.uint8, torch.int8) or scales.dtype != torch.uint8:
             raise ValueError("codes are uint8 (int8 for int8 blocks), scales uint8")
         if not codes.is_cuda or scales.device != codes.device:
             raise ValueError("codes and scales must be on one CUDA device")
-        self.codes, self.scales, self.rows, self.cols, self.elem = codes, scales, rows, cols, elem
-        self._view = _MXView(_ptr(codes), _ptr(scales), rows, cols, MX_ELEM[elem])
+        self._codes, self._scales, self._buf = codes, scales, None
+        self._set(_ptr(codes), _ptr(scales), rows, cols, elem, code, codes.device)
+
+    def _set(self, cptr, sptr, rows, cols, elem, code, device):
+        self.rows, self.cols, self.elem, self.device = rows, cols, elem, device
+        self._view = _MXView(cptr, sptr, rows, cols, code)
         self._ref = ctypes.addressof(self._view)
 
+    @classmethod
+    def empty(cls, rows: int, cols: int, elem: str, device) -> "MX":
+        """Room for a matrix, codes and scales in one allocation of torch's current stream."""
+        q = cls.__new__(cls)
+        code = MX_ELEM[elem]
+        cp, sp = _pitches(cols, code)
+        q._codes = q._scales = None
+        q._buf = buf = torch.empty(rows * (cp + sp), dtype=torch.uint8, device=device)
+        p = buf.data_ptr()
+        q._set(p, p + rows * cp, rows, cols, elem, code, buf.device)
+        return q
+
     @property
-    def device(self) -> torch.device:
-        return self.codes.device
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            cp, _ = _pitches(self.cols, MX_ELEM[self.elem])
+            c = self._buf[:self.rows * cp].view(self.rows, cp)
+            self._codes = c.view(torch.int8) if self.elem == "int8" else c
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            cp, sp = _pitches(self.cols, MX_ELEM[self.elem])
+            self._scales = self._buf[self.rows * cp:].view(self.rows, sp)
+        return self._scales
 
 
-class _On:
-    """Makes the tensors' device current, and the given stream torch's current one, for the
-    allocations and the launch of one call."""
+def _pitches(cols: int, code: int) -> tuple[int, int]:
+    nb = (cols + 31) >> 5
+    return nb << (5 if code else 4), (nb + 15) & ~15
 
-    __slots__ = ("ptr", "_ctx")
+
+class _Using:
+    """Makes a stream (and its device) torch's current one for the allocations and the launch of a
+    call."""
+
+    __slots__ = ("_ctx", "ptr")
 
     def __init__(self, device: torch.device, stream):
-        self._ctx = None
         if stream is None:
-            if device.index != torch.cuda.current_device():
-                self._ctx = torch.cuda.device(device)
+            self._ctx = torch.cuda.device(device)
             self.ptr = torch.cuda.current_stream(device).cuda_stream
-        else:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)),
-                                                   device=device)
-            self._ctx = torch.cuda.stream(stream)
-            self.ptr = stream.cuda_stream
+            return
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)),
+                                               device=device)
+        elif stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the data on {device}")
+        self._ctx = torch.cuda.stream(stream)
+        self.ptr = stream.cuda_stream
 
     def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
+        self._ctx.__enter__()
         return self.ptr
 
     def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
+        self._ctx.__exit__(*exc)
+
+
+def _mx_call(device: torch.device, stream, fn, *args):
+    """fn(stream pointer, *args) with the data's device current, and torch's current stream the
+    given one (None: the device's current stream)."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return fn(_raw_stream(device.index), *args)
+    with _Using(device, stream) as s:
+        return fn(s, *args)
 
 
 def _operand(t: torch.Tensor, shape: tuple, dtype: torch.dtype, device: torch.device, what: str) -> int:
@@ -435,9 +477,22 @@ def _mx_dtype(t: torch.Tensor) -> int:
     return DTYPE[name]
 
 
-def _scratch(op: str, batch: int, m: int, n: int, r: int, dtype: int, device: torch.device):
-    b = _mx_workspace_bytes(_MX_OP[op], batch, m, n, r, dtype)
-    return (torch.empty(b, dtype=torch.uint8, device=device) if b else None), b
+def _scratch(op: int, batch: int, m: int, n: int, r: int, dtype: int, device: torch.device):
+    """Scratch memory of a call: the tensor that holds it (or None), its pointer and size."""
+    b = _mx_workspace_bytes(op, batch, m, n, r, dtype)
+    if b == 0:
+        return None, None, 0
+    t = torch.empty(b, dtype=torch.uint8, device=device)
+    return t, t.data_ptr(), b
+
+
+def _quantize(s, X, xp, dt, rows, cols, elem):
+    q = MX.empty(rows, cols, elem, X.device)
+    v = q._view
+    st = lib.hsl_mx_quantize(xp, dt, rows, cols, v.elem, v.codes, v.scales, s)
+    if st:
+        _ok(st, "hsl_mx_quantize")
+    return q
 
 
 def mx_quantize(X: torch.Tensor, elem: str = "e2m1", stream=None) -> MX:
@@ -447,73 +502,105 @@ def mx_quantize(X: torch.Tensor, elem: str = "e2m1", stream=None) -> MX:
     if elem not in MX_ELEM:
         raise ValueError(f"unknown element type {elem!r}")
     rows, cols = X.shape
+    if cols < 1:
+        raise ValueError("X must have a column")
     dt = _mx_dtype(X)
-    xp = _operand(X, (rows, cols), X.dtype, X.device, "X")
-    nb = (cols + 31) // 32
-    with _On(X.device, stream) as s:
-        codes = torch.empty(rows, nb * (16 if elem == "e2m1" else 32), device=X.device,
-                            dtype=torch.uint8 if elem == "e2m1" else torch.int8)
-        scales = torch.empty(rows, (nb + 15) // 16 * 16, dtype=torch.uint8, device=X.device)
-        q = MX(codes, scales, cols, elem)
-        _ok(lib.hsl_mx_quantize(xp, dt, rows, cols, MX_ELEM[elem], codes.data_ptr(),
-                                scales.data_ptr(), s), "hsl_mx_quantize")
-    return q
+    if not X.is_contiguous():
+        raise ValueError("X must be contiguous")
+    return _mx_call(X.device, stream, _quantize, X, X.data_ptr(), dt, rows, cols, elem)
+
+
+def _dequantize(s, q, dtype):
+    X = torch.empty(q.rows, q.cols, dtype=TORCH_DTYPE[dtype], device=q.device)
+    st = lib.hsl_mx_dequantize(q._ref, X.data_ptr(), DTYPE[dtype], s)
+    if st:
+        _ok(st, "hsl_mx_dequantize")
+    return X
 
 
 def mx_dequantize(q: MX, dtype: str = "bf16", stream=None) -> torch.Tensor:
     """The values that the blocks stand for, [rows][cols] (hsl_mx_dequantize)."""
-    with _On(q.device, stream) as s:
-        X = torch.empty(q.rows, q.cols, dtype=TORCH_DTYPE[dtype], device=q.device)
-        _ok(lib.hsl_mx_dequantize(q._ref, X.data_ptr(), DTYPE[dtype], s), "hsl_mx_dequantize")
-    return X
+    if dtype not in DTYPE:
+        raise ValueError(f"unknown dtype {dtype!r}")
+    return _mx_call(q.device, stream, _dequantize, q, dtype)
 
 
-def _mx4_product(fn, name: str, op: str, D: MX, X: torch.Tensor, k: int, f: int, add, Y, stream):
+def _apply(s, trans, D, X, xp, ap, add, Y, batch, f, dt):
+    dev = D.device
+    if Y is None:
+        Y = X.new_empty(batch, f)
+        yp = Y.data_ptr()
+    else:
+        yp = _operand(Y, (batch, f), X.dtype, dev, "the output")
+    keep, wp, wb = _scratch(trans, batch, D.rows, D.cols, 0, dt, dev)
+    fn = lib.hsl_mx4_apply_t if trans else lib.hsl_mx4_apply
+    st = fn(D._ref, xp, ap, yp, batch, dt, wp, wb, s)
+    if st:
+        _ok(st, "hsl_mx4_apply_t" if trans else "hsl_mx4_apply")
+    return Y
+
+
+def _mx4_product(trans: int, D: MX, X: torch.Tensor, add, Y, stream):
     if X.dim() != 2:
         raise ValueError("the input must be 2-D [batch][features]")
-    dev, dt = D.codes.device, _mx_dtype(X)
+    k, f = (D.rows, D.cols) if trans else (D.cols, D.rows)
+    dt = _mx_dtype(X)
     batch = X.shape[0]
-    xp = _operand(X, (batch, k), X.dtype, dev, "the input")
-    ap = _operand(add, (batch, f), X.dtype, dev, "add") if add is not None else None
-    with _On(dev, stream) as s:
-        if Y is None:
-            Y = torch.empty(batch, f, dtype=X.dtype, device=dev)
-        yp = _operand(Y, (batch, f), X.dtype, dev, "the output")
-        ws, wb = _scratch(op, batch, D.rows, D.cols, 0, dt, dev)
-        _ok(fn(D._ref, xp, ap, yp, batch, dt, ws.data_ptr() if wb else None, wb, s), name)
-    return Y
+    xp = _operand(X, (batch, k), X.dtype, D.device, "the input")
+    ap = None if add is None else _operand(add, (batch, f), X.dtype, D.device, "add")
+    return _mx_call(D.device, stream, _apply, trans, D, X, xp, ap, add, Y, batch, f, dt)
 
 
 def mx4_apply(D: MX, X: torch.Tensor, Y: torch.Tensor | None = None,
               add: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y [batch][m] = X [batch][n] Dᵀ (+ add), D [m][n] in e2m1 blocks (hsl_mx4_apply).
     ``add`` may be Y, e.g. the output of the layer's sparse and low-rank part."""
-    return _mx4_product(lib.hsl_mx4_apply, "hsl_mx4_apply", "apply", D, X, D.cols, D.rows, add, Y, stream)
+    return _mx4_product(0, D, X, add, Y, stream)
 
 
 def mx4_apply_t(D: MX, dY: torch.Tensor, dX: torch.Tensor | None = None,
                 add: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """dX [batch][n] = dY [batch][m] D (+ add): the gradient of mx4_apply's input
     (hsl_mx4_apply_t)."""
-    return _mx4_product(lib.hsl_mx4_apply_t, "hsl_mx4_apply_t", "apply_t", D, dY, D.rows, D.cols, add, dX,
-                        stream)
+    return _mx4_product(1, D, dY, add, dX, stream)
+
+
+def _matmul(s, A, B, Y, ap, add, tdt, dt):
+    if Y is None:
+        Y = torch.empty(A.rows, B.rows, dtype=tdt, device=A.device)
+        yp = Y.data_ptr()
+    else:
+        yp = _operand(Y, (A.rows, B.rows), tdt, A.device, "Y")
+    keep, wp, wb = _scratch(2, A.rows, B.rows, A.cols, 0, dt, A.device)
+    st = lib.hsl_mx4_matmul(A._ref, B._ref, ap, yp, dt, wp, wb, s)
+    if st:
+        _ok(st, "hsl_mx4_matmul")
+    return Y
 
 
 def mx4_matmul(A: MX, B: MX, Y: torch.Tensor | None = None, dtype: str = "bf16",
                add: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y [A.rows][B.rows] = A Bᵀ (+ add), both in e2m1 blocks (hsl_mx4_matmul)."""
-    dev, tdt = A.device, TORCH_DTYPE[dtype]
-    if B.device != dev:
-        raise ValueError(f"B is on {B.device}, expected {dev}")
-    ap = _operand(add, (A.rows, B.rows), tdt, dev, "add") if add is not None else None
-    with _On(dev, stream) as s:
-        if Y is None:
-            Y = torch.empty(A.rows, B.rows, dtype=tdt, device=dev)
-        yp = _operand(Y, (A.rows, B.rows), tdt, dev, "Y")
-        ws, wb = _scratch("matmul", A.rows, B.rows, A.cols, 0, DTYPE[dtype], dev)
-        _ok(lib.hsl_mx4_matmul(A._ref, B._ref, ap, yp, DTYPE[dtype], ws.data_ptr() if wb else None, wb, s),
-            "hsl_mx4_matmul")
-    return Y
+    if dtype not in DTYPE:
+        raise ValueError(f"unknown dtype {dtype!r}")
+    if B.device != A.device:
+        raise ValueError(f"B is on {B.device}, expected {A.device}")
+    tdt = TORCH_DTYPE[dtype]
+    ap = None if add is None else _operand(add, (A.rows, B.rows), tdt, A.device, "add")
+    return _mx_call(A.device, stream, _matmul, A, B, Y, ap, add, tdt, DTYPE[dtype])
+
+
+def _factor_grad(s, X, dY, U, V, gp, up, vp, ap, add, dx, dt):
+    dev = X.device
+    m, r = U.shape
+    dU, dV = torch.empty_like(U), torch.empty_like(V)
+    dX = dY.new_empty(X.rows, X.cols) if dx else None
+    keep, wp, wb = _scratch(3, X.rows, m, X.cols, r, dt, dev)
+    st = lib.hsl_mx8_factor_grad(X._ref, gp, m, up, vp, r, ap, dU.data_ptr(), dV.data_ptr(),
+                                 dX.data_ptr() if dx else None, dt, wp, wb, s)
+    if st:
+        _ok(st, "hsl_mx8_factor_grad")
+    return (dU, dV, dX) if dx else (dU, dV)
 
 
 def mx8_factor_grad(X: MX, dY: torch.Tensor, U: torch.Tensor, V: torch.Tensor, dx: bool = False,
@@ -522,27 +609,19 @@ def mx8_factor_grad(X: MX, dY: torch.Tensor, U: torch.Tensor, V: torch.Tensor, d
     dU [m][r] and dV [n][r], and with ``dx`` also dX [T][n] = dY U Vᵀ (+ add)."""
     if dY.dim() != 2 or U.dim() != 2:
         raise ValueError("dY and U must be 2-D")
-    dev, dt = X.device, _mx_dtype(dY)
-    m, r = U.shape
-    gp = _operand(dY, (X.rows, m), dY.dtype, dev, "dY")
-    up = _operand(U, (m, r), dY.dtype, dev, "U")
-    vp = _operand(V, (X.cols, r), dY.dtype, dev, "V")
     if add is not None and not dx:
         raise ValueError("add is for dX: pass dx=True")
-    ap = _operand(add, (X.rows, X.cols), dY.dtype, dev, "add") if add is not None else None
-    with _On(dev, stream) as s:
-        dU, dV = torch.empty_like(U), torch.empty_like(V)
-        dX = torch.empty(X.rows, X.cols, dtype=dY.dtype, device=dev) if dx else None
-        ws, wb = _scratch("factor_grad", X.rows, m, X.cols, r, dt, dev)
-        _ok(lib.hsl_mx8_factor_grad(X._ref, gp, m, up, vp, r, ap, dU.data_ptr(), dV.data_ptr(),
-                                    dX.data_ptr() if dx else None, dt, ws.data_ptr() if wb else None,
-                                    wb, s), "hsl_mx8_factor_grad")
-    return (dU, dV, dX) if dx else (dU, dV)
+    dev, dt, tdt = X.device, _mx_dtype(dY), dY.dtype
+    m, r = U.shape
+    gp = _operand(dY, (X.rows, m), tdt, dev, "dY")
+    up = _operand(U, (m, r), tdt, dev, "U")
+    vp = _operand(V, (X.cols, r), tdt, dev, "V")
+    ap = None if add is None else _operand(add, (X.rows, X.cols), tdt, dev, "add")
+    return _mx_call(dev, stream, _factor_grad, X, dY, U, V, gp, up, vp, ap, add, dx, dt)
 
 
 def mx_check(device=None, stream=None) -> None:
     """Synchronise the stream and raise if a device wait of the microscaled operators gave up
     on the device (hsl_mx_check)."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    with _On(dev, stream) as s:
-        _ok(lib.hsl_mx_check(s), "hsl_mx_check")
+    _ok(_mx_call(dev, stream, lib.hsl_mx_check), "hsl_mx_check")
