@@ -88,13 +88,6 @@ __device__ __forceinline__ bool g_wait(uint64_t* bar, uint32_t parity, volatile 
   return false;
 }
 
-// One lane of a converged warp, chosen so that the compiler knows the choice is uniform.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
-  return p != 0;
-}
-
 // M- or N-major operand in the 128-byte swizzle: 64 values along the row, 8 k per
 // 1024-byte atom; the next 64 values of the row dimension 8192 bytes on.
 __device__ __forceinline__ uint64_t desc_mn_sw128(const void* tile) {
@@ -283,7 +276,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (elect_one()) {
+    if (tc::elect_one()) {
       const uint32_t idesc = tc::idesc_bf16(128, g.BN) | (a_is_mmajor(AK) ? 1u << 15 : 0u) |
                              (BMN ? 1u << 16 : 0u);
       int s = 0;

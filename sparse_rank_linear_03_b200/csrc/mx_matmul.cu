@@ -55,6 +55,7 @@ struct MmArgs {
 };
 
 __device__ __forceinline__ bool f_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (tc::mbar_try(bar, parity)) return true;
   if (*abort_flag) return false;
   if (tc::mbar_wait(bar, parity, &g_mx_matmul_err)) return true;
   *abort_flag = 1;
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (tc::elect_one()) {
       const uint32_t id0 = idesc_mxf4(128, g.BN, 0), id2 = idesc_mxf4(128, g.BN, 2);
       int s = 0;
       uint32_t ph = 0;
