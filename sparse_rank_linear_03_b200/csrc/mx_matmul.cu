@@ -4,10 +4,12 @@
 //
 // tcgen05.mma kind::mxf4 takes both operands as packed 4-bit floats and multiplies
 // each 32-term piece of a dot product by the two blocks' powers of two, with fp32
-// sums: the definition itself, no widening.  The rows of B (features) are the M side of
-// the MMA, the rows of A (tokens) its N side.
+// sums: the definition itself, no widening.  With 256 tokens or more the tokens are the M
+// side of the MMA and the features its N side: a TMEM lane then holds neighbouring
+// values of an output row, which go out in 16-byte pieces.  With fewer, the features are
+// the M side, so that no accumulator row is idle.
 //
-//   warp 0 lane 0   TMA of the code tiles: 128·MH rows of B and BN rows of A, 256
+//   warp 0 lane 0   TMA of the code tiles: 128·MH rows of the M side, BN of the N side, 256
 //                   values (128 bytes) each, 128-byte swizzle
 //   warp 10 lane 0  TMA of the scale bytes, 16 per row: two K-blocks at a time
 //   warps 2-5       put a K-block's scales where the MMA reads them: TMEM lane
@@ -19,7 +21,7 @@
 //
 // Bound by the copies into shared memory: at 4 bits a 128 × 256 × 256 step takes the
 // MMA 512 cycles and brings 48 KB, so the tile is 256 × 192 (two accumulators
-// sharing the A-row tile): 56 KB per 768 cycles.  The two accumulators take 384
+// sharing the N side's tile): 56 KB per 768 cycles.  The two accumulators take 384
 // TMEM columns, the scales of the stages the rest.  Every wait is bounded.
 #include <cuda.h>
 
@@ -43,12 +45,12 @@ constexpr int F_SRING = 3;                 // scale tiles (two K-blocks each) in
 constexpr int F_SMEM_BUDGET = 216 * 1024;  // code stages and scale tiles
 
 struct MmMaps {
-  CUtensorMap b, bs;  // codes box {128 B, 128}, scales box {16 B, 128}
-  CUtensorMap a, as;  // codes box {128 B, BN}, scales box {16 B, BN}
-  CUtensorMap c;      // box {128·MH, BN}
+  CUtensorMap b, bs;  // M side: codes box {128 B, 128}, scales box {16 B, 128}
+  CUtensorMap a, as;  // N side: codes box {128 B, BN}, scales box {16 B, BN}
+  CUtensorMap c;      // box {64, 128} (kRows) or {128·MH, BN}
 };
 struct MmArgs {
-  int M, N, nk, nb;  // rows of B, rows of A, K-blocks of 256, blocks per row
+  int M, N, nk, nb;  // rows of the M side, of the N side, K-blocks of 256, blocks per row
   int BN, stages, cstore;
   const void* add;
   void* C;
@@ -80,7 +82,8 @@ __device__ __forceinline__ uint32_t idesc_mxf4(int M, int N, uint32_t sf) {
          (uint32_t(M >> 4) << 24) | (sf << 29);
 }
 
-template <typename TO, int MH>
+// kRows: C is [M][N] (tokens on the M side), else [N][M].
+template <typename TO, int MH, bool kRows>
 __global__ void __launch_bounds__(F_THREADS, 1)
     k_mx_matmul(const __grid_constant__ MmMaps maps, const MmArgs g) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -92,7 +95,10 @@ __global__ void __launch_bounds__(F_THREADS, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ntn = (g.N + g.BN - 1) / g.BN;
-  const int i0 = (blockIdx.x / ntn) * (128 * MH), j0 = (blockIdx.x % ntn) * g.BN;
+  // the tokens run fastest: CTAs at work at the same time share the weights' tiles in L2
+  const int ntm = (g.M + 128 * MH - 1) / (128 * MH);
+  const int i0 = (kRows ? blockIdx.x % ntm : blockIdx.x / ntn) * (128 * MH);
+  const int j0 = (kRows ? blockIdx.x / ntm : blockIdx.x % ntn) * g.BN;
   constexpr int kM = MH * 128;
   const int kStage = kM * 128 + g.BN * 128;
   const int kScale = (kM + g.BN) * 16;
@@ -294,20 +300,59 @@ __global__ void __launch_bounds__(F_THREADS, 1)
         float v[32];
         tc::tmem_ld32(tb + c0, v);
         const int jn = min(32, min(g.BN - c0, g.N - j0 - c0));
-        const int64_t at = int64_t(j0 + c0) * g.M + i;
-        if (add && i < g.M) {
+        if (kRows) {
+          const int64_t at = int64_t(i) * g.N + j0 + c0;
+          if (add && i < g.M) {
+            if (jn == 32 && g.cstore && sizeof(TO) == 2) {
 #pragma unroll
-          for (int q = 0; q < 32; ++q)
-            if (q < jn) v[q] += VT<TO>::f(add[at + int64_t(q) * g.M]);
-        }
-        if (g.cstore) {
+              for (int q = 0; q < 4; ++q) {
+                const uint4 w = *reinterpret_cast<const uint4*>(add + at + q * 8);
+                v[8 * q] += bf_lo(w.x); v[8 * q + 1] += bf_hi(w.x);
+                v[8 * q + 2] += bf_lo(w.y); v[8 * q + 3] += bf_hi(w.y);
+                v[8 * q + 4] += bf_lo(w.z); v[8 * q + 5] += bf_hi(w.z);
+                v[8 * q + 6] += bf_lo(w.w); v[8 * q + 7] += bf_hi(w.w);
+              }
+            } else {
 #pragma unroll
-          for (int q = 0; q < 32; ++q)
-            if (c0 + q < g.BN) stg[(c0 + q) * kM + R] = __float2bfloat16_rn(v[q]);
-        } else if (i < g.M) {
+              for (int q = 0; q < 32; ++q)
+                if (q < jn) v[q] += VT<TO>::f(add[at + q]);
+            }
+          }
+          if (g.cstore) {
+            // 64-column tiles of 128 rows in the 128-byte swizzle
+            unsigned char* row = smem + ((R >> 7) * (g.BN >> 6) + (c >> 1)) * 16384 + (R & 127) * 128;
 #pragma unroll
-          for (int q = 0; q < 32; ++q)
-            if (q < jn) C[at + int64_t(q) * g.M] = VT<TO>::from_f(v[q]);
+            for (int q = 0; q < 4; ++q) {
+              uint32_t w[4];
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v[8 * q + 2 * z], v[8 * q + 2 * z + 1]);
+                w[z] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+              *reinterpret_cast<uint4*>(row + ((((c & 1) * 4 + q) ^ (R & 7)) << 4)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else if (i < g.M) {
+#pragma unroll
+            for (int q = 0; q < 32; ++q)
+              if (q < jn) C[at + q] = VT<TO>::from_f(v[q]);
+          }
+        } else {
+          const int64_t at = int64_t(j0 + c0) * g.M + i;
+          if (add && i < g.M) {
+#pragma unroll
+            for (int q = 0; q < 32; ++q)
+              if (q < jn) v[q] += VT<TO>::f(add[at + int64_t(q) * g.M]);
+          }
+          if (g.cstore) {
+#pragma unroll
+            for (int q = 0; q < 32; ++q)
+              if (c0 + q < g.BN) stg[(c0 + q) * kM + R] = __float2bfloat16_rn(v[q]);
+          } else if (i < g.M) {
+#pragma unroll
+            for (int q = 0; q < 32; ++q)
+              if (q < jn) C[at + int64_t(q) * g.M] = VT<TO>::from_f(v[q]);
+          }
         }
       }
     } else {
@@ -317,7 +362,14 @@ __global__ void __launch_bounds__(F_THREADS, 1)
       tc::fence_async_smem();
       asm volatile("barrier.sync 1, 256;" ::: "memory");  // the eight epilogue warps, always
       if (tid == 0 && ok && !*abrt) {
-        tc::tma_store_2d(&maps.c, stg, i0, j0);
+        if (kRows) {
+          for (int h = 0; h < MH; ++h)
+            for (int q = 0; q < g.BN / 64; ++q)
+              if (i0 + h * 128 < g.M && j0 + q * 64 < g.N)
+                tc::tma_store_2d(&maps.c, smem + (h * (g.BN >> 6) + q) * 16384, j0 + q * 64, i0 + h * 128);
+        } else {
+          tc::tma_store_2d(&maps.c, stg, i0, j0);
+        }
         tc::bulk_commit();
         tc::bulk_wait_read_all();
       }
@@ -331,9 +383,9 @@ __global__ void __launch_bounds__(F_THREADS, 1)
   }
 }
 
-template <typename TO, int MH>
+template <typename TO, int MH, bool kRows>
 hsl_status launch_mm(const MmMaps& maps, const MmArgs& g, cudaStream_t s) {
-  void (*fn)(const MmMaps, const MmArgs) = k_mx_matmul<TO, MH>;
+  void (*fn)(const MmMaps, const MmArgs) = k_mx_matmul<TO, MH, kRows>;
   const int stage = (MH * 128 + g.BN) * 128, scale = (MH * 128 + g.BN) * 16;
   const int bytes = std::max(g.stages * stage + F_SRING * scale, MH * 128 * g.BN * 2) + 1024;
   if (cudaError_t e = allow_dyn_smem(reinterpret_cast<const void*>(fn), bytes))
@@ -350,46 +402,58 @@ bool mx_matmul_supported() { return tmap_available(); }
 
 hsl_status mx_matmul_run(const MxOperand& A, int64_t T, const MxOperand& B, int64_t m, int64_t n,
                          const void* add, void* Y, hsl_dtype dtype, cudaStream_t s) {
-  // Two accumulators of up to 192 columns where that still gives every SM a tile,
-  // else one of up to 256.
-  int64_t ntn = (T + 191) / 192;
+  const bool rows = T >= 256;
+  const MxOperand &ms = rows ? A : B, &ns = rows ? B : A;
+  const int64_t M = rows ? T : m, N = rows ? m : T;
+  const bool aligned = dtype == HSL_BF16 && m % 8 == 0 && reinterpret_cast<uintptr_t>(Y) % 16 == 0 &&
+                       (!add || reinterpret_cast<uintptr_t>(add) % 16 == 0);
+  // Two accumulators of up to 192 columns where that still gives every SM a tile, else one of up
+  // to 256.  Rows of C are stored in tiles of 64 columns.
   int mh = 2;
-  if ((m + 255) / 256 * ntn < 148) {
+  int64_t ntn = (N + 191) / 192;
+  if ((M + 255) / 256 * ntn < 148) {
     mh = 1;
-    ntn = (T + 255) / 256;
+    ntn = (N + 255) / 256;
+    // with few tiles, narrower ones for more SMs
+    if (rows) ntn = std::min((N + 63) / 64, std::max<int64_t>(ntn, 148 / ((M + 127) / 128)));
   }
   MmArgs g = {};
-  g.M = int(m);
-  g.N = int(T);
+  g.M = int(M);
+  g.N = int(N);
   g.nb = int(mx::blocks(n));
   g.nk = (g.nb + 7) / 8;
-  g.BN = int(round_up((T + ntn - 1) / ntn, 16));
-  const int rows = mh * 128 + g.BN;
+  g.BN = int(round_up((N + ntn - 1) / ntn, rows ? 64 : 16));
+  const int srows = mh * 128 + g.BN;
   const int sf_cols = mh * 8 + 2 * ((g.BN + 127) / 128 * 4);
-  g.stages = std::min(F_MAX_STAGES, (F_SMEM_BUDGET - F_SRING * rows * 16) / (rows * 128));
+  g.stages = std::min(F_MAX_STAGES, (F_SMEM_BUDGET - F_SRING * srows * 16) / (srows * 128));
   // the last column read of an accumulator may lie up to 16 past BN: inside the scales' columns
   g.stages = std::min(g.stages, (512 - mh * g.BN) / sf_cols);
   g.add = add;
   g.C = Y;
-  g.cstore = (dtype == HSL_BF16 && m % 8 == 0 && reinterpret_cast<uintptr_t>(Y) % 16 == 0) ? 1 : 0;
+  g.cstore = aligned ? 1 : 0;
   MmMaps maps;
   memset(&maps, 0, sizeof(maps));
   const auto U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const auto SW = CU_TENSOR_MAP_SWIZZLE_128B;
   const auto NO = CU_TENSOR_MAP_SWIZZLE_NONE;
-  bool ok = make_tmap_2d(&maps.b, U8, 1, B.p, m, B.pitch, B.pitch, 128, 128, SW) &&
-            make_tmap_2d(&maps.a, U8, 1, A.p, T, A.pitch, A.pitch, 128, g.BN, SW) &&
-            make_tmap_2d(&maps.bs, U8, 1, B.scales, m, B.spitch, B.spitch, 16, 128, NO) &&
-            make_tmap_2d(&maps.as, U8, 1, A.scales, T, A.spitch, A.spitch, 16, g.BN, NO);
+  bool ok = make_tmap_2d(&maps.b, U8, 1, ms.p, M, ms.pitch, ms.pitch, 128, 128, SW) &&
+            make_tmap_2d(&maps.a, U8, 1, ns.p, N, ns.pitch, ns.pitch, 128, g.BN, SW) &&
+            make_tmap_2d(&maps.bs, U8, 1, ms.scales, M, ms.spitch, ms.spitch, 16, 128, NO) &&
+            make_tmap_2d(&maps.as, U8, 1, ns.scales, N, ns.spitch, ns.spitch, 16, g.BN, NO);
   if (ok && g.cstore)
-    ok = make_tmap_2d(&maps.c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, Y, T, m, m, 128 * mh, g.BN, NO);
+    ok = rows ? make_tmap_2d(&maps.c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, Y, T, m, m, 64, 128, SW)
+              : make_tmap_2d(&maps.c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, Y, T, m, m, 128 * mh, g.BN, NO);
   if (!ok) {
     set_message("tensor map encoding failed");
     return HSL_ERR_CUDA;
   }
-  if (dtype == HSL_F32)
-    return mh == 2 ? launch_mm<float, 2>(maps, g, s) : launch_mm<float, 1>(maps, g, s);
-  return mh == 2 ? launch_mm<__nv_bfloat16, 2>(maps, g, s) : launch_mm<__nv_bfloat16, 1>(maps, g, s);
+  if (dtype == HSL_F32) {
+    if (rows) return mh == 2 ? launch_mm<float, 2, true>(maps, g, s) : launch_mm<float, 1, true>(maps, g, s);
+    return mh == 2 ? launch_mm<float, 2, false>(maps, g, s) : launch_mm<float, 1, false>(maps, g, s);
+  }
+  using bf = __nv_bfloat16;
+  if (rows) return mh == 2 ? launch_mm<bf, 2, true>(maps, g, s) : launch_mm<bf, 1, true>(maps, g, s);
+  return mh == 2 ? launch_mm<bf, 2, false>(maps, g, s) : launch_mm<bf, 1, false>(maps, g, s);
 }
 
 cudaError_t mx_matmul_error_word(uint32_t** p) {
