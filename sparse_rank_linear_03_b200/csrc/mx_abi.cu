@@ -68,7 +68,7 @@ size_t workspace_bytes(hsl_mx_op op, int64_t T, int64_t m, int64_t n, int64_t r,
   const size_t simt = op == HSL_MX_OP_FACTOR_GRAD ? size_t(2 * T * r * 4) : 0;
   if (dt == HSL_F32 || T == 0 || m == 0) return simt;
   size_t tc = 0;
-  if (op == HSL_MX_OP_APPLY && mx_decode_fits(T, m, n)) return 0;
+  if (op == HSL_MX_OP_APPLY && mx_decode_fits(T, m, n)) return mx_decode_workspace(T, n);
   if (op == HSL_MX_OP_APPLY || op == HSL_MX_OP_APPLY_T)
     tc = mx_gemm_apply_workspace(op == HSL_MX_OP_APPLY_T, T, m, n);
   if (op == HSL_MX_OP_FACTOR_GRAD && r > 0) tc = mx_gemm_grad_workspace(T, m, n, r);
@@ -147,7 +147,7 @@ hsl_status hsl_mx4_apply(const hsl_mx* D, const void* X, const void* add, void* 
     return e;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == HSL_BF16 && mx_decode_fits(batch, D->rows, D->cols))
-    return mx_decode_run(operand(D, false), D->rows, D->cols, X, add, Y, batch, s);
+    return mx_decode_run(operand(D, false), D->rows, D->cols, X, add, Y, batch, ws, s);
   if (dtype == HSL_BF16 && mx_gemm_supported(X))
     return mx_gemm_apply_run(false, operand(D, false), D->rows, D->cols, X, add, Y, batch, ws, s);
   if (dtype == HSL_F32 && batch <= kMxDecodeF32Max)

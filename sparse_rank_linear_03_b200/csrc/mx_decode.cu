@@ -7,7 +7,7 @@
 // does takes about half an integer instruction:
 //
 //   cvt turns two codes into two fp16 values, which mma.sync (m16n8k16, fp32 sums)
-//   multiplies with the tokens, 16 rows of D × 8 columns.  Each block has its own
+//   multiplies with the tokens, 16 rows of D × 8 or 16 columns.  Each block has its own
 //   MMAs, and its scale multiplies their 4 sums per lane (fp32 FMA).
 //
 //   The tokens become fp16 without losing a bit: a token's values are sorted into
@@ -15,7 +15,9 @@
 //   power of two, is a column of its own (8 significant bits over 32 binades end at
 //   2^−23, fp16 reaches 2^−24).  Activations fit one window nearly always; there is room
 //   for two columns per token up to 4 tokens, and what does not fit takes
-//   another pass over D.  At the end each column is scaled back.  Infinities
+//   another pass over D.  A kernel of its own makes the columns (k_mx_tokens; every CTA doing it
+//   for itself took 4 to 10 µs), while the main kernel's first copies of D are already
+//   under way.  At the end each column is scaled back.  Infinities
 //   and NaN go to the first window as they are.  Block scales enter as 2^(e − 142), so
 //   that a column's sums lie as if its largest value were about 1.
 //
@@ -89,12 +91,13 @@ struct DcMaps {
   CUtensorMap s;   // scales: box {128, 16·tps}
 };
 struct DcArgs {
-  const __nv_bfloat16* X;
+  const int2* tokens;   // per token: largest exponent field, windows
+  const uint4* columns;  // [window][token][cpieces] pieces of eight fp16
   const __nv_bfloat16* add;
   __nv_bfloat16* Y;
-  int m, n, nb, T;
-  int vec;     // rows of X start on 16 bytes
+  int m, nb, T;
   int wcols;   // columns per token, at most
+  int cpieces;  // pieces per column in global memory
   int slice;   // units of K whose columns are in shared memory at a time
   int su;      // units per stage and row tile
   int tps;     // row tiles per stage
@@ -107,24 +110,54 @@ struct DcArgs {
 // chunk c ^ (r & 7), so that the eight rows of a warp's access lie in different banks.
 __host__ __device__ constexpr int dc_stage_bytes(int su, int rows) { return (su + 1) * rows * 128; }
 
-// 16-byte piece c (eight values) of a column in shared memory: the eight lanes of an access
-// (two columns × four neighbouring pieces) meet eight different bank groups.
-__device__ __forceinline__ int xs_at(int col, int c, int pieces) { return col * pieces + (c ^ ((col & 1) << 2)); }
+// A column's 16-byte pieces (eight values each) in shared memory: 64 bytes between columns, so
+// that the eight lanes of an access (two columns × four neighbouring pieces) meet
+// eight different bank groups.
+__host__ __device__ constexpr int dc_col_pitch(int slice) { return slice * (DC_UNIT / 8) + 4; }
 
-__device__ __forceinline__ uint4 load_piece(const DcArgs& a, int tok, int col) {
+// Eight values of a token, zeros past n.
+__device__ __forceinline__ uint4 load_piece(const __nv_bfloat16* x, int col, int n, int vec) {
   uint4 v = make_uint4(0, 0, 0, 0);
-  const __nv_bfloat16* p = a.X + int64_t(tok) * a.n + col;
-  if (a.vec && col + 8 <= a.n) {
+  const __nv_bfloat16* p = x + col;
+  if (vec && col + 8 <= n) {
     v = __ldg(reinterpret_cast<const uint4*>(p));
   } else {
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (col + j < a.n)
+      if (col + j < n)
         w[j >> 1] |= uint32_t(__ldg(reinterpret_cast<const uint16_t*>(p) + j)) << ((j & 1) * 16);
     v = make_uint4(w[0], w[1], w[2], w[3]);
   }
   return v;
+}
+// Largest and smallest exponent field of a piece's finite values that are not zero (-1 and 255 if
+// there is none), two values at a time.
+__device__ __forceinline__ void exponents(const uint4& v, int& hi, int& lo) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t h = 0, l = 0xFFFFFFFFu;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t m = w[j] & 0x7FFF7FFFu;
+    h = __vmaxu2(h, m);
+    l = __vminu2(l, ((m | 0x80008000u) - 0x00010001u) ^ 0x80008000u);  // m − 1; a zero is the largest
+  }
+  const uint32_t top = max(h >> 16, h & 0xFFFFu), low = min(l >> 16, l & 0xFFFFu);
+  hi = -1;
+  lo = 255;
+  if (top >= 0x7F80u) {  // an infinity or a NaN among them
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t bits = (w[j >> 1] >> ((j & 1) * 16)) & 0x7FFFu;
+      if (bits != 0 && bits < 0x7F80u) {
+        hi = max(hi, int(bits >> 7));
+        lo = min(lo, int(bits >> 7));
+      }
+    }
+  } else if (top != 0) {
+    hi = int(top >> 7);
+    lo = int((low + 1) >> 7);
+  }
 }
 // The values of a piece that belong to window `win` of a token whose largest exponent field is
 // `top`, scaled by 2^(142 − top + 32 win) to fp16; zeros elsewhere.
@@ -152,6 +185,63 @@ __device__ __forceinline__ uint4 window_piece(const uint4& v, int top, int win, 
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// A CTA per token: its exponents, then its windows as columns of fp16 (in global memory).
+constexpr int DC_TOKEN_THREADS = 512;
+constexpr int DC_TOKEN_KEEP = 4;  // pieces that a thread keeps in registers from the first pass
+__global__ void __launch_bounds__(DC_TOKEN_THREADS)
+    k_mx_tokens(const __nv_bfloat16* __restrict__ X, int n, int vec, int pieces, int2* __restrict__ tokens,
+                uint4* __restrict__ columns) {
+  pdl_trigger();  // the product's copies of D need not wait
+  __shared__ int red[2][DC_TOKEN_THREADS / 32];
+  const int tok = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const __nv_bfloat16* x = X + int64_t(tok) * n;
+  uint4 kept[DC_TOKEN_KEEP];
+  int hi = -1, lo = 255;
+#pragma unroll
+  for (int k = 0; k < DC_TOKEN_KEEP; ++k) {
+    const int c = threadIdx.x + k * DC_TOKEN_THREADS;
+    kept[k] = c < pieces ? load_piece(x, c * 8, n, vec) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int k = 0; k < DC_TOKEN_KEEP; ++k) {
+    int h, l;
+    exponents(kept[k], h, l);
+    hi = max(hi, h);
+    lo = min(lo, l);
+  }
+  for (int c = threadIdx.x + DC_TOKEN_KEEP * DC_TOKEN_THREADS; c < pieces; c += DC_TOKEN_THREADS) {
+    int h, l;
+    exponents(load_piece(x, c * 8, n, vec), h, l);
+    hi = max(hi, h);
+    lo = min(lo, l);
+  }
+  hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+  lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+  if (lane == 0) {
+    red[0][warp] = hi;
+    red[1][warp] = lo;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < DC_TOKEN_THREADS / 32; ++w) {
+    hi = max(hi, red[0][w]);
+    lo = min(lo, red[1][w]);
+  }
+  if (hi < 0) hi = lo = 127;  // nothing but zeros, infinities and NaN
+  const int windows = (hi - lo) / 32 + 1;
+  if (threadIdx.x == 0) tokens[tok] = make_int2(hi, windows);
+  for (int w = 0; w < windows; ++w) {
+    uint4* out = columns + (int64_t(w) * gridDim.x + tok) * pieces;
+#pragma unroll
+    for (int k = 0; k < DC_TOKEN_KEEP; ++k) {
+      const int c = threadIdx.x + k * DC_TOKEN_THREADS;
+      if (c < pieces) out[c] = window_piece(kept[k], hi, w, windows == 1);
+    }
+    for (int c = threadIdx.x + DC_TOKEN_KEEP * DC_TOKEN_THREADS; c < pieces; c += DC_TOKEN_THREADS)
+      out[c] = window_piece(load_piece(x, c * 8, n, vec), hi, w, windows == 1);
+  }
+}
+
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
@@ -162,11 +252,13 @@ __device__ uint32_t g_mx_decode_err;
 
 constexpr int DC_MAX_STAGES = 8;
 constexpr int DC_THREADS = (DC_WARPS + 1) * 32;
-// Room for the warps' sums: of two row tiles with 8 columns, of more with fewer columns.
-constexpr int DC_RED = 2 * DC_WARPS * 16 * 8 * 4;
+// Room for the warps' sums: of one row tile with 16 columns, of more with fewer columns.
+constexpr int DC_RED_PITCH = 20;  // a column's 16 rows, spread over the banks
+constexpr int DC_RED = DC_WARPS * 16 * DC_RED_PITCH * 4;
 
 __device__ __forceinline__ void dc_sync() { asm volatile("barrier.sync 1, 512;" ::: "memory"); }  // the 16 warps
 
+template <int NT>
 __global__ void __launch_bounds__(DC_THREADS, 1)
     k_mx_decode(const __grid_constant__ DcMaps maps, const DcArgs a) {
   constexpr int kRows = 16;
@@ -174,9 +266,12 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   // (an offset, not a rounded integer: the compiler still knows that this is shared memory)
   unsigned char* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ uint64_t full[DC_MAX_STAGES], empty[DC_MAX_STAGES];
-  __shared__ int abort_flag, emax[8], emin[8];
-  float* red = reinterpret_cast<float*>(smem);  // [slot][DC_WARPS][kRows][columns]
-  const int pieces = a.slice * (DC_UNIT / 8);
+  __shared__ uint64_t xfull;
+  __shared__ int abort_flag;
+  __shared__ int2 token[16];
+  __shared__ float unscale[2][16];  // per column: 2^k in two factors
+  float* red = reinterpret_cast<float*>(smem);  // [slot][DC_WARPS][columns][DC_RED_PITCH]
+  const int pieces = a.slice * (DC_UNIT / 8), cpitch = dc_col_pitch(a.slice);
   uint4* xs = reinterpret_cast<uint4*>(smem + DC_RED);
   unsigned char* ring = smem + a.ring;
   float* ysum = reinterpret_cast<float*>(smem + a.ysum);  // [row tile of this CTA][token][kRows]
@@ -193,6 +288,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       tc::mbar_init(&full[i], 1);
       tc::mbar_init(&empty[i], DC_WARPS);
     }
+    tc::mbar_init(&xfull, 1);
     tc::fence_mbar_init();
   }
   __syncthreads();
@@ -246,9 +342,8 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
           __syncthreads();
         }
         if (pass == 0)
-          for (int t = 0; t < a.T; ++t) passes = max(passes, ((emax[t] - emin[t]) / 32 + a.wcols) / a.wcols);
+          for (int t = 0; t < a.T; ++t) passes = max(passes, (token[t].y + a.wcols - 1) / a.wcols);
       }
-      __syncthreads();  // (the exponents may be written again)
     }
     if (lane == 0 && *abrt)
       for (int q = 0; q < a.stages && q < issued; ++q)  // copies in flight land first
@@ -260,67 +355,59 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   // this warp's row tile within a stage and its unit there
   const int sub = warp / a.su, my = warp - sub * a.su;
   int s = 0;
-  uint32_t ph = 0;
+  uint32_t ph = 0, round = 0;  // round: passes over D so far
   for (int u0 = 0; u0 < units; u0 += a.slice) {
     const int uend = min(u0 + a.slice, units);
-    // the tokens' largest and smallest exponent fields (of finite values that are not zero)
-    if (threadIdx.x < a.T) {
-      emax[threadIdx.x] = -1;
-      emin[threadIdx.x] = 255;
+    if (u0 == 0) {
+      pdl_wait();  // the columns are written
+      if (threadIdx.x < a.T) token[threadIdx.x] = __ldcg(a.tokens + threadIdx.x);
     }
-    dc_sync();  // (and the columns of the last slice are read)
-    for (int e = threadIdx.x; e < a.T * pieces; e += DC_WARPS * 32) {
-      const int tok = e / pieces, c = e - tok * pieces;  // one token per warp: pieces % 32 == 0
-      const uint4 v = load_piece(a, tok, u0 * DC_UNIT + c * 8);
-      xs[xs_at(tok, c, pieces)] = v;  // as it is; one column per token replaces it in place
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      int hi = -1, lo = 255;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t bits = (w[j >> 1] >> ((j & 1) * 16)) & 0x7FFFu;
-        const int b = int(bits >> 7);
-        if (bits != 0 && b != 255) {
-          hi = max(hi, b);
-          lo = min(lo, b);
-        }
-      }
-      hi = __reduce_max_sync(0xFFFFFFFFu, hi);
-      lo = __reduce_min_sync(0xFFFFFFFFu, lo);
-      if (lane == 0 && hi >= 0) {
-        atomicMax(&emax[tok], hi);
-        atomicMin(&emin[tok], lo);
-      }
-    }
-    dc_sync();
-    if (threadIdx.x < a.T && emax[threadIdx.x] < 0) emax[threadIdx.x] = emin[threadIdx.x] = 127;
     __syncthreads();
     int windows = 1;
-    for (int k = 0; k < a.T; ++k) windows = max(windows, (emax[k] - emin[k]) / 32 + 1);
+    for (int k = 0; k < a.T; ++k) windows = max(windows, token[k].y);
     const int per_tok = min(windows, a.wcols), cols = a.T * per_tok;
     const int passes = (windows + a.wcols - 1) / a.wcols;
 
-    for (int pass = 0; pass < passes; ++pass) {
-      if (pass || per_tok > 1) dc_sync();  // the last pass's columns, or the tokens, are read
-      for (int e = threadIdx.x; e < cols * pieces; e += DC_WARPS * 32) {
-        const int col = e / pieces, c = e - col * pieces;
-        const int tok = col / per_tok, win = pass * a.wcols + col - tok * per_tok;
-        uint4* x = &xs[xs_at(col, c, pieces)];
-        // (the same thread wrote the same piece when one column per token is kept)
-        const uint4 v = passes == 1 && per_tok == 1 ? *x : load_piece(a, tok, u0 * DC_UNIT + c * 8);
-        *x = window_piece(v, emax[tok], win, windows == 1);
+    for (int pass = 0; pass < passes; ++pass, ++round) {
+      tc::fence_async_smem();
+      dc_sync();  // the last round's columns are read
+      if (threadIdx.x == 0) {
+        const int have = min(pieces, a.cpieces - u0 * (DC_UNIT / 8));  // the last slice may be shorter
+        int count = 0;
+        for (int c = 0; c < cols; ++c) count += pass * a.wcols + c % per_tok < token[c / per_tok].y;
+        tc::mbar_expect_tx(&xfull, uint32_t(count * have * 16));
+        for (int c = 0; c < cols; ++c) {
+          const int tok = c / per_tok, win = pass * a.wcols + c % per_tok;
+          if (win < token[tok].y)
+            tc::bulk_load(xs + c * cpitch, a.columns + (int64_t(win) * a.T + tok) * a.cpieces + u0 * (DC_UNIT / 8),
+                          uint32_t(have * 16), &xfull);
+        }
       }
+      if (threadIdx.x < cols) {
+        const int tok = threadIdx.x / per_tok;
+        const int k = token[tok].x - 127 - 32 * (pass * a.wcols + int(threadIdx.x) % per_tok);
+        // (a column past the token's windows is all zeros: any factor will do)
+        const int k0 = max(k, -252) / 2, k1 = max(k, -252) - k0;
+        unscale[0][threadIdx.x] = __uint_as_float(uint32_t(127 + k0) << 23);
+        unscale[1][threadIdx.x] = __uint_as_float(uint32_t(127 + k1) << 23);
+      }
+      for (int c = 0; c < cols; ++c)  // windows that a token does not have
+        if (pass * a.wcols + c % per_tok >= token[c / per_tok].y)
+          for (int e = threadIdx.x; e < pieces; e += DC_WARPS * 32) xs[c * cpitch + e] = make_uint4(0, 0, 0, 0);
+      if (!tc::mbar_wait(&xfull, round & 1, &g_mx_decode_err)) *abrt = 1;
       dc_sync();
       const bool first = u0 == 0 && pass == 0, last = uend == units && pass == passes - 1;
       // The warps' sums of several row tiles are kept before they are added up together: a
       // meeting of the warps per tile costs more than the tile's copies.
-      const int slots = DC_RED / (DC_WARPS * kRows * 4 * cols);
+      const int slots = DC_RED / (DC_WARPS * DC_RED_PITCH * 4 * cols);
       int slot = 0, local = 0;
-      // Column g (or any other, where there are fewer: those sums are not used) at this lane's
-      // words; pieces of odd columns are swapped in fours.
-      const int mycol = min(g, cols - 1), flip = (mycol & 1) * 4;
-      const uint4* xb = xs + mycol * pieces + t;
+      // Columns g, 8 + g at this lane's words (the last column where there are fewer: those sums
+      // are not used)
+      const uint4* xb[NT];
+#pragma unroll
+      for (int q = 0; q < NT; ++q) xb[q] = xs + min(q * 8 + g, cols - 1) * cpitch + t;
       for (int grp = blockIdx.x; grp < groups; grp += gridDim.x) {
-        float acc[4] = {};
+        float acc[NT][4] = {};
         for (int u = u0; u < uend; u += a.su) {
           const bool got = tc::mbar_try(&full[s], ph) ||
                            (!*abrt && tc::mbar_wait(&full[s], ph, &g_mx_decode_err));
@@ -350,21 +437,23 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
             widen_scales(e0.y, s0 + 4);
             widen_scales(e1.x, s1);
             widen_scales(e1.y, s1 + 4);
-            const uint4* xe = xb + (unit - u0) * 32 + flip;
-            const uint4* xo = xb + (unit - u0) * 32 - flip;
+            const int xu = (unit - u0) * 32;
 #pragma unroll
             for (int b = 0; b < 8; ++b) {
               uint32_t v0[4], v1[4];
               widen_word(w0[b], v0);
               widen_word(w1[b], v1);
-              const uint4 x = (b & 1) ? xo[b * 4] : xe[b * 4];
-              float c[4] = {0.f, 0.f, 0.f, 0.f};
-              mma16816(c, v0[0], v1[0], v0[1], v1[1], x.x, x.y);
-              mma16816(c, v0[2], v1[2], v0[3], v1[3], x.z, x.w);
-              acc[0] = fmaf(s0[b], c[0], acc[0]);
-              acc[1] = fmaf(s0[b], c[1], acc[1]);
-              acc[2] = fmaf(s1[b], c[2], acc[2]);
-              acc[3] = fmaf(s1[b], c[3], acc[3]);
+#pragma unroll
+              for (int q = 0; q < NT; ++q) {
+                const uint4 x = xb[q][xu + b * 4];
+                float c[4] = {0.f, 0.f, 0.f, 0.f};
+                mma16816(c, v0[0], v1[0], v0[1], v1[1], x.x, x.y);
+                mma16816(c, v0[2], v1[2], v0[3], v1[3], x.z, x.w);
+                acc[q][0] = fmaf(s0[b], c[0], acc[q][0]);
+                acc[q][1] = fmaf(s0[b], c[1], acc[q][1]);
+                acc[q][2] = fmaf(s1[b], c[2], acc[q][2]);
+                acc[q][3] = fmaf(s1[b], c[3], acc[q][3]);
+              }
             }
           }
           __syncwarp();
@@ -374,29 +463,32 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
             ph ^= 1;
           }
         }
-        float* out = red + ((slot * DC_WARPS + warp) * kRows + g) * cols;
+        float* out = red + (slot * DC_WARPS + warp) * cols * DC_RED_PITCH + g;
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-          if (2 * t + q < cols) {
-            out[2 * t + q] = acc[q];
-            out[8 * cols + 2 * t + q] = acc[2 + q];
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int col = n * 8 + 2 * t + q;
+            if (col < cols) {
+              out[col * DC_RED_PITCH] = acc[n][q];
+              out[col * DC_RED_PITCH + 8] = acc[n][2 + q];
+            }
           }
         ++slot;
         if (slot < slots && grp + int(gridDim.x) < groups) continue;
         dc_sync();
-        const int per = kRows * a.T, per_grp = per * a.tps;
-        for (int e = threadIdx.x; e < per_grp * slot; e += DC_WARPS * 32) {
-          const int q = e / per_grp, ts = (e - q * per_grp) / per, rest = e - q * per_grp - ts * per;
-          const int i = rest % kRows, tok = rest / kRows;
+        for (int e = threadIdx.x; e < kRows * a.T * a.tps * slot; e += DC_WARPS * 32) {
+          const int i = e & 15, tile = (e >> 4) / a.T, tok = (e >> 4) - tile * a.T;
+          const int q = a.tps == 1 ? tile : tile / a.tps, ts = tile - q * a.tps;
           const int row = ((grp - (slot - 1 - q) * int(gridDim.x)) * a.tps + ts) * kRows + i;
           if (row >= a.m) continue;
-          const float* p = red + ((q * DC_WARPS + ts * a.su) * kRows + i) * cols + tok * per_tok;
+          const float* p = red + ((q * DC_WARPS + ts * a.su) * cols + tok * per_tok) * DC_RED_PITCH + i;
           float v = 0.f;
           for (int c = per_tok - 1; c >= 0; --c) {
-            float col = p[c];
+            float col = p[c * DC_RED_PITCH];
 #pragma unroll 4
-            for (int w = 1; w < a.su; ++w) col += p[w * kRows * cols + c];
-            v += ldexpf(col, emax[tok] - 127 - 32 * (pass * a.wcols + c));
+            for (int w = 1; w < a.su; ++w) col += p[(w * cols + c) * DC_RED_PITCH];
+            v += col * unscale[0][tok * per_tok + c] * unscale[1][tok * per_tok + c];
           }
           float* keep = ysum + ((int64_t(local + q) * a.tps + ts) * a.T + tok) * kRows + i;
           if (!first) v += *keep;
@@ -413,7 +505,6 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         slot = 0;
       }
     }
-    __syncthreads();
   }
 }
 
@@ -497,7 +588,7 @@ struct DcPlan {
 };
 DcPlan decode_plan(int64_t T, int64_t m, int64_t n) {
   DcPlan p = {};
-  p.wcols = 2 * T <= 8 ? 2 : 1;
+  p.wcols = T <= 4 ? 2 : 1;
   const int rows = 16;
   const int units = int((mx::blocks(n) + 7) / 8);
   const int64_t tiles = (m + rows - 1) / rows;
@@ -513,7 +604,7 @@ DcPlan decode_plan(int64_t T, int64_t m, int64_t n) {
     const int64_t groups = (tiles + p.tps - 1) / p.tps;
     p.grid = int(std::min<int64_t>(groups, 148));
     const int64_t ysum = (groups + p.grid - 1) / p.grid * p.tps * T * rows * 4;
-    const int64_t xs = T * p.wcols * p.slice * (DC_UNIT * 2);
+    const int64_t xs = T * p.wcols * dc_col_pitch(p.slice) * 16;
     const int stage = dc_stage_bytes(p.su, p.tps * rows);
     const int64_t left = DC_SMEM_MAX - round_up(red + xs, 1024) - ysum;
     if (left < 2 * stage) continue;
@@ -533,8 +624,14 @@ bool mx_decode_fits(int64_t T, int64_t m, int64_t n) {
   return T <= kMxDecodeMax && tmap_available() && decode_plan(T, m, n).stages >= 2;
 }
 
+// The workspace: per token its exponent and windows (256 bytes), then its columns: eight windows hold every
+// bf16 value.
+size_t mx_decode_workspace(int64_t T, int64_t n) {
+  return size_t(256 + 8 * T * ((mx::blocks(n) + 7) / 8) * DC_UNIT * 2);
+}
+
 hsl_status mx_decode_run(const MxOperand& D, int64_t m, int64_t n, const void* X, const void* add, void* Y,
-                         int64_t T, cudaStream_t s) {
+                         int64_t T, void* ws, cudaStream_t s) {
   const DcPlan p = decode_plan(T, m, n);
   DcArgs a;
   DcMaps maps;
@@ -549,14 +646,14 @@ hsl_status mx_decode_run(const MxOperand& D, int64_t m, int64_t n, const void* X
     set_message("tensor map encoding failed");
     return HSL_ERR_CUDA;
   }
-  a.X = static_cast<const __nv_bfloat16*>(X);
+  a.tokens = static_cast<const int2*>(ws);
+  a.columns = reinterpret_cast<const uint4*>(static_cast<const char*>(ws) + 256);
+  a.cpieces = int((mx::blocks(n) + 7) / 8) * (DC_UNIT / 8);
   a.add = static_cast<const __nv_bfloat16*>(add);
   a.Y = static_cast<__nv_bfloat16*>(Y);
   a.m = int(m);
-  a.n = int(n);
   a.nb = int(mx::blocks(n));
   a.T = int(T);
-  a.vec = n % 8 == 0 && reinterpret_cast<uintptr_t>(X) % 16 == 0 ? 1 : 0;
   a.wcols = p.wcols;
   a.ring = p.ring;
   a.slice = p.slice;
@@ -564,11 +661,26 @@ hsl_status mx_decode_run(const MxOperand& D, int64_t m, int64_t n, const void* X
   a.tps = p.tps;
   a.stages = p.stages;
   a.ysum = p.ysum;
-  if (cudaError_t e = allow_dyn_smem(reinterpret_cast<const void*>(k_mx_decode), p.bytes))
+  void (*fn)(const DcMaps, const DcArgs) = T <= 8 ? k_mx_decode<1> : k_mx_decode<2>;
+  if (cudaError_t e = allow_dyn_smem(reinterpret_cast<const void*>(fn), p.bytes))
     return cuda_fail(e, "4-bit decode smem attribute");
-  note_launch();
-  k_mx_decode<<<unsigned(p.grid), DC_THREADS, size_t(p.bytes), s>>>(maps, a);
-  return cuda_fail(cudaGetLastError(), "4-bit decode launch");
+  const int vec = n % 8 == 0 && reinterpret_cast<uintptr_t>(X) % 16 == 0 ? 1 : 0;
+  note_launch(2);
+  k_mx_tokens<<<unsigned(T), DC_TOKEN_THREADS, 0, s>>>(static_cast<const __nv_bfloat16*>(X), int(n), vec, a.cpieces,
+                                                       static_cast<int2*>(ws),
+                                                       reinterpret_cast<uint4*>(static_cast<char*>(ws) + 256));
+  if (hsl_status e = cuda_fail(cudaGetLastError(), "4-bit decode launch")) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(p.grid));
+  cfg.blockDim = dim3(DC_THREADS);
+  cfg.dynamicSmemBytes = size_t(p.bytes);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_fail(cudaLaunchKernelEx(&cfg, fn, maps, a), "4-bit decode launch");
 }
 
 cudaError_t mx_decode_error_word(uint32_t** p) {

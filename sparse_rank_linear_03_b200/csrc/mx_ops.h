@@ -53,11 +53,12 @@ hsl_status mx_gemm_grad_run(const MxOperand& X, int64_t T, int64_t n, const void
                             void* dX, void* ws, cudaStream_t s);
 cudaError_t mx_gemm_error_word(uint32_t** p);
 // A few tokens (mx_decode.cu), any alignment of X.  bf16: as many as mx_decode_fits says.
-constexpr int64_t kMxDecodeMax = 8, kMxDecodeF32Max = 64;
+constexpr int64_t kMxDecodeMax = 16, kMxDecodeF32Max = 64;
 bool mx_decode_fits(int64_t T, int64_t m, int64_t n);
 cudaError_t mx_decode_error_word(uint32_t** p);
+size_t mx_decode_workspace(int64_t T, int64_t n);
 hsl_status mx_decode_run(const MxOperand& D, int64_t m, int64_t n, const void* X, const void* add, void* Y,
-                         int64_t T, cudaStream_t s);
+                         int64_t T, void* ws, cudaStream_t s);
 hsl_status mx_decode_f32_run(const MxOperand& D, int64_t m, int64_t n, const void* X, const void* add,
                              void* Y, int64_t T, cudaStream_t s);
 // Both factors in e2m1 blocks (mx_matmul.cu): Y[T][m] = A Bᵀ (+ add)
