@@ -64,6 +64,7 @@ struct GemmMaps {
   CUtensorMap b0;  // B: box {64, BN} (K-major) or {64, 64}
   CUtensorMap b1;  // low part
   CUtensorMap c;   // OUT_T: box {128·MH, BN}
+  CUtensorMap add; // like c
   CUtensorMap q;   // codes: box {CodeTile::kInner bytes, CodeTile::kRows}
   CUtensorMap qs;  // scales of [K][M] blocks: box {16 bytes, 64}
 };
@@ -75,6 +76,7 @@ struct GemmArgs {
   int BN, stages, splits;
   int codes;         // code tiles in flight
   int cstore;        // OUT_T: tiled store possible
+  int addt;          // OUT_T: add comes as a tile as well
   const __nv_bfloat16* add;
   __nv_bfloat16* C;
   float* part;       // [splits][N][M] or [splits][M][N]
@@ -165,7 +167,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   // (an offset, not a rounded integer: the compiler still knows that this is shared memory)
   unsigned char* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
-  __shared__ uint64_t full[G_MAX_STAGES], empty[G_MAX_STAGES], accf;
+  __shared__ uint64_t full[G_MAX_STAGES], empty[G_MAX_STAGES], accf, addf;
   __shared__ uint64_t raw[G_MAX_STAGES], taken[G_MAX_STAGES];  // code tile landed, read
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
@@ -196,8 +198,10 @@ __global__ void __launch_bounds__(G_THREADS, 1)
       tc::mbar_init(&taken[s], 8);
     }
     tc::mbar_init(&accf, 1);
+    tc::mbar_init(&addf, 1);
     tc::fence_mbar_init();
     tc::prefetch_tmap(&maps.b0);
+    if (OUT == OUT_T && g.addt) tc::tma_prefetch_2d(&maps.add, i0, j0);  // into L2 for the epilogue
   }
   if (warp == 1) {
     tc::tmem_alloc(&tmem_slot, cols);
@@ -382,8 +386,17 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     // epilogue: warp w reaches TMEM lanes 32 (w mod 4) onwards; the four groups of four
     // warps divide the accumulators and their columns
     __syncwarp();
-    const bool ok = tc::mbar_wait(&accf, 0, &g_mx_gemm_err) && !*abrt;
+    bool ok = tc::mbar_wait(&accf, 0, &g_mx_gemm_err) && !*abrt;
     __nv_bfloat16* stg = reinterpret_cast<__nv_bfloat16*>(smem);
+    if (OUT == OUT_T && g.addt && ok) {
+      // the tile of add into the idle ring, where each value is replaced by the result (loads of
+      // single values from global memory took five times as long as the product)
+      if (threadIdx.x == 64) {
+        tc::mbar_expect_tx(&addf, uint32_t(128 * MH * g.BN * 2));
+        tc::tma_load_2d(stg, &maps.add, i0, j0, &addf);
+      }
+      ok = tc::mbar_wait(&addf, 0, &g_mx_gemm_err);
+    }
     if (ok) {
       tc::tc_fence_after();
       const int grp = (warp - 2) >> 2;
@@ -416,7 +429,11 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 if (q < jn) p[int64_t(q) * g.M] = v[q];
             }
           } else {
-            if (g.add && i < g.M) {
+            if (g.addt) {
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                if (c0 + q < g.BN) v[q] += __bfloat162float(stg[(c0 + q) * (128 * MH) + R]);
+            } else if (g.add && i < g.M) {
               const __nv_bfloat16* p = g.add + int64_t(j0 + c0) * g.M + i;
 #pragma unroll
               for (int q = 0; q < 32; ++q)
@@ -491,30 +508,64 @@ __global__ void __launch_bounds__(G_THREADS, 1)
 }
 
 // Σ over the splits' partials in split order, then add and round: to bf16, or to a bf16 pair
-// (hi + lo carries 16 significant bits) whose rows are padded to `pitch` with zeros.
+// (hi + lo carries 16 significant bits) whose rows are padded to `pitch` with zeros.  Four
+// values per thread where rows and pointers allow it (V = 4), else one.
+template <int V>
+__device__ __forceinline__ void sum_splits(const float* part, int splits, int64_t stride, int64_t at, float (&v)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; ++j) v[j] = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const float* p = part + int64_t(s) * stride + at;
+    if (V == 4) {
+      const float4 q = __ldcs(reinterpret_cast<const float4*>(p));
+      v[0] += q.x; v[1 % V] += q.y; v[2 % V] += q.z; v[3 % V] += q.w;
+    } else {
+      v[0] += p[0];
+    }
+  }
+}
+template <int V>
+__device__ __forceinline__ void store_bf(__nv_bfloat16* p, const float (&v)[V]) {
+  if (V == 4) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1 % V]), b = __floats2bfloat162_rn(v[2 % V], v[3 % V]);
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  } else {
+    p[0] = __float2bfloat16_rn(v[0]);
+  }
+}
+template <int V>
 __global__ void __launch_bounds__(256)
     k_mx_reduce(const float* __restrict__ part, int splits, int64_t count, const __nv_bfloat16* add,
                 __nv_bfloat16* C) {
-  const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t e = (int64_t(blockIdx.x) * 256 + threadIdx.x) * V;
   if (e >= count) return;
-  float v = part[e];
-  for (int s = 1; s < splits; ++s) v += part[int64_t(s) * count + e];
-  if (add) v += __bfloat162float(add[e]);
-  C[e] = __float2bfloat16_rn(v);
+  float v[V];
+  sum_splits<V>(part, splits, count, e, v);
+  if (add) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] += __bfloat162float(add[e + j]);
+  }
+  store_bf<V>(C + e, v);
 }
+template <int V>
 __global__ void __launch_bounds__(256)
     k_mx_reduce_pair(const float* __restrict__ part, int splits, int64_t rows, int n, int pitch,
                      __nv_bfloat16* __restrict__ hi, __nv_bfloat16* __restrict__ lo) {
-  const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t e = (int64_t(blockIdx.x) * 256 + threadIdx.x) * V;
   if (e >= rows * pitch) return;
   const int64_t row = e / pitch;
   const int c = int(e - row * pitch);
-  float v = 0.f;
-  if (c < n)
-    for (int s = 0; s < splits; ++s) v += part[(int64_t(s) * rows + row) * n + c];
-  const __nv_bfloat16 h = __float2bfloat16_rn(v);
-  hi[e] = h;
-  lo[e] = __float2bfloat16_rn(v - __bfloat162float(h));
+  float v[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) v[j] = 0.f;
+  if (c < n) sum_splits<V>(part, splits, rows * n, row * n + c, v);  // (V = 4: n = pitch)
+  float low[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) low[j] = v[j] - __bfloat162float(__float2bfloat16_rn(v[j]));
+  store_bf<V>(hi + e, v);
+  store_bf<V>(lo + e, low);
 }
 // Rows of n bf16 to rows of `pitch` (a multiple of 8, so that a tile copy can read them).
 __global__ void __launch_bounds__(256)
@@ -550,9 +601,10 @@ GemmShape shape_of(int ak, int64_t M, int64_t N, int64_t K, bool bmn, int terms,
   // 160 columns costs the widening, not the MMAs).  2048 tokens × 11008 rows: 208
   // columns (2.9 rounds) against 256 (2.3 rounds, the third mostly idle).
   int64_t ntn = (N + 255) / 256;
-  const int64_t t2 = (M + 255) / 256;
-  s.MH = t2 * ntn >= 148 ? 2 : 1;
-  if (s.MH == 2) {
+  const int64_t t2 = (M + 255) / 256, t1 = (M + 127) / 128, nk = (K + 63) / 64;
+  s.splits = 1;
+  if (t2 * ntn >= 148) {
+    s.MH = 2;
     int64_t best = INT64_MAX, at = ntn;
     for (int64_t c = ntn; c <= 2 * ntn; ++c) {
       const int64_t bn = round_up((N + c - 1) / c, 16);
@@ -565,11 +617,25 @@ GemmShape shape_of(int ak, int64_t M, int64_t N, int64_t K, bool bmn, int terms,
     ntn = at;
   }
   s.BN = int(round_up((N + ntn - 1) / ntn, 16));
-  const int64_t tiles = s.MH == 2 ? t2 * ntn : (M + 127) / 128 * ntn;
-  const int64_t nk = (K + 63) / 64;
-  s.splits = 1;
-  if (may_split && tiles < 148)
-    s.splits = int(std::max<int64_t>(1, std::min<int64_t>(148 / tiles, nk / 4)));
+  if (t2 * ntn < 148) {
+    // Fewer tiles than SMs: K is split where the caller has room for partial sums.  Cycles per
+    // K-block as measured: widening 256 rows 1040, 128 rows 720 (its chain of waits does
+    // not shrink with the rows); copies and MMAs 5 per column and accumulator pair, 3 for one.
+    // The partial sums pass through HBM twice, at about 3500 bytes per cycle.
+    const bool blocks = a_is_blocks(ak);
+    auto cost = [&](int mh, int64_t* splits) {
+      const int64_t tiles = (mh == 2 ? t2 : t1) * ntn;
+      *splits = may_split ? std::max<int64_t>(1, std::min<int64_t>(148 / tiles, nk / 4)) : 1;
+      const int64_t per = std::max<int64_t>(blocks ? (mh == 2 ? 1040 : 720) : 0,
+                                            int64_t(terms) * s.BN * (mh == 2 ? 5 : 3));
+      return (nk + *splits - 1) / *splits * per * ((tiles * *splits + 147) / 148) +
+             (*splits > 1 ? *splits * M * N * 8 / 3500 : 0);
+    };
+    int64_t s1 = 1, s2 = 1;
+    const int64_t c1 = cost(1, &s1), c2 = cost(2, &s2);
+    s.MH = c2 < c1 ? 2 : 1;
+    s.splits = int(s.MH == 2 ? s2 : s1);
+  }
   // Code tiles are small and come from farther away than anything else: four of them in
   // flight at least, then as many stages as fit (two at least: a pair of terms with an
   // 8-bit factor leaves room for them only with one accumulator), then more code tiles.
@@ -607,6 +673,14 @@ hsl_status launch_gemm(int mh, const GemmMaps& maps, const GemmArgs& g, cudaStre
 const auto kBF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
 const auto kSW = CU_TENSOR_MAP_SWIZZLE_128B;
 
+// The tiled store of C [T][M] and, where add allows it, the tiled load of add.
+bool out_maps(GemmMaps* maps, GemmArgs* g, int64_t T, int64_t M, int mh) {
+  g->cstore = (M % 8 == 0 && reinterpret_cast<uintptr_t>(g->C) % 16 == 0) ? 1 : 0;
+  g->addt = (g->cstore && g->add && reinterpret_cast<uintptr_t>(g->add) % 16 == 0) ? 1 : 0;
+  return (!g->cstore || make_tmap_2d(&maps->c, kBF, 2, g->C, T, M, M, 128 * mh, g->BN, CU_TENSOR_MAP_SWIZZLE_NONE)) &&
+         (!g->addt || make_tmap_2d(&maps->add, kBF, 2, g->add, T, M, M, 128 * mh, g->BN, CU_TENSOR_MAP_SWIZZLE_NONE));
+}
+
 // The tensor maps of a factor in blocks (stored rows × cols).
 bool block_maps(GemmMaps* maps, int ak, int mh, const MxOperand& o, int64_t rows) {
   const auto U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
@@ -634,6 +708,18 @@ hsl_status pad_rows(const void* src, int64_t rows, int64_t n, int64_t pitch, voi
   return cuda_fail(cudaGetLastError(), "row padding launch");
 }
 
+}  // namespace
+
+namespace {
+hsl_status reduce_run(const float* part, int splits, int64_t count, const __nv_bfloat16* add, __nv_bfloat16* C,
+                      cudaStream_t s) {
+  note_launch();
+  if (count % 4 == 0 && reinterpret_cast<uintptr_t>(C) % 8 == 0)
+    k_mx_reduce<4><<<blocks_of(count / 4), 256, 0, s>>>(part, splits, count, add, C);
+  else
+    k_mx_reduce<1><<<blocks_of(count), 256, 0, s>>>(part, splits, count, add, C);
+  return cuda_fail(cudaGetLastError(), "split sum launch");
+}
 }  // namespace
 
 // ---- Y = X Dᵀ and dX = dY D -----------------------------------------------------
@@ -686,14 +772,9 @@ hsl_status mx_gemm_apply_run(bool trans, const MxOperand& D, int64_t m, int64_t 
     if (hsl_status e = trans ? launch_gemm<A_E2M1_M, false, 1, OUT_T_PART>(sh.MH, maps, g, s)
                              : launch_gemm<A_E2M1_K, false, 1, OUT_T_PART>(sh.MH, maps, g, s))
       return e;
-    note_launch();
-    k_mx_reduce<<<blocks_of(T * M), 256, 0, s>>>(g.part, sh.splits, T * M, g.add, g.C);
-    return cuda_fail(cudaGetLastError(), "split sum launch");
+    return reduce_run(g.part, sh.splits, T * M, g.add, g.C, s);
   }
-  g.cstore = (M % 8 == 0 && reinterpret_cast<uintptr_t>(Y) % 16 == 0) ? 1 : 0;
-  if (g.cstore && !make_tmap_2d(&maps.c, kBF, 2, Y, T, M, M, 128 * sh.MH, sh.BN,
-                                CU_TENSOR_MAP_SWIZZLE_NONE))
-    return map_failed();
+  if (!out_maps(&maps, &g, T, M, sh.MH)) return map_failed();
   return trans ? launch_gemm<A_E2M1_M, false, 1, OUT_T>(sh.MH, maps, g, s)
                : launch_gemm<A_E2M1_K, false, 1, OUT_T>(sh.MH, maps, g, s);
 }
@@ -781,7 +862,10 @@ hsl_status mx_gemm_grad_run(const MxOperand& X, int64_t T, int64_t n, const void
   };
   auto pair = [&](const GemmShape& sh, __nv_bfloat16* hi, __nv_bfloat16* lo) {
     note_launch();
-    k_mx_reduce_pair<<<blocks_of(T * p.rp), 256, 0, s>>>(part, sh.splits, T, int(r), int(p.rp), hi, lo);
+    if (r % 8 == 0)
+      k_mx_reduce_pair<4><<<blocks_of(T * p.rp / 4), 256, 0, s>>>(part, sh.splits, T, int(r), int(p.rp), hi, lo);
+    else
+      k_mx_reduce_pair<1><<<blocks_of(T * p.rp), 256, 0, s>>>(part, sh.splits, T, int(r), int(p.rp), hi, lo);
     return cuda_fail(cudaGetLastError(), "split sum launch");
   };
   GemmMaps maps;
@@ -819,9 +903,7 @@ hsl_status mx_gemm_grad_run(const MxOperand& X, int64_t T, int64_t n, const void
     if (hsl_status e = of_u ? launch_gemm<A_BF16_M, true, 2, OUT_R_PART>(sh.MH, maps, g, s)
                             : launch_gemm<A_INT8_M, true, 2, OUT_R_PART>(sh.MH, maps, g, s))
       return e;
-    note_launch();
-    k_mx_reduce<<<blocks_of(M * r), 256, 0, s>>>(part, sh.splits, M * r, nullptr, g.C);
-    return cuda_fail(cudaGetLastError(), "split sum launch");
+    return reduce_run(part, sh.splits, M * r, nullptr, g.C, s);
   };
   if (hsl_status e = second(true, p.u, m, zh, zl, dU)) return e;
   if (hsl_status e = second(false, p.v, n, gh, gl, dV)) return e;
@@ -834,10 +916,7 @@ hsl_status mx_gemm_grad_run(const MxOperand& X, int64_t T, int64_t n, const void
     return map_failed();
   g.add = static_cast<const __nv_bfloat16*>(add);
   g.C = static_cast<__nv_bfloat16*>(dX);
-  g.cstore = (n % 8 == 0 && reinterpret_cast<uintptr_t>(dX) % 16 == 0) ? 1 : 0;
-  if (g.cstore && !make_tmap_2d(&maps.c, kBF, 2, dX, T, n, n, 128 * p.x.MH, p.x.BN,
-                                CU_TENSOR_MAP_SWIZZLE_NONE))
-    return map_failed();
+  if (!out_maps(&maps, &g, T, n, p.x.MH)) return map_failed();
   return launch_gemm<A_BF16_K, false, 2, OUT_T>(p.x.MH, maps, g, s);
 }
 
