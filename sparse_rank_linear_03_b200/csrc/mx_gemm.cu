@@ -50,7 +50,7 @@ __device__ uint32_t g_mx_gemm_err;
 constexpr int G_BK = 64;
 constexpr int G_THREADS = 608;   // 19 warps: copies, MMA, 2 × 8 widening (all 16 in the epilogue), code copies
 constexpr int G_MAX_STAGES = 8;
-constexpr int G_SMEM_BUDGET = 222 * 1024;  // stages; the barriers and alignment take under 3 KB more
+constexpr int G_SMEM_BUDGET = 224 * 1024;  // stages and code tiles; barriers and alignment take 2 KB more
 
 enum AKind { A_BF16_K, A_BF16_M, A_E2M1_K, A_E2M1_M, A_INT8_K, A_INT8_M };
 enum OutKind { OUT_T, OUT_R, OUT_T_PART, OUT_R_PART };  // C[n][m] or C[m][n]; bf16 or fp32 partials
@@ -137,11 +137,14 @@ struct Block {
   uint4 c[kInt8 ? 2 : 1];
   uint32_t e;
 };
-// Writes the block's 32 bf16 to chunks 4·half .. 4·half + 3 of tile row `row`.
+__device__ __forceinline__ void sts128(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+// Writes the block's 32 bf16 to chunks 4·half .. 4·half + 3 of a tile row.  `row` is the address of
+// the row's chunk 0 as the swizzle places it: chunk c lies at row ^ (c << 4).
 template <bool kInt8>
-__device__ __forceinline__ void widen(const Block<kInt8>& b, unsigned char* tile, int row, int half) {
-  unsigned char* r = tile + row * 128;
-  const int x = row & 7;
+__device__ __forceinline__ void widen(const Block<kInt8>& b, uint32_t row, int half) {
   if (kInt8) {
     const uint32_t s = int8_scale(b.e);
     const uint32_t w[8] = {b.c[0].x, b.c[0].y, b.c[0].z, b.c[0].w,
@@ -150,14 +153,13 @@ __device__ __forceinline__ void widen(const Block<kInt8>& b, unsigned char* tile
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const uint2 lo = widen_int8(w[2 * q], s), hi = widen_int8(w[2 * q + 1], s);
-      *reinterpret_cast<uint4*>(r + (((half * 4 + q) ^ x) << 4)) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      sts128(row ^ ((half * 4 + q) << 4), make_uint4(lo.x, lo.y, hi.x, hi.y));
     }
   } else {
     const uint32_t s = e2m1_scale(b.e);
     const uint32_t w[4] = {b.c[0].x, b.c[0].y, b.c[0].z, b.c[0].w};
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      *reinterpret_cast<uint4*>(r + (((half * 4 + q) ^ x) << 4)) = widen_e2m1(w[q], s);
+    for (int q = 0; q < 4; ++q) sts128(row ^ ((half * 4 + q) << 4), widen_e2m1(w[q], s));
   }
 }
 
@@ -333,8 +335,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
       }
       int s = group, cs = group;
       uint32_t ph = 1, cph = 0;
+      const uint32_t smem32 = tc::smem_u32(smem) + trow * 128 + ((trow & 7) << 4);
       for (int kb = group; kb < nk; kb += 2) {
-        unsigned char* a = smem + s * kStage;
         Block<kInt8> blk[MH];
         if (!g_wait(&raw[cs], cph, abrt)) break;
         const unsigned char* q = cring + cs * Code::kBytes;
@@ -370,9 +372,13 @@ __global__ void __launch_bounds__(G_THREADS, 1)
           cs -= g.codes;
           cph ^= 1;
         }
+        // (A parity tells one completion from the next only.  A warp that waits for the MMAs of
+        // K-block kb − stages has seen those of kb − 2 − stages done, so it is never two
+        // completions ahead; code tiles are an even number, so that a tile's place belongs to
+        // one group, which has seen every earlier completion of its barrier.)
         if (!g_wait(&empty[s], ph, abrt)) break;
 #pragma unroll
-        for (int b = 0; b < MH; ++b) widen(blk[b], a, trow, half0 + b);
+        for (int b = 0; b < MH; ++b) widen(blk[b], smem32 + s * kStage, half0 + b);
         tc::fence_async_smem();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&full[s]);
@@ -608,7 +614,8 @@ GemmShape shape_of(int ak, int64_t M, int64_t N, int64_t K, bool bmn, int terms,
     int64_t best = INT64_MAX, at = ntn;
     for (int64_t c = ntn; c <= 2 * ntn; ++c) {
       const int64_t bn = round_up((N + c - 1) / c, 16);
-      const int64_t cost = (t2 * c + 147) / 148 * std::max<int64_t>(bn, 160);
+      const bool three = 3 * stage_bytes(bmn, terms, 2, int(bn)) + 4 * code_bytes(ak, 2) <= G_SMEM_BUDGET;
+      const int64_t cost = (t2 * c + 147) / 148 * std::max<int64_t>(bn, 160) * (three ? 4 : 5);
       if (cost < best) {
         best = cost;
         at = c;
@@ -636,15 +643,14 @@ GemmShape shape_of(int ak, int64_t M, int64_t N, int64_t K, bool bmn, int terms,
     s.MH = c2 < c1 ? 2 : 1;
     s.splits = int(s.MH == 2 ? s2 : s1);
   }
-  // Code tiles are small and come from farther away than anything else: four of them in
-  // flight at least, then as many stages as fit (two at least: a pair of terms with an
-  // 8-bit factor leaves room for them only with one accumulator), then more code tiles.
+  // Code tiles are small and come from farther away than anything else: four of them in flight at
+  // least, then as many stages as fit (two at least: a pair of terms with an 8-bit factor
+  // leaves room for them only with one accumulator), then more code tiles, an even number.
   auto fit = [&](int mh) {
     const int code = code_bytes(ak, mh), stage = stage_bytes(bmn, terms, mh, s.BN);
     s.codes = code ? 4 : 0;
-    if (G_SMEM_BUDGET - s.codes * code < 3 * stage) s.codes = code ? 3 : 0;
     s.stages = std::min(G_MAX_STAGES, (G_SMEM_BUDGET - s.codes * code) / stage);
-    if (code) s.codes = std::min(G_MAX_STAGES, (G_SMEM_BUDGET - s.stages * stage) / code);
+    if (code) s.codes = std::min(G_MAX_STAGES, (G_SMEM_BUDGET - s.stages * stage) / code) & ~1;
   };
   fit(s.MH);
   if (s.MH == 2 && s.stages < 2) fit(s.MH = 1);
