@@ -231,10 +231,11 @@ hsl_status hsl_mx_check(hsl_stream stream) {
   set_message("");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cudaError_t e = cudaStreamSynchronize(s)) return cuda_fail(e, "stream synchronize");
-  uint32_t* words[3] = {};
+  uint32_t* words[4] = {};
   if (cudaError_t e = mx_gemm_error_word(&words[0])) return cuda_fail(e, "error word address");
   if (cudaError_t e = mx_matmul_error_word(&words[1])) return cuda_fail(e, "error word address");
   if (cudaError_t e = mx_decode_error_word(&words[2])) return cuda_fail(e, "error word address");
+  if (cudaError_t e = mx_grad_error_word(&words[3])) return cuda_fail(e, "error word address");
   uint32_t all = 0;
   for (uint32_t* p : words) {
     uint32_t v = 0;

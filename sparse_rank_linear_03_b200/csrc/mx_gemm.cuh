@@ -1,0 +1,704 @@
+// Products on the tensor cores with one factor held in microscaled blocks.
+//
+//   C = A · (B0 + B1)ᵀ (+ add),   A [M][K], B [N][K], fp32 sums in TMEM
+//
+// A is the large factor: a 4-bit weight matrix, an 8-bit checkpoint, or a bf16
+// matrix, each either stored as [M][K] or used transposed from [K][M].  B is a bf16
+// matrix (tokens, factors), stored as [N][K] or [K][N]; B1 is the low part of a
+// value held as a bf16 pair.  The same kernel is the forward product (M = features,
+// N = tokens), its input gradient (the same matrix, transposed) and the four
+// skinny products of the factors' gradients (N = r).
+//
+// Blocks are widened to bf16 on their way into shared memory.  That is exact: an
+// e2m1 value has 2 significant bits and an int8 value 7, the block's scale is a
+// power of two, and bf16 has 8 significant bits and fp32's exponents (values
+// down to 2^−133 are bf16 subnormals).  So the products differ from the definition
+// by the rounding of the fp32 sums only.
+//
+// Both storage orders use the same shared-memory tile: rows of 64 values (128
+// bytes) in the 128-byte swizzle.  For [M][K] a tile row is a row of A and the 64
+// values run along K; for [K][M] a tile row is a k and the 64 values run along M,
+// which the MMA reads as an M-major operand.  Widening is the same either way: a
+// thread turns the one or two blocks of its tile row into 128 bytes.
+//
+//   warp 0 lane 0   TMA of the B tile(s), and of A when it is bf16
+//   warp 1 lane 0   tcgen05.mma, M = 128 per accumulator, N up to 256, K = 16
+//   warp 18 lane 0  TMA of the code tiles, into a ring of their own
+//   warps 2-17      widen A's blocks, two groups of eight taking turns at the K-blocks;
+//                   then the epilogue: tcgen05.ld, add, round, store
+//
+// MH = 2 gives the CTA two 128-row accumulators that share every B tile: a K-block
+// of 256 × 256 × 64 takes the MMAs about 1024 cycles, in which 32 KB of B and
+// 8 KB of codes arrive and the eight warps spend about 400 issue cycles widening.
+// Every wait is bounded.
+#pragma once
+
+#include <cuda.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "common.cuh"
+#include "internal.h"
+#include "mx.cuh"
+#include "mx_ops.h"
+#include "tc.cuh"
+
+namespace hsl {
+namespace {
+
+__device__ uint32_t g_mx_gemm_err;
+
+constexpr int G_BK = 64;
+constexpr int G_THREADS = 608;   // 19 warps: copies, MMA, 2 × 8 widening (all 16 in the epilogue), code copies
+constexpr int G_MAX_STAGES = 8;
+constexpr int G_SMEM_BUDGET = 224 * 1024;  // stages and code tiles; barriers and alignment take 2 KB more
+
+enum AKind { A_BF16_K, A_BF16_M, A_E2M1_K, A_E2M1_M, A_INT8_K, A_INT8_M };
+enum OutKind { OUT_T, OUT_R, OUT_T_PART };  // C[n][m]; C[m][n], or its fp32 partials (g.part); partials of C[n][m]
+
+constexpr bool a_is_blocks(int a) { return a >= A_E2M1_K; }
+constexpr bool a_is_mmajor(int a) { return a == A_BF16_M || a == A_E2M1_M || a == A_INT8_M; }
+constexpr bool a_is_int8(int a) { return a == A_INT8_K || a == A_INT8_M; }
+
+struct GemmMaps {
+  CUtensorMap a;   // bf16 A: box {64, 128} (K-major) or {64, 64}
+  CUtensorMap b0;  // B: box {64, BN} (K-major) or {64, 64}
+  CUtensorMap b1;  // low part
+  CUtensorMap c;   // OUT_T: box {128·MH, BN}
+  CUtensorMap add; // like c
+  CUtensorMap q;   // codes: box {CodeTile::kInner bytes, CodeTile::kRows}
+  CUtensorMap qs;  // scales of [K][M] blocks: box {16 bytes, 64}
+};
+struct GemmArgs {
+  const uint8_t* scales;  // [M][K] blocks: read 16 at a time per row
+  int64_t spitch;
+  int arows, nb;          // stored rows of A, blocks per row
+  int M, N, nk;      // nk: K-blocks of 64
+  int BN, stages, splits;
+  int codes;         // code tiles in flight
+  int cstore;        // OUT_T: tiled store possible
+  int addt;          // OUT_T: add comes as a tile as well
+  const __nv_bfloat16* add;
+  __nv_bfloat16* C;
+  float* part;       // [splits][N][M] or [splits][M][N]; OUT_R: nullptr where C is written
+};
+
+__device__ __forceinline__ bool g_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (tc::mbar_try(bar, parity)) return true;
+  if (*abort_flag) return false;
+  if (tc::mbar_wait(bar, parity, &g_mx_gemm_err)) return true;
+  *abort_flag = 1;
+  return false;
+}
+
+// M- or N-major operand in the 128-byte swizzle: 64 values along the row, 8 k per
+// 1024-byte atom; the next 64 values of the row dimension 8192 bytes on.
+__device__ __forceinline__ uint64_t desc_mn_sw128(const void* tile) {
+  const uint64_t addr = tc::smem_u32(tile);
+  uint64_t d = 0;
+  d |= (addr >> 4) & 0x3FFFull;
+  d |= uint64_t(8192 >> 4) << 16;  // leading byte offset: the next 64 values
+  d |= uint64_t(1024 >> 4) << 32;  // stride byte offset: the next 8 k
+  d |= uint64_t(1) << 46;
+  d |= uint64_t(2) << 61;          // SWIZZLE_128B
+  return d;
+}
+
+// ---- widening -----------------------------------------------------------------
+using mx::e2m1_scale;
+using mx::int8_scale;
+using mx::widen_e2m1;
+using mx::widen_int8;
+
+// The code tile of a K-block in shared memory, as copied: kBoxes boxes of kRows rows of
+// kInner bytes in the swizzle of that width, so that the threads of a warp, a row
+// each, read their 16-byte chunks without bank conflicts.
+template <int AK, int MH>
+struct CodeTile {
+  static constexpr int kElem = a_is_int8(AK) ? 2 : 1;  // half-bytes per value
+  static constexpr int kRowBytes = (a_is_mmajor(AK) ? 128 * MH : 64) * kElem / 2;
+  static constexpr int kRows = a_is_mmajor(AK) ? 64 : 128 * MH;
+  static constexpr int kInner = kRowBytes < 128 ? kRowBytes : 128;
+  static constexpr int kBoxes = kRowBytes / kInner;
+  static constexpr int kCodes = kRows * kRowBytes;
+  static constexpr int kScales = a_is_mmajor(AK) ? 64 * 16 : 0;
+  static constexpr int kBytes = a_is_blocks(AK) ? kCodes + kScales : 0;
+  // address of 16-byte chunk c of row r
+  __device__ static __forceinline__ uint32_t at(int r, int c) {
+    constexpr int per = kInner / 16;
+    const int box = c / per, in = c % per;
+    const int x = kInner == 128 ? r & 7 : kInner == 64 ? (r >> 1) & 3 : (r >> 2) & 1;
+    return uint32_t(box * kRows * kInner + r * kInner + ((in ^ x) << 4));
+  }
+};
+
+// The codes and scale of one block of 32.
+template <bool kInt8>
+struct Block {
+  uint4 c[kInt8 ? 2 : 1];
+  uint32_t e;
+};
+__device__ __forceinline__ void sts128(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+// Writes the block's 32 bf16 to chunks 4·half .. 4·half + 3 of a tile row.  `row` is the address of
+// the row's chunk 0 as the swizzle places it: chunk c lies at row ^ (c << 4).
+template <bool kInt8>
+__device__ __forceinline__ void widen(const Block<kInt8>& b, uint32_t row, int half) {
+  if (kInt8) {
+    const uint32_t s = int8_scale(b.e);
+    const uint32_t w[8] = {b.c[0].x, b.c[0].y, b.c[0].z, b.c[0].w,
+                           b.c[kInt8 ? 1 : 0].x, b.c[kInt8 ? 1 : 0].y, b.c[kInt8 ? 1 : 0].z,
+                           b.c[kInt8 ? 1 : 0].w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint2 lo = widen_int8(w[2 * q], s), hi = widen_int8(w[2 * q + 1], s);
+      sts128(row ^ ((half * 4 + q) << 4), make_uint4(lo.x, lo.y, hi.x, hi.y));
+    }
+  } else {
+    const uint32_t s = e2m1_scale(b.e);
+    const uint32_t w[4] = {b.c[0].x, b.c[0].y, b.c[0].z, b.c[0].w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sts128(row ^ ((half * 4 + q) << 4), widen_e2m1(w[q], s));
+  }
+}
+
+// Tile `block` of the product.
+template <int AK, bool BMN, int TERMS, int MH, int OUT>
+__device__ __forceinline__ void gemm_tile(const GemmMaps& maps, const GemmArgs& g, int block) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  // (an offset, not a rounded integer: the compiler still knows that this is shared memory)
+  unsigned char* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+  __shared__ uint64_t full[G_MAX_STAGES], empty[G_MAX_STAGES], accf, addf;
+  __shared__ uint64_t raw[G_MAX_STAGES], taken[G_MAX_STAGES];  // code tile landed, read
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ntn = (g.N + g.BN - 1) / g.BN;
+  const int tile = block / g.splits, split = block % g.splits;
+  const int i0 = (tile / ntn) * (128 * MH), j0 = (tile % ntn) * g.BN;
+  const int kb0 = int(int64_t(g.nk) * split / g.splits);
+  const int nk = int(int64_t(g.nk) * (split + 1) / g.splits) - kb0;
+  constexpr int kA = MH * 128 * 128;  // bytes of the A tile
+  const int bgroups = (g.BN + 63) / 64;
+  const int kB = BMN ? bgroups * 8192 : g.BN * 128;
+  using Code = CodeTile<AK, MH>;
+  const int kStage = kA + TERMS * kB;
+  unsigned char* cring = smem + g.stages * kStage;
+  uint32_t cols = MH == 2 ? 64 : 32;  // whole 32-column reads past 2 × 16 columns stay inside
+  while (cols < uint32_t(MH * g.BN)) cols *= 2;
+
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int s = 0; s < g.stages; ++s) {
+      tc::mbar_init(&full[s], a_is_blocks(AK) ? 1 + 8 : 1);  // copies, and the eight widening warps
+      tc::mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < g.codes; ++s) {
+      tc::mbar_init(&raw[s], 1);
+      tc::mbar_init(&taken[s], 8);
+    }
+    tc::mbar_init(&accf, 1);
+    tc::mbar_init(&addf, 1);
+    tc::fence_mbar_init();
+    tc::prefetch_tmap(&maps.b0);
+    if (OUT == OUT_T && g.addt) tc::tma_prefetch_2d(&maps.add, i0, j0);  // into L2 for the epilogue
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(&tmem_slot, cols);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  volatile int* abrt = &abort_flag;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int s = 0, issued = 0;
+      uint32_t ph = 1;
+      for (int kb = 0; kb < nk; ++kb) {
+        if (!g_wait(&empty[s], ph, abrt)) break;
+        unsigned char* a = smem + s * kStage;
+        unsigned char* b = a + kA;
+        const int k0 = (kb0 + kb) * G_BK;
+        tc::mbar_expect_tx(&full[s], (a_is_blocks(AK) ? 0 : kA) + TERMS * kB);
+        if (AK == A_BF16_K) {
+#pragma unroll
+          for (int h = 0; h < MH; ++h)
+            tc::tma_load_2d(a + h * 16384, &maps.a, k0, i0 + h * 128, &full[s]);
+        } else if (AK == A_BF16_M) {
+#pragma unroll
+          for (int h = 0; h < 2 * MH; ++h)
+            tc::tma_load_2d(a + h * 8192, &maps.a, i0 + h * 64, k0, &full[s]);
+        }
+#pragma unroll
+        for (int t = 0; t < TERMS; ++t) {
+          const CUtensorMap* map = t ? &maps.b1 : &maps.b0;
+          if (BMN) {
+            for (int q = 0; q < bgroups; ++q)
+              tc::tma_load_2d(b + t * kB + q * 8192, map, j0 + q * 64, k0, &full[s]);
+          } else {
+            tc::tma_load_2d(b + t * kB, map, k0, j0, &full[s]);
+          }
+        }
+        ++issued;
+        if (++s == g.stages) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+      // the copies in flight have landed before the CTA's shared memory is given up
+      for (int q = 0; q < g.stages && q < issued; ++q) {
+        const int last = (issued - 1 - q) / g.stages;  // uses of stage q before its last one
+        if (*abrt) tc::mbar_wait(&full[q], uint32_t(last) & 1, &g_mx_gemm_err);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 18) {
+    if (lane == 0 && a_is_blocks(AK)) {
+      int s = 0, issued = 0;
+      uint32_t ph = 1;
+      for (int kb = 0; kb < nk; ++kb) {
+        if (!g_wait(&taken[s], ph, abrt)) break;
+        unsigned char* q = cring + s * Code::kBytes;
+        const int k0 = (kb0 + kb) * G_BK;
+        const int qx = (a_is_mmajor(AK) ? i0 : k0) * Code::kElem / 2, qy = a_is_mmajor(AK) ? k0 : i0;
+        tc::mbar_expect_tx(&raw[s], Code::kBytes);
+#pragma unroll
+        for (int x = 0; x < Code::kBoxes; ++x)
+          tc::tma_load_2d(q + x * Code::kRows * Code::kInner, &maps.q, qx + x * Code::kInner, qy, &raw[s]);
+        if (a_is_mmajor(AK)) tc::tma_load_2d(q + Code::kCodes, &maps.qs, (i0 / 32) & ~15, k0, &raw[s]);
+        ++issued;
+        if (++s == g.codes) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+      for (int q = 0; q < g.codes && q < issued; ++q)
+        if (*abrt) tc::mbar_wait(&raw[q], uint32_t((issued - 1 - q) / g.codes) & 1, &g_mx_gemm_err);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (tc::elect_one()) {
+      const uint32_t idesc = tc::idesc_bf16(128, g.BN) | (a_is_mmajor(AK) ? 1u << 15 : 0u) |
+                             (BMN ? 1u << 16 : 0u);
+      int s = 0;
+      uint32_t ph = 0;
+      for (int kb = 0; kb < nk; ++kb) {
+        if (!g_wait(&full[s], ph, abrt)) break;
+        tc::tc_fence_after();
+        unsigned char* a = smem + s * kStage;
+#pragma unroll
+        for (int t = 0; t < TERMS; ++t) {
+          const uint64_t bd = BMN ? desc_mn_sw128(a + kA + t * kB) : tc::desc_sw128(a + kA + t * kB);
+#pragma unroll
+          for (int h = 0; h < MH; ++h) {
+            const uint64_t ad =
+                a_is_mmajor(AK) ? desc_mn_sw128(a + h * 16384) : tc::desc_sw128(a + h * 16384);
+#pragma unroll
+            for (int k = 0; k < G_BK / 16; ++k)
+              tc::mma_bf16(tmem + h * g.BN, tc::desc_advance(ad, k * (a_is_mmajor(AK) ? 2048 : 32)),
+                           tc::desc_advance(bd, k * (BMN ? 2048 : 32)), idesc,
+                           (kb > 0 || k > 0 || t > 0) ? 1u : 0u);
+          }
+        }
+        tc::mma_commit(&empty[s]);
+        if (++s == g.stages) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+      tc::mma_commit(&accf);
+    }
+    __syncwarp();
+  } else {
+    const int tid = (threadIdx.x - 64) & 255, group = (warp - 2) >> 3;
+    if (a_is_blocks(AK)) {
+      constexpr bool kInt8 = a_is_int8(AK);
+      // MH = 2: tile row tid, both blocks; MH = 1: two threads share a tile row
+      const int trow = MH == 2 ? tid : (tid & 127);
+      const int half0 = MH == 2 ? 0 : (tid >> 7);
+      // The two groups of eight warps take the K-blocks in turn, so that one group's wait for
+      // its codes and its hand-over overlap the other's arithmetic.
+      // [M][K]: the row's scales, 16 blocks (8 K-blocks) at a time, one load ahead
+      const bool row_ok = i0 + trow < g.arows;
+      const uint4* srow = reinterpret_cast<const uint4*>(g.scales + int64_t(i0 + trow) * g.spitch);
+      const int sgroups = int(g.spitch / 16);
+      int sgrp = (kb0 + group) >> 3;
+      uint4 sc = make_uint4(0, 0, 0, 0), sn = sc;
+      if (!a_is_mmajor(AK) && row_ok) {
+        if (sgrp < sgroups) sc = __ldg(srow + sgrp);
+        if (sgrp + 1 < sgroups) sn = __ldg(srow + sgrp + 1);
+      }
+      int s = group, cs = group;
+      uint32_t ph = 1, cph = 0;
+      const uint32_t smem32 = tc::smem_u32(smem) + trow * 128 + ((trow & 7) << 4);
+      for (int kb = group; kb < nk; kb += 2) {
+        Block<kInt8> blk[MH];
+        if (!g_wait(&raw[cs], cph, abrt)) break;
+        const unsigned char* q = cring + cs * Code::kBytes;
+#pragma unroll
+        for (int b = 0; b < MH; ++b) {
+          const int r = a_is_mmajor(AK) ? (trow & 63) : trow;
+          const int n0 = (a_is_mmajor(AK) ? (trow >> 6) * 2 : 0) + half0 + b;  // block in the row
+          if (kInt8) {
+            blk[b].c[0] = *reinterpret_cast<const uint4*>(q + Code::at(r, 2 * n0));
+            blk[b].c[kInt8 ? 1 : 0] = *reinterpret_cast<const uint4*>(q + Code::at(r, 2 * n0 + 1));
+          } else {
+            blk[b].c[0] = *reinterpret_cast<const uint4*>(q + Code::at(r, n0));
+          }
+          if (a_is_mmajor(AK)) blk[b].e = q[Code::kCodes + r * 16 + ((i0 / 32) & 15) + n0];
+        }
+        if (!a_is_mmajor(AK)) {
+          const int kk = kb0 + kb;
+          if ((kk >> 3) != sgrp) {  // steps of 2: the next group of 8 K-blocks
+            sgrp = kk >> 3;
+            sc = sn;
+            if (row_ok && sgrp + 1 < sgroups) sn = __ldg(srow + sgrp + 1);
+          }
+          const uint32_t w = (kk & 4) ? ((kk & 2) ? sc.w : sc.z) : ((kk & 2) ? sc.y : sc.x);
+          const uint32_t pair = (kk & 1) ? w >> 16 : w;
+#pragma unroll
+          for (int b = 0; b < MH; ++b)  // padding bytes after the last block count as 0
+            blk[b].e = kk * 2 + half0 + b < g.nb ? (pair >> (8 * (half0 + b))) & 0xFFu : 0u;
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&taken[cs]);
+        cs += 2;
+        if (cs >= g.codes) {
+          cs -= g.codes;
+          cph ^= 1;
+        }
+        // (A parity tells one completion from the next only.  A warp that waits for the MMAs of
+        // K-block kb − stages has seen those of kb − 2 − stages done, so it is never two
+        // completions ahead; code tiles are an even number, so that a tile's place belongs to
+        // one group, which has seen every earlier completion of its barrier.)
+        if (!g_wait(&empty[s], ph, abrt)) break;
+#pragma unroll
+        for (int b = 0; b < MH; ++b) widen(blk[b], smem32 + s * kStage, half0 + b);
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&full[s]);
+        s += 2;
+        if (s >= g.stages) {
+          s -= g.stages;
+          ph ^= 1;
+        }
+      }
+    }
+    // epilogue: warp w reaches TMEM lanes 32 (w mod 4) onwards; the four groups of four
+    // warps divide the accumulators and their columns
+    __syncwarp();
+    bool ok = tc::mbar_wait(&accf, 0, &g_mx_gemm_err) && !*abrt;
+    __nv_bfloat16* stg = reinterpret_cast<__nv_bfloat16*>(smem);
+    if (OUT == OUT_T && g.addt && ok) {
+      // the tile of add into the idle ring, where each value is replaced by the result (loads of
+      // single values from global memory took five times as long as the product)
+      if (threadIdx.x == 64) {
+        tc::mbar_expect_tx(&addf, uint32_t(128 * MH * g.BN * 2));
+        tc::tma_load_2d(stg, &maps.add, i0, j0, &addf);
+      }
+      ok = tc::mbar_wait(&addf, 0, &g_mx_gemm_err);
+    }
+    if (ok) {
+      tc::tc_fence_after();
+      const int grp = (warp - 2) >> 2;
+      const int acc = MH == 2 ? grp & 1 : 0;
+      const int L = ((warp & 3) << 5) | lane;
+      const int R = acc * 128 + L;
+      const int i = i0 + R;
+      const uint32_t tb = tmem + (uint32_t((warp & 3) * 32) << 16) + uint32_t(acc * g.BN);
+      // columns in steps of 32 (the last step may reach past BN, inside the allocation)
+      const int steps = (g.BN + 31) / 32;
+      constexpr int kShare = 4 / MH;  // groups of four warps per accumulator
+      const int part = grp / MH;
+      const int c_lo = steps * part / kShare, c_hi = steps * (part + 1) / kShare;
+#pragma unroll 1
+      for (int c = c_lo; c < c_hi; ++c) {
+        const int c0 = c * 32;
+        float v[32];
+        tc::tmem_ld32(tb + c0, v);
+        if (nk == 0) {
+#pragma unroll
+          for (int q = 0; q < 32; ++q) v[q] = 0.f;
+        }
+        const int jn = min(32, min(g.BN - c0, g.N - j0 - c0));  // columns of this step in the tile
+        if (OUT == OUT_T || OUT == OUT_T_PART) {
+          if (OUT == OUT_T_PART) {
+            float* p = g.part + (int64_t(split) * g.N + j0 + c0) * g.M + i;
+            if (i < g.M) {
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                if (q < jn) p[int64_t(q) * g.M] = v[q];
+            }
+          } else {
+            if (g.addt) {
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                if (c0 + q < g.BN) v[q] += __bfloat162float(stg[(c0 + q) * (128 * MH) + R]);
+            } else if (g.add && i < g.M) {
+              const __nv_bfloat16* p = g.add + int64_t(j0 + c0) * g.M + i;
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                if (q < jn) v[q] += __bfloat162float(p[int64_t(q) * g.M]);
+            }
+            if (g.cstore) {
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                if (c0 + q < g.BN) stg[(c0 + q) * (128 * MH) + R] = __float2bfloat16_rn(v[q]);
+            } else if (i < g.M) {
+              __nv_bfloat16* p = g.C + int64_t(j0 + c0) * g.M + i;
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                if (q < jn) p[int64_t(q) * g.M] = __float2bfloat16_rn(v[q]);
+            }
+          }
+        } else if (i < g.M && jn > 0) {
+          if (g.part) {
+            float* p = g.part + (int64_t(split) * g.M + i) * g.N + j0 + c0;
+            if (jn == 32 && g.N % 4 == 0) {
+#pragma unroll
+              for (int q = 0; q < 32; q += 4)
+                *reinterpret_cast<float4*>(p + q) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
+            } else {
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                if (q < jn) p[q] = v[q];
+            }
+          } else {
+            __nv_bfloat16* p = g.C + int64_t(i) * g.N + j0 + c0;
+            if (jn == 32 && g.cstore) {  // rows of C start on 16 bytes
+#pragma unroll
+              for (int q = 0; q < 32; q += 8) {
+                uint4 o;
+                uint32_t* w = &o.x;
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                  const __nv_bfloat162 h = __floats2bfloat162_rn(v[q + 2 * z], v[q + 2 * z + 1]);
+                  w[z] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+                *reinterpret_cast<uint4*>(p + q) = o;
+              }
+            } else {
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                if (q < jn) p[q] = __float2bfloat16_rn(v[q]);
+            }
+          }
+        }
+      }
+    } else {
+      *abrt = 1;
+    }
+    if (OUT == OUT_T && g.cstore) {
+      // the rounded tile [column][row] lies in the idle ring: one tiled store.  All sixteen
+      // warps meet here, whether or not a wait gave up before.
+      tc::fence_async_smem();
+      asm volatile("barrier.sync 1, 512;" ::: "memory");
+      if (threadIdx.x == 64 && ok && !*abrt) {
+        tc::tma_store_2d(&maps.c, stg, i0, j0);
+        tc::bulk_commit();
+        tc::bulk_wait_read_all();
+      }
+    }
+  }
+  tc::tc_fence_before();
+  tc::cta_sync();
+  if (warp == 1) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, cols);
+  }
+}
+
+template <int AK, bool BMN, int TERMS, int MH, int OUT>
+__global__ void __launch_bounds__(G_THREADS, 1)
+    k_mx_gemm(const __grid_constant__ GemmMaps maps, const GemmArgs g) {
+  gemm_tile<AK, BMN, TERMS, MH, OUT>(maps, g, blockIdx.x);
+}
+
+// Σ over the splits' partials in split order; four values per thread where rows and pointers allow it
+// (V = 4), else one.
+template <int V>
+__device__ __forceinline__ void sum_splits(const float* part, int splits, int64_t stride, int64_t at, float (&v)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; ++j) v[j] = 0.f;
+#pragma unroll 8
+  for (int s = 0; s < splits; ++s) {
+    const float* p = part + int64_t(s) * stride + at;
+    if (V == 4) {
+      const float4 q = __ldcs(reinterpret_cast<const float4*>(p));
+      v[0] += q.x; v[1 % V] += q.y; v[2 % V] += q.z; v[3 % V] += q.w;
+    } else {
+      v[0] += p[0];
+    }
+  }
+}
+template <int V>
+__device__ __forceinline__ void store_bf(__nv_bfloat16* p, const float (&v)[V]) {
+  if (V == 4) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1 % V]), b = __floats2bfloat162_rn(v[2 % V], v[3 % V]);
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  } else {
+    p[0] = __float2bfloat16_rn(v[0]);
+  }
+}
+// Rows of n bf16 to rows of `pitch` (a multiple of 8, so that a tile copy can read them).
+__global__ void __launch_bounds__(256)
+    k_mx_pad_rows(const uint16_t* __restrict__ src, int64_t rows, int n, int pitch,
+                  uint16_t* __restrict__ dst) {
+  const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (e >= rows * pitch) return;
+  const int64_t row = e / pitch;
+  const int c = int(e - row * pitch);
+  dst[e] = c < n ? src[row * n + c] : uint16_t(0);
+}
+
+unsigned blocks_of(int64_t count) { return unsigned((count + 255) / 256); }
+
+// ---- host ---------------------------------------------------------------------
+struct GemmShape {
+  int BN, MH, splits, stages, codes;
+};
+
+int code_bytes(int ak, int mh) {
+  if (!a_is_blocks(ak)) return 0;
+  return 128 * mh * (a_is_int8(ak) ? 64 : 32) + (a_is_mmajor(ak) ? 1024 : 0);
+}
+int stage_bytes(bool bmn, int terms, int mh, int bn) {
+  return mh * 16384 + terms * (bmn ? (bn + 63) / 64 * 8192 : bn * 128);
+}
+
+// Stages and code tiles of a tile shape.  Code tiles are small and come from farther away than
+// anything else: four of them in flight at least, then as many stages as fit (two at
+// least: a pair of terms with an 8-bit factor leaves room for them only with one
+// accumulator), then more code tiles, an even number.
+void fit_rings(GemmShape* s, int ak, bool bmn, int terms) {
+  const int code = code_bytes(ak, s->MH), stage = stage_bytes(bmn, terms, s->MH, s->BN);
+  s->codes = code ? 4 : 0;
+  s->stages = std::min(G_MAX_STAGES, (G_SMEM_BUDGET - s->codes * code) / stage);
+  if (code) s->codes = std::min(G_MAX_STAGES, (G_SMEM_BUDGET - s->stages * stage) / code) & ~1;
+}
+bool rings_fit(int ak, bool bmn, int terms, int mh, int bn, int stages) {
+  return stages * stage_bytes(bmn, terms, mh, bn) + (a_is_blocks(ak) ? 4 : 0) * code_bytes(ak, mh) <=
+         G_SMEM_BUDGET;
+}
+// Cycles of a K-block as measured: widening 256 rows 1040, 128 rows 720 (its chain of waits does not
+// shrink with the rows); copies and MMAs 5 per column and accumulator pair, 3 for one.
+int64_t kblock_cycles(int ak, int terms, int mh, int bn) {
+  return std::max<int64_t>(a_is_blocks(ak) ? (mh == 2 ? 1040 : 720) : 0, int64_t(terms) * bn * (mh == 2 ? 5 : 3));
+}
+
+// Tile and split of an M × N × K product.
+GemmShape shape_of(int ak, int64_t M, int64_t N, int64_t K, bool bmn, int terms, bool may_split) {
+  GemmShape s;
+  // With at least a tile per SM, 256-row tiles whose width makes the last round of
+  // CTAs as full as it can be: time goes as rounds × columns (a K-block of fewer than
+  // 160 columns costs the widening, not the MMAs).  2048 tokens × 11008 rows: 208
+  // columns (2.9 rounds) against 256 (2.3 rounds, the third mostly idle).
+  int64_t ntn = (N + 255) / 256;
+  const int64_t t2 = (M + 255) / 256, t1 = (M + 127) / 128, nk = (K + 63) / 64;
+  s.splits = 1;
+  if (t2 * ntn >= 148) {
+    s.MH = 2;
+    int64_t best = INT64_MAX, at = ntn;
+    for (int64_t c = ntn; c <= 2 * ntn; ++c) {
+      const int64_t bn = round_up((N + c - 1) / c, 16);
+      const int64_t cost = (t2 * c + 147) / 148 * std::max<int64_t>(bn, 160) *
+                           (rings_fit(ak, bmn, terms, 2, int(bn), 3) ? 4 : 5);
+      if (cost < best) {
+        best = cost;
+        at = c;
+      }
+    }
+    ntn = at;
+  }
+  s.BN = int(round_up((N + ntn - 1) / ntn, 16));
+  if (t2 * ntn < 148) {
+    // Fewer tiles than SMs: K is split where the caller has room for partial sums, which pass through
+    // HBM twice, at about 3500 bytes per cycle.
+    auto cost = [&](int mh, int64_t* splits) {
+      const int64_t tiles = (mh == 2 ? t2 : t1) * ntn;
+      *splits = may_split ? std::max<int64_t>(1, std::min<int64_t>(148 / tiles, nk / 4)) : 1;
+      return (nk + *splits - 1) / *splits * kblock_cycles(ak, terms, mh, s.BN) * ((tiles * *splits + 147) / 148) +
+             (*splits > 1 ? *splits * M * N * 8 / 3500 : 0);
+    };
+    int64_t s1 = 1, s2 = 1;
+    const int64_t c1 = cost(1, &s1), c2 = cost(2, &s2);
+    s.MH = c2 < c1 && rings_fit(ak, bmn, terms, 2, s.BN, 2) ? 2 : 1;
+    s.splits = int(s.MH == 2 ? s2 : s1);
+  }
+  fit_rings(&s, ak, bmn, terms);
+  return s;
+}
+
+int tile_smem(int ak, bool bmn, int terms, int mh, bool staged, const GemmArgs& g) {
+  int bytes = g.stages * stage_bytes(bmn, terms, mh, g.BN) + g.codes * code_bytes(ak, mh);
+  if (staged) bytes = std::max(bytes, mh * 128 * g.BN * 2);  // the epilogue's tile
+  return bytes + 1024;
+}
+int64_t tile_count(int mh, const GemmArgs& g) {
+  return int64_t((g.M + 128 * mh - 1) / (128 * mh)) * ((g.N + g.BN - 1) / g.BN) * g.splits;
+}
+
+template <int AK, bool BMN, int TERMS, int MH, int OUT>
+hsl_status launch_gemm(const GemmMaps& maps, const GemmArgs& g, cudaStream_t s) {
+  void (*fn)(const GemmMaps, const GemmArgs) = k_mx_gemm<AK, BMN, TERMS, MH, OUT>;
+  const int bytes = tile_smem(AK, BMN, TERMS, MH, OUT == OUT_T, g);
+  if (cudaError_t e = allow_dyn_smem(reinterpret_cast<const void*>(fn), bytes))
+    return cuda_fail(e, "block product smem attribute");
+  note_launch();
+  fn<<<unsigned(tile_count(MH, g)), G_THREADS, size_t(bytes), s>>>(maps, g);
+  return cuda_fail(cudaGetLastError(), "block product launch");
+}
+template <int AK, bool BMN, int TERMS, int OUT>
+hsl_status launch_gemm(int mh, const GemmMaps& maps, const GemmArgs& g, cudaStream_t s) {
+  return mh == 2 ? launch_gemm<AK, BMN, TERMS, 2, OUT>(maps, g, s)
+                 : launch_gemm<AK, BMN, TERMS, 1, OUT>(maps, g, s);
+}
+
+const auto kBF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+const auto kSW = CU_TENSOR_MAP_SWIZZLE_128B;
+
+// The tiled store of C [T][M] and, where add allows it, the tiled load of add.
+bool out_maps(GemmMaps* maps, GemmArgs* g, int64_t T, int64_t M, int mh) {
+  g->cstore = (M % 8 == 0 && reinterpret_cast<uintptr_t>(g->C) % 16 == 0) ? 1 : 0;
+  g->addt = (g->cstore && g->add && reinterpret_cast<uintptr_t>(g->add) % 16 == 0) ? 1 : 0;
+  return (!g->cstore || make_tmap_2d(&maps->c, kBF, 2, g->C, T, M, M, 128 * mh, g->BN, CU_TENSOR_MAP_SWIZZLE_NONE)) &&
+         (!g->addt || make_tmap_2d(&maps->add, kBF, 2, g->add, T, M, M, 128 * mh, g->BN, CU_TENSOR_MAP_SWIZZLE_NONE));
+}
+
+// The tensor maps of a factor in blocks (stored rows × cols).
+bool block_maps(GemmMaps* maps, int ak, int mh, const MxOperand& o, int64_t rows) {
+  const auto U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const int row_bytes = (a_is_mmajor(ak) ? 128 * mh : 64) / (a_is_int8(ak) ? 1 : 2);
+  const int inner = std::min(row_bytes, 128);
+  const auto sw = inner == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                  : inner == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                : CU_TENSOR_MAP_SWIZZLE_32B;
+  return make_tmap_2d(&maps->q, U8, 1, o.p, rows, o.pitch, o.pitch, inner, a_is_mmajor(ak) ? 64 : 128 * mh, sw) &&
+         (!a_is_mmajor(ak) || make_tmap_2d(&maps->qs, U8, 1, o.scales, rows, o.spitch, o.spitch, 16, 64,
+                                           CU_TENSOR_MAP_SWIZZLE_NONE));
+}
+
+hsl_status map_failed() {
+  set_message("tensor map encoding failed");
+  return HSL_ERR_CUDA;
+}
+
+int64_t up16(int64_t b) { return (b + 255) / 256 * 256; }
+
+hsl_status pad_rows(const void* src, int64_t rows, int64_t n, int64_t pitch, void* dst, cudaStream_t s) {
+  note_launch();
+  k_mx_pad_rows<<<blocks_of(rows * pitch), 256, 0, s>>>(static_cast<const uint16_t*>(src), rows, int(n),
+                                                        int(pitch), static_cast<uint16_t*>(dst));
+  return cuda_fail(cudaGetLastError(), "row padding launch");
+}
+
+}  // namespace
+}  // namespace hsl

@@ -42,7 +42,7 @@ hsl_status mx_dequantize_run(const void* codes, const void* scales, int64_t rows
 hsl_status mx_simt_run(const MxOperand& A, const MxOperand& B, int64_t M, int64_t N, int64_t K,
                        const void* add, void* C, hsl_dtype cdt, cudaStream_t s);
 
-// Tensor-core products (mx_gemm.cu), bf16: X, dY, U, V on 16 bytes (mx_gemm_supported)
+// Tensor-core products (mx_gemm.cu, mx_grad.cu), bf16: X, dY, U, V on 16 bytes (mx_gemm_supported)
 bool mx_gemm_supported(const void* X);
 size_t mx_gemm_apply_workspace(bool trans, int64_t T, int64_t m, int64_t n);
 hsl_status mx_gemm_apply_run(bool trans, const MxOperand& D, int64_t m, int64_t n, const void* X,
@@ -52,6 +52,7 @@ hsl_status mx_gemm_grad_run(const MxOperand& X, int64_t T, int64_t n, const void
                             const void* U, const void* V, int64_t r, const void* add, void* dU, void* dV,
                             void* dX, void* ws, cudaStream_t s);
 cudaError_t mx_gemm_error_word(uint32_t** p);
+cudaError_t mx_grad_error_word(uint32_t** p);
 // A few tokens (mx_decode.cu), any alignment of X.  bf16: as many as mx_decode_fits says.
 constexpr int64_t kMxDecodeMax = 16, kMxDecodeF32Max = 64;
 bool mx_decode_fits(int64_t T, int64_t m, int64_t n);
