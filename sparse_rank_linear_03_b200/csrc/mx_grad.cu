@@ -13,23 +13,55 @@
 namespace hsl {
 namespace {
 
-// The maps of a tile function live in the kernel's parameters: 64-byte aligned, one set per product.
+// Each branch is the tile of one product (mx_gemm_tile.cuh).
 template <int MG>
 __global__ void __launch_bounds__(G_THREADS, 1)
-    k_mx_grad_first(const __grid_constant__ GemmMaps gm, const __grid_constant__ GemmMaps zm, const GemmArgs ga,
-                    const GemmArgs za, int ng) {
-  if (int(blockIdx.x) < ng) gemm_tile<A_BF16_K, true, 1, MG, OUT_R>(gm, ga, blockIdx.x);
-  else gemm_tile<A_INT8_K, true, 1, 1, OUT_R>(zm, za, blockIdx.x - ng);
+    k_mx_grad_first(const __grid_constant__ GemmMaps gm, const __grid_constant__ GemmMaps zm,
+                    const __grid_constant__ GemmArgs ga, const __grid_constant__ GemmArgs za, int ng) {
+  constexpr bool BMN = true;
+  constexpr int TERMS = 1, OUT = OUT_R;
+  if (int(blockIdx.x) < ng) {
+    constexpr int AK = A_BF16_K, MH = MG;
+    const GemmMaps& maps = gm;
+    const GemmArgs& g = ga;
+    const int block = blockIdx.x;
+#include "mx_gemm_tile.cuh"
+  } else {
+    constexpr int AK = A_INT8_K, MH = 1;
+    const GemmMaps& maps = zm;
+    const GemmArgs& g = za;
+    const int block = blockIdx.x - ng;
+#include "mx_gemm_tile.cuh"
+  }
 }
 template <int MU, int MX>
 __global__ void __launch_bounds__(G_THREADS, 1)
     k_mx_grad_second(const __grid_constant__ GemmMaps um, const __grid_constant__ GemmMaps vm,
-                     const __grid_constant__ GemmMaps xm, const GemmArgs ua, const GemmArgs va, const GemmArgs xa,
-                     int nu, int nv) {
-  const int b = blockIdx.x;
-  if (b < nu) gemm_tile<A_BF16_M, true, 2, MU, OUT_R>(um, ua, b);
-  else if (b < nu + nv) gemm_tile<A_INT8_M, true, 2, 1, OUT_R>(vm, va, b - nu);
-  else gemm_tile<A_BF16_K, false, 2, MX, OUT_T>(xm, xa, b - nu - nv);
+                     const __grid_constant__ GemmMaps xm, const __grid_constant__ GemmArgs ua,
+                     const __grid_constant__ GemmArgs va, const __grid_constant__ GemmArgs xa, int nu, int nv) {
+  constexpr int TERMS = 2;
+  if (int(blockIdx.x) < nu) {
+    constexpr bool BMN = true;
+    constexpr int AK = A_BF16_M, MH = MU, OUT = OUT_R;
+    const GemmMaps& maps = um;
+    const GemmArgs& g = ua;
+    const int block = blockIdx.x;
+#include "mx_gemm_tile.cuh"
+  } else if (int(blockIdx.x) < nu + nv) {
+    constexpr bool BMN = true;
+    constexpr int AK = A_INT8_M, MH = 1, OUT = OUT_R;
+    const GemmMaps& maps = vm;
+    const GemmArgs& g = va;
+    const int block = blockIdx.x - nu;
+#include "mx_gemm_tile.cuh"
+  } else {
+    constexpr bool BMN = false;
+    constexpr int AK = A_BF16_K, MH = MX, OUT = OUT_T;
+    const GemmMaps& maps = xm;
+    const GemmArgs& g = xa;
+    const int block = blockIdx.x - nu - nv;
+#include "mx_gemm_tile.cuh"
+  }
 }
 
 // A sum over splits, and where it goes: a bf16 pair with rows padded to `pitch`, or bf16.
