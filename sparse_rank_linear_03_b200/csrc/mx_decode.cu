@@ -456,6 +456,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
               }
             }
           }
+          tc::fence_async_smem();  // the loads are done before a copy may overwrite what they read
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&empty[s]);
           if (++s == a.stages) {

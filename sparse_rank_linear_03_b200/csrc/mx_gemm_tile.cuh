@@ -203,8 +203,7 @@
           for (int b = 0; b < MH; ++b)  // padding bytes after the last block count as 0
             blk[b].e = kk * 2 + half0 + b < g.nb ? (pair >> (8 * (half0 + b))) & 0xFFu : 0u;
         }
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&taken[cs]);
+        const int read = cs;
         cs += 2;
         if (cs >= g.codes) {
           cs -= g.codes;
@@ -217,9 +216,14 @@
         if (!g_wait(&empty[s], ph, abrt)) break;
 #pragma unroll
         for (int b = 0; b < MH; ++b) widen(blk[b], smem32 + s * kStage, half0 + b);
+        // The fence also orders the reads of the codes before the copy that may overwrite them: an
+        // arrival alone was seen to overtake loads still under way.
         tc::fence_async_smem();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&full[s]);
+        if (lane == 0) {
+          tc::mbar_arrive(&full[s]);
+          tc::mbar_arrive(&taken[read]);
+        }
         s += 2;
         if (s >= g.stages) {
           s -= g.stages;

@@ -228,6 +228,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
 #pragma unroll
         for (int q = 0; q < 8; ++q)
           if (q < ncols) wn[q] = src[kM + min(q * 32 + lane, g.BN - 1)];
+        tc::fence_async_smem();  // the loads are done before a copy may overwrite what they read
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sempty[sr]);
         if (++sr == F_SRING) {

@@ -279,3 +279,34 @@ def test_apply_scales_at_the_ends(hsl, T):
     t = tensor(tokens(T, n, 5), "bf16")
     want, mag = mx.apply(d, f64(t)), mx.apply(np.abs(d), np.abs(f64(t)))
     close(hsl.mx4_apply(D, t), want, mag, n, "bf16", n * 2.0 ** -140)
+
+
+@pytest.mark.parametrize("op,T,m,n,r", [
+    ("apply", 1, 4096, 4096, 0), ("apply", 16, 4096, 4096, 0), ("apply", 64, 11008, 4096, 0),
+    ("apply", 200, 11008, 4096, 0), ("apply", 2048, 11008, 4096, 0), ("apply_t", 64, 4096, 11008, 0),
+    ("apply_t", 200, 4096, 11008, 0), ("apply_t", 2048, 4096, 11008, 0), ("matmul", 64, 4096, 8192, 0),
+    ("matmul", 2048, 11008, 8192, 0), ("factor_grad", 500, 4096, 4096, 128),
+    ("factor_grad", 2048, 11008, 4096, 256)])
+def test_every_call_gives_the_same_bits(hsl, op, T, m, n, r):
+    """Calls one behind the other at sizes that fill the device: sums are in a fixed order, so a
+    copy that overtakes a reader, or a tile that starts too early, shows as another bit."""
+    g = torch.Generator(device="cuda").manual_seed(T + m)
+    rand = lambda a, b: torch.randn(a, b, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    if op == "matmul":
+        A, B = hsl.mx_quantize(rand(T, n)), hsl.mx_quantize(rand(m, n))
+        call = lambda: (hsl.mx4_matmul(A, B),)  # noqa: E731
+    elif op == "factor_grad":
+        X, dY, U, V, add = hsl.mx_quantize(rand(T, n), "int8"), rand(T, m), rand(m, r), rand(n, r), rand(T, n)
+        call = lambda: hsl.mx8_factor_grad(X, dY, U, V, dx=True, add=add)  # noqa: E731
+    else:
+        D = hsl.mx_quantize(rand(m, n))
+        x = rand(T, n if op == "apply" else m)
+        call = lambda: (getattr(hsl, "mx4_" + op)(D, x),)  # noqa: E731
+    first = call()
+    torch.cuda.synchronize()
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(40):
+        for a, b in zip(call(), first):
+            differ += (a != b).sum()
+    assert int(differ) == 0
+    hsl.mx_check()
