@@ -1,6 +1,7 @@
 // C ABI of the microscaled operators (declared in include/hsl.h): argument checks,
 // workspace layout and the choice of kernel.  Nothing is kept between calls: all
 // data, the workspace included, is the caller's.
+#include <algorithm>
 #include <cstring>
 #include <string>
 
@@ -51,6 +52,7 @@ MxOperand operand(const hsl_mx* q, bool trans) {
   o.spitch = mx::scale_pitch(q->cols);
   o.kind = q->elem == HSL_MX_INT8 ? MxOperand::kInt8 : MxOperand::kE2M1;
   o.trans = trans ? 1 : 0;
+  o.vec = 0;
   return o;
 }
 MxOperand operand(const void* p, hsl_dtype dt, int64_t pitch, bool trans) {
@@ -61,18 +63,37 @@ MxOperand operand(const void* p, hsl_dtype dt, int64_t pitch, bool trans) {
   o.spitch = 0;
   o.kind = dt == HSL_F32 ? MxOperand::kF32 : MxOperand::kBF16;
   o.trans = trans ? 1 : 0;
+  o.vec = dt == HSL_F32 && pitch % 4 == 0 && aligned16(p) ? 1 : 0;
   return o;
 }
 
+// Scratch of the fp32 kernels: Z and G of the factor gradients, then a product's K ranges.
+size_t zg_bytes(int64_t T, int64_t r) { return size_t(round_up(2 * T * r * 4, 256)); }
+size_t simt_bytes(hsl_mx_op op, int64_t T, int64_t m, int64_t n, int64_t r) {
+  switch (op) {
+    case HSL_MX_OP_APPLY: return mx_simt_workspace(T, m, n);
+    case HSL_MX_OP_APPLY_T: return mx_simt_workspace(T, n, m);
+    case HSL_MX_OP_MATMUL: return mx_simt_workspace(T, m, n);
+    default: break;
+  }
+  if (r == 0) return 0;
+  const size_t parts[] = {mx_simt_workspace(T, r, n), mx_simt_workspace(T, r, m), mx_simt_workspace(m, r, T),
+                          mx_simt_workspace(n, r, T), mx_simt_workspace(T, n, r)};
+  return zg_bytes(T, r) + *std::max_element(parts, parts + 5);
+}
+// Whether a call takes the tensor-core kernels is decided by its sizes here and by the alignment of its
+// pointers at the call, so the scratch holds either.
 size_t workspace_bytes(hsl_mx_op op, int64_t T, int64_t m, int64_t n, int64_t r, hsl_dtype dt) {
-  const size_t simt = op == HSL_MX_OP_FACTOR_GRAD ? size_t(2 * T * r * 4) : 0;
-  if (dt == HSL_F32 || T == 0 || m == 0) return simt;
-  size_t tc = 0;
+  if (T == 0 || m == 0) return simt_bytes(op, T, m, n, r);
+  if (op == HSL_MX_OP_MATMUL) return mx_matmul_supported() ? 0 : simt_bytes(op, T, m, n, r);
+  if (dt == HSL_F32) {
+    if (op == HSL_MX_OP_APPLY && T <= kMxDecodeF32Max) return 0;
+    return simt_bytes(op, T, m, n, r);
+  }
   if (op == HSL_MX_OP_APPLY && mx_decode_fits(T, m, n)) return mx_decode_workspace(T, n);
-  if (op == HSL_MX_OP_APPLY || op == HSL_MX_OP_APPLY_T)
-    tc = mx_gemm_apply_workspace(op == HSL_MX_OP_APPLY_T, T, m, n);
-  if (op == HSL_MX_OP_FACTOR_GRAD && r > 0) tc = mx_gemm_grad_workspace(T, m, n, r);
-  return simt > tc ? simt : tc;
+  const size_t tc = op == HSL_MX_OP_FACTOR_GRAD ? (r > 0 ? mx_gemm_grad_workspace(T, m, n, r) : 0)
+                                                : mx_gemm_apply_workspace(op == HSL_MX_OP_APPLY_T, T, m, n);
+  return std::max(tc, simt_bytes(op, T, m, n, r));
 }
 
 hsl_status check_workspace(const void* ws, size_t have, size_t need) {
@@ -153,7 +174,7 @@ hsl_status hsl_mx4_apply(const hsl_mx* D, const void* X, const void* add, void* 
   if (dtype == HSL_F32 && batch <= kMxDecodeF32Max)
     return mx_decode_f32_run(operand(D, false), D->rows, D->cols, X, add, Y, batch, s);
   return mx_simt_run(operand(X, dtype, D->cols, false), operand(D, false), batch, D->rows, D->cols,
-                     add, Y, dtype, s);
+                     add, Y, dtype, ws, s);
 }
 
 hsl_status hsl_mx4_apply_t(const hsl_mx* D, const void* dY, const void* add, void* dX, int64_t batch,
@@ -171,7 +192,7 @@ hsl_status hsl_mx4_apply_t(const hsl_mx* D, const void* dY, const void* add, voi
   if (dtype == HSL_BF16 && D->rows > 0 && mx_gemm_supported(dY))
     return mx_gemm_apply_run(true, operand(D, true), D->rows, D->cols, dY, add, dX, batch, ws, s);
   return mx_simt_run(operand(dY, dtype, D->rows, false), operand(D, true), batch, D->cols, D->rows,
-                     add, dX, dtype, s);
+                     add, dX, dtype, ws, s);
 }
 
 hsl_status hsl_mx4_matmul(const hsl_mx* A, const hsl_mx* B, const void* add, void* Y, hsl_dtype dtype,
@@ -189,7 +210,7 @@ hsl_status hsl_mx4_matmul(const hsl_mx* A, const hsl_mx* B, const void* add, voi
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (mx_matmul_supported())
     return mx_matmul_run(operand(A, false), A->rows, operand(B, false), B->rows, A->cols, add, Y, dtype, s);
-  return mx_simt_run(operand(A, false), operand(B, false), A->rows, B->rows, A->cols, add, Y, dtype, s);
+  return mx_simt_run(operand(A, false), operand(B, false), A->rows, B->rows, A->cols, add, Y, dtype, ws, s);
 }
 
 hsl_status hsl_mx8_factor_grad(const hsl_mx* X, const void* dY, int64_t m, const void* U,
@@ -211,20 +232,21 @@ hsl_status hsl_mx8_factor_grad(const hsl_mx* X, const void* dY, int64_t m, const
   if (dtype == HSL_BF16 && T > 0 && mx_gemm_supported(dY) && mx_gemm_supported(U) && mx_gemm_supported(V))
     return mx_gemm_grad_run(operand(X, false), T, n, dY, m, U, V, r, add, dU, dV, dX, ws, s);
   float* Z = static_cast<float*>(ws);
-  float* G = Z + T * r;
+  float* G = Z ? Z + T * r : nullptr;
+  void* part = Z ? static_cast<char*>(ws) + zg_bytes(T, r) : nullptr;
   const MxOperand x = operand(X, false), xt = operand(X, true);
-  if (hsl_status e = mx_simt_run(x, operand(V, dtype, r, true), T, r, n, nullptr, Z, HSL_F32, s)) return e;
+  if (hsl_status e = mx_simt_run(x, operand(V, dtype, r, true), T, r, n, nullptr, Z, HSL_F32, part, s)) return e;
   if (hsl_status e = mx_simt_run(operand(dY, dtype, m, false), operand(U, dtype, r, true), T, r, m,
-                                 nullptr, G, HSL_F32, s))
+                                 nullptr, G, HSL_F32, part, s))
     return e;
   if (hsl_status e = mx_simt_run(operand(dY, dtype, m, true), operand(Z, HSL_F32, r, true), m, r, T,
-                                 nullptr, dU, dtype, s))
+                                 nullptr, dU, dtype, part, s))
     return e;
-  if (hsl_status e = mx_simt_run(xt, operand(G, HSL_F32, r, true), n, r, T, nullptr, dV, dtype, s))
+  if (hsl_status e = mx_simt_run(xt, operand(G, HSL_F32, r, true), n, r, T, nullptr, dV, dtype, part, s))
     return e;
   if (!dX) return HSL_OK;
   return mx_simt_run(operand(G, HSL_F32, r, false), operand(V, dtype, r, false), T, n, r, add, dX, dtype,
-                     s);
+                     part, s);
 }
 
 hsl_status hsl_mx_check(hsl_stream stream) {

@@ -17,30 +17,17 @@ struct MxOperand {
   int64_t spitch;         // scale bytes per stored row
   int32_t kind;
   int32_t trans;
+  int32_t vec;            // f32: rows start on 16 bytes
 };
-
-// The operand's rows i0, i0 + 1, ...; i0 a multiple of 32 for transposed blocks.
-inline MxOperand mx_operand_from(const MxOperand& o, int64_t i0) {
-  MxOperand r = o;
-  const char* p = static_cast<const char*>(o.p);
-  const int64_t esize = o.kind == MxOperand::kF32 ? 4 : o.kind == MxOperand::kBF16 ? 2 : 1;
-  if (!o.trans) {
-    r.p = p + i0 * o.pitch * esize;
-    if (o.scales) r.scales = o.scales + i0 * o.spitch;
-  } else {
-    r.p = p + (o.kind == MxOperand::kE2M1 ? i0 / 2 : i0 * esize);
-    if (o.scales) r.scales = o.scales + i0 / 32;
-  }
-  return r;
-}
 
 hsl_status mx_quantize_run(const void* X, hsl_dtype dtype, int64_t rows, int64_t cols, bool int8,
                            void* codes, void* scales, cudaStream_t s);
 hsl_status mx_dequantize_run(const void* codes, const void* scales, int64_t rows, int64_t cols,
                              bool int8, void* X, hsl_dtype dtype, cudaStream_t s);
-// C[M][N] (row pitch N) = add + A Bᵀ in fp32
+// C[M][N] (row pitch N) = add + A Bᵀ in fp32; `part` holds mx_simt_workspace bytes
+size_t mx_simt_workspace(int64_t M, int64_t N, int64_t K);
 hsl_status mx_simt_run(const MxOperand& A, const MxOperand& B, int64_t M, int64_t N, int64_t K,
-                       const void* add, void* C, hsl_dtype cdt, cudaStream_t s);
+                       const void* add, void* C, hsl_dtype cdt, void* part, cudaStream_t s);
 
 // Tensor-core products (mx_gemm.cu, mx_grad.cu), bf16: X, dY, U, V on 16 bytes (mx_gemm_supported)
 bool mx_gemm_supported(const void* X);
