@@ -464,6 +464,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
             ph ^= 1;
           }
         }
+        if (slot == 0 && local) dc_sync();  // the last sums are read
         float* out = red + (slot * DC_WARPS + warp) * cols * DC_RED_PITCH + g;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -478,16 +479,21 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         ++slot;
         if (slot < slots && grp + int(gridDim.x) < groups) continue;
         dc_sync();
-        for (int e = threadIdx.x; e < kRows * a.T * a.tps * slot; e += DC_WARPS * 32) {
+        // half of a warp per 16 rows, so that every warp has its share of few outputs; the warps go on
+        // to the next row tile as they finish
+        for (int e = warp * 16 + (lane & 15) + (lane >> 4) * (DC_WARPS * 16); e < kRows * a.T * a.tps * slot;
+             e += DC_WARPS * 32) {
           const int i = e & 15, tile = (e >> 4) / a.T, tok = (e >> 4) - tile * a.T;
           const int q = a.tps == 1 ? tile : tile / a.tps, ts = tile - q * a.tps;
           const int row = ((grp - (slot - 1 - q) * int(gridDim.x)) * a.tps + ts) * kRows + i;
           if (row >= a.m) continue;
+          const int64_t at = int64_t(tok) * a.m + row;
+          const float plus = last && a.add ? __bfloat162float(a.add[at]) : 0.f;
           const float* p = red + ((q * DC_WARPS + ts * a.su) * cols + tok * per_tok) * DC_RED_PITCH + i;
           float v = 0.f;
           for (int c = per_tok - 1; c >= 0; --c) {
             float col = p[c * DC_RED_PITCH];
-#pragma unroll 4
+#pragma unroll 8
             for (int w = 1; w < a.su; ++w) col += p[(w * cols + c) * DC_RED_PITCH];
             v += col * unscale[0][tok * per_tok + c] * unscale[1][tok * per_tok + c];
           }
@@ -497,11 +503,9 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
             *keep = v;
             continue;
           }
-          const int64_t at = int64_t(tok) * a.m + row;
-          if (a.add) v += __bfloat162float(a.add[at]);
+          if (a.add) v += plus;
           a.Y[at] = __float2bfloat16_rn(v);
         }
-        dc_sync();
         local += slot;
         slot = 0;
       }

@@ -271,13 +271,16 @@ GemmShape shape_of(int ak, int64_t M, int64_t N, int64_t K, bool bmn, int terms,
   }
   s.BN = int(round_up((N + ntn - 1) / ntn, 16));
   if (t2 * ntn < 148) {
-    // Fewer tiles than SMs: K is split where the caller has room for partial sums, which pass through
-    // HBM twice, at about 3500 bytes per cycle.
+    // Fewer tiles than SMs: K is split where the caller has room for partial sums and where that saves
+    // more than the launch that adds them up, about 6000 cycles, and their way through HBM
+    // and back, at about 3500 bytes per cycle.
     auto cost = [&](int mh, int64_t* splits) {
       const int64_t tiles = (mh == 2 ? t2 : t1) * ntn;
+      const int64_t per = kblock_cycles(ak, terms, mh, s.BN), whole = nk * per * ((tiles + 147) / 148);
       *splits = may_split ? std::max<int64_t>(1, std::min<int64_t>(148 / tiles, nk / 4)) : 1;
-      return (nk + *splits - 1) / *splits * kblock_cycles(ak, terms, mh, s.BN) * ((tiles * *splits + 147) / 148) +
-             (*splits > 1 ? *splits * M * N * 8 / 3500 : 0);
+      const int64_t cut = (nk + *splits - 1) / *splits * per + 6000 + *splits * M * N * 8 / 3500;
+      if (*splits == 1 || whole <= cut) *splits = 1;
+      return *splits == 1 ? whole : cut;
     };
     int64_t s1 = 1, s2 = 1;
     const int64_t c1 = cost(1, &s1), c2 = cost(2, &s2);
