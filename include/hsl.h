@@ -321,7 +321,8 @@ hsl_status hsl_set_permutation(hsl_handle h, const int32_t* row_order, const int
  * the sizes of a call (16-byte aligned; contents need not survive the call, and
  * calls that may overlap need one each).  The device of the pointers and the
  * stream must be current.  All are asynchronous on s, allocate nothing and can
- * be captured.  Rows, columns and batches are at most 2^30. */
+ * be captured.  Outputs and scratch may not overlap each other or an input (but
+ * `add` may be the output itself).  Rows, columns and batches are at most 2^30. */
 typedef enum { HSL_MX_E2M1 = 0, HSL_MX_INT8 = 1 } hsl_mx_elem;
 typedef struct {
   const void* codes;
@@ -389,7 +390,9 @@ hsl_status hsl_mx4_matmul(const hsl_mx* A, const hsl_mx* B, const void* add, voi
  * X [T][n] blocks (T = X.rows; T = 0 writes zeros to dU and dV), dY [T][m],
  * U and dU [m][r], V and dV [n][r], dX and add [T][n] of dtype; dX may be NULL
  * (then add must be), add may be NULL or dX itself.  1 ≤ r ≤ 256.  Z and G are
- * kept to 16 bits of significand or more, sums in fp32.
+ * kept to 16 bits of significand or more, sums in fp32.  With an infinity in dY,
+ * U or V, what is infinite by the formulas may come out as a NaN (and nothing else
+ * is touched).
  * [HSS] §Implementation and operational patterns, backward pass (the gradients
  * of U and V, as derived from the forward decomposition). */
 hsl_status hsl_mx8_factor_grad(const hsl_mx* X, const void* dY, int64_t m, const void* U,

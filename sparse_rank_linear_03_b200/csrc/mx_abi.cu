@@ -2,8 +2,8 @@
 // workspace layout and the choice of kernel.  Nothing is kept between calls: all
 // data, the workspace included, is the caller's.
 #include <algorithm>
-#include <cstring>
-#include <string>
+#include <cstdio>
+#include <initializer_list>
 
 #include "common.cuh"
 #include "internal.h"
@@ -17,6 +17,11 @@ hsl_status bad_arg(const char* why) {
   set_message(why);
   return HSL_ERR_INVALID_ARG;
 }
+hsl_status bad_arg(const char* what, const char* why) {
+  char text[96];
+  std::snprintf(text, sizeof(text), "%s%s", what, why);
+  return bad_arg(text);
+}
 hsl_status not_supported(const char* why) {
   set_message(why);
   return HSL_ERR_UNSUPPORTED;
@@ -29,20 +34,43 @@ bool size_ok(int64_t v) { return v >= 1 && v <= kMaxSize; }
 
 // The checks that every operator makes of a matrix in blocks.
 hsl_status check_mx(const hsl_mx* q, int elem, const char* what) {
-  if (!q) return bad_arg((std::string(what) + " is NULL").c_str());
-  if (q->elem != HSL_MX_E2M1 && q->elem != HSL_MX_INT8)
-    return bad_arg((std::string(what) + ": unknown element type").c_str());
+  if (!q) return bad_arg(what, " is NULL");
+  if (q->elem != HSL_MX_E2M1 && q->elem != HSL_MX_INT8) return bad_arg(what, ": unknown element type");
   if (elem >= 0 && int(q->elem) != elem)
-    return not_supported((std::string(what) + (elem == HSL_MX_E2M1 ? " must hold e2m1 blocks"
-                                                                     : " must hold int8 blocks")).c_str());
-  if (q->rows < 0 || q->rows > kMaxSize || !size_ok(q->cols))
-    return bad_arg((std::string(what) + ": rows or cols out of range").c_str());
-  if (q->rows > 0 && (!q->codes || !q->scales))
-    return bad_arg((std::string(what) + ": codes/scales is NULL").c_str());
+    return not_supported(elem == HSL_MX_E2M1 ? "the weights must hold e2m1 blocks"
+                                             : "the checkpoint must hold int8 blocks");
+  if (q->rows < 0 || q->rows > kMaxSize || !size_ok(q->cols)) return bad_arg(what, ": rows or cols out of range");
+  if (q->rows > 0 && (!q->codes || !q->scales)) return bad_arg(what, ": codes/scales is NULL");
   if (!aligned16(q->codes) || !aligned16(q->scales))
-    return bad_arg((std::string(what) + ": codes and scales must be 16-byte aligned").c_str());
+    return bad_arg(what, ": codes and scales must be 16-byte aligned");
   return HSL_OK;
 }
+
+// A call's outputs and scratch may not share memory with each other or with its inputs.
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+bool meet(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && x < y + uintptr_t(b.bytes) && y < x + uintptr_t(a.bytes);
+}
+hsl_status check_apart(std::initializer_list<Span> out, std::initializer_list<Span> in) {
+  for (const Span* o = out.begin(); o != out.end(); ++o) {
+    for (const Span* p = out.begin(); p != o; ++p)
+      if (meet(*o, *p)) return bad_arg("two outputs, or an output and the workspace, overlap");
+    for (const Span& i : in)
+      if (meet(*o, i)) return bad_arg("an output or the workspace overlaps an input");
+  }
+  return HSL_OK;
+}
+Span codes_of(const hsl_mx* q) {
+  return {q->codes, q->rows * mx::code_pitch(q->cols, q->elem == HSL_MX_INT8)};
+}
+Span scales_of(const hsl_mx* q) { return {q->scales, q->rows * mx::scale_pitch(q->cols)}; }
+int64_t size_of(hsl_dtype d) { return d == HSL_F32 ? 4 : 2; }
+// add may be the output itself
+Span add_of(const void* add, const void* out, int64_t bytes) { return {add == out ? nullptr : add, bytes}; }
 
 MxOperand operand(const hsl_mx* q, bool trans) {
   MxOperand o;
@@ -98,8 +126,11 @@ size_t workspace_bytes(hsl_mx_op op, int64_t T, int64_t m, int64_t n, int64_t r,
 
 hsl_status check_workspace(const void* ws, size_t have, size_t need) {
   if (need == 0) return HSL_OK;
-  if (!ws || have < need)
-    return bad_arg(("workspace too small: " + std::to_string(need) + " bytes needed").c_str());
+  if (!ws || have < need) {
+    char text[64];
+    std::snprintf(text, sizeof(text), "workspace too small: %zu bytes needed", need);
+    return bad_arg(text);
+  }
   if (!aligned16(ws)) return bad_arg("workspace must be 16-byte aligned");
   return HSL_OK;
 }
@@ -129,6 +160,7 @@ hsl_status hsl_mx_quantize(const void* X, hsl_dtype dtype, int64_t rows, int64_t
   if (hsl_status e = check_mx(&q, -1, "the result")) return e;
   if (rows == 0) return HSL_OK;
   if (!X) return bad_arg("X is NULL");
+  if (hsl_status e = check_apart({codes_of(&q), scales_of(&q)}, {{X, rows * cols * size_of(dtype)}})) return e;
   return mx_quantize_run(X, dtype, rows, cols, elem == HSL_MX_INT8, codes, scales,
                          static_cast<cudaStream_t>(s));
 }
@@ -139,6 +171,7 @@ hsl_status hsl_mx_dequantize(const hsl_mx* q, void* X, hsl_dtype dtype, hsl_stre
   if (hsl_status e = check_mx(q, -1, "the matrix")) return e;
   if (q->rows == 0) return HSL_OK;
   if (!X) return bad_arg("X is NULL");
+  if (hsl_status e = check_apart({{X, q->rows * q->cols * size_of(dtype)}}, {codes_of(q), scales_of(q)})) return e;
   return mx_dequantize_run(q->codes, q->scales, q->rows, q->cols, q->elem == HSL_MX_INT8, X, dtype,
                            static_cast<cudaStream_t>(s));
 }
@@ -163,8 +196,11 @@ hsl_status hsl_mx4_apply(const hsl_mx* D, const void* X, const void* add, void* 
   if (batch < 0 || batch > kMaxSize) return bad_arg("batch out of range");
   if (batch == 0 || D->rows == 0) return HSL_OK;
   if (!X || !Y) return bad_arg("X/Y is NULL");
-  if (hsl_status e = check_workspace(ws, ws_bytes,
-                                     workspace_bytes(HSL_MX_OP_APPLY, batch, D->rows, D->cols, 0, dtype)))
+  const size_t need = workspace_bytes(HSL_MX_OP_APPLY, batch, D->rows, D->cols, 0, dtype);
+  if (hsl_status e = check_workspace(ws, ws_bytes, need)) return e;
+  const int64_t xb = batch * D->cols * size_of(dtype), yb = batch * D->rows * size_of(dtype);
+  if (hsl_status e = check_apart({{Y, yb}, {ws, int64_t(need)}},
+                                 {{X, xb}, add_of(add, Y, yb), codes_of(D), scales_of(D)}))
     return e;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == HSL_BF16 && mx_decode_fits(batch, D->rows, D->cols))
@@ -185,8 +221,11 @@ hsl_status hsl_mx4_apply_t(const hsl_mx* D, const void* dY, const void* add, voi
   if (batch < 0 || batch > kMaxSize) return bad_arg("batch out of range");
   if (batch == 0) return HSL_OK;
   if (!dX || (D->rows > 0 && !dY)) return bad_arg("dY/dX is NULL");
-  if (hsl_status e = check_workspace(ws, ws_bytes,
-                                     workspace_bytes(HSL_MX_OP_APPLY_T, batch, D->rows, D->cols, 0, dtype)))
+  const size_t need = workspace_bytes(HSL_MX_OP_APPLY_T, batch, D->rows, D->cols, 0, dtype);
+  if (hsl_status e = check_workspace(ws, ws_bytes, need)) return e;
+  const int64_t xb = batch * D->cols * size_of(dtype), yb = batch * D->rows * size_of(dtype);
+  if (hsl_status e = check_apart({{dX, xb}, {ws, int64_t(need)}},
+                                 {{dY, yb}, add_of(add, dX, xb), codes_of(D), scales_of(D)}))
     return e;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == HSL_BF16 && D->rows > 0 && mx_gemm_supported(dY))
@@ -204,8 +243,11 @@ hsl_status hsl_mx4_matmul(const hsl_mx* A, const hsl_mx* B, const void* add, voi
   if (A->cols != B->cols) return bad_arg("A and B must have the same number of columns");
   if (A->rows == 0 || B->rows == 0) return HSL_OK;
   if (!Y) return bad_arg("Y is NULL");
-  if (hsl_status e = check_workspace(
-          ws, ws_bytes, workspace_bytes(HSL_MX_OP_MATMUL, A->rows, B->rows, A->cols, 0, dtype)))
+  const size_t need = workspace_bytes(HSL_MX_OP_MATMUL, A->rows, B->rows, A->cols, 0, dtype);
+  if (hsl_status e = check_workspace(ws, ws_bytes, need)) return e;
+  const int64_t yb = A->rows * B->rows * size_of(dtype);
+  if (hsl_status e = check_apart({{Y, yb}, {ws, int64_t(need)}},
+                                 {add_of(add, Y, yb), codes_of(A), scales_of(A), codes_of(B), scales_of(B)}))
     return e;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (mx_matmul_supported())
@@ -225,8 +267,12 @@ hsl_status hsl_mx8_factor_grad(const hsl_mx* X, const void* dY, int64_t m, const
   if (add && !dX) return bad_arg("add without dX");
   const int64_t T = X->rows, n = X->cols;
   if (T > 0 && !dY) return bad_arg("dY is NULL");
-  if (hsl_status e = check_workspace(ws, ws_bytes,
-                                     workspace_bytes(HSL_MX_OP_FACTOR_GRAD, T, m, n, r, dtype)))
+  const size_t need = workspace_bytes(HSL_MX_OP_FACTOR_GRAD, T, m, n, r, dtype);
+  if (hsl_status e = check_workspace(ws, ws_bytes, need)) return e;
+  const int64_t eb = size_of(dtype), ub = m * r * eb, vb = n * r * eb, xb = T * n * eb;
+  if (hsl_status e = check_apart(
+          {{dU, ub}, {dV, vb}, {dX, xb}, {ws, int64_t(need)}},
+          {{dY, T * m * eb}, {U, ub}, {V, vb}, add_of(add, dX, xb), codes_of(X), scales_of(X)}))
     return e;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == HSL_BF16 && T > 0 && mx_gemm_supported(dY) && mx_gemm_supported(U) && mx_gemm_supported(V))

@@ -15,7 +15,11 @@ def view(codes=P, scales=P, rows=8, cols=64, elem=0):
     return hsl._MXView(codes, scales, rows, cols, elem)
 
 
+_kept = []   # views stay alive behind their addresses
+
+
 def ref(v):
+    _kept.append(v)
     return ctypes.addressof(v) if v is not None else None
 
 
@@ -123,6 +127,47 @@ def test_factor_grad_refusals():
     assert f(wb=16) == INVALID
     assert f(ws=P + 4) == INVALID
     assert b"workspace" in lib.hsl_last_message()
+
+
+def test_overlaps_are_refused():
+    """Spans that touch are fine, a shared byte is not; `add` may be the output itself."""
+    K = 1 << 20                                          # far apart
+    d = lambda **k: view(codes=4 * K, scales=8 * K, **k)  # noqa: E731   8 rows x 64: 256 + 128 bytes
+    b = ctypes.c_size_t()
+
+    def apart(status):
+        # (spans that are apart end in a launch that finds no device, or no tensor map: not here)
+        assert status == INVALID and b"overlap" in lib.hsl_last_message()
+
+    # 2 x 64 bf16 in, 2 x 8 out
+    assert lib.hsl_mx_workspace(0, 2, 8, 64, 0, 1, ctypes.byref(b)) == OK
+    for fn, xb, yb in ((lib.hsl_mx4_apply, 256, 32), (lib.hsl_mx4_apply_t, 32, 256)):
+        f = lambda X=16 * K, add=None, Y=32 * K, ws=64 * K: fn(  # noqa: E731
+            ref(d()), X, add, Y, 2, 1, ws, 1 << 40, None)
+        apart(f(Y=16 * K))
+        apart(f(Y=16 * K + xb - 2))
+        apart(f(Y=16 * K - yb + 2))
+        apart(f(add=32 * K + 2))                         # neither the output nor apart from it
+        apart(f(Y=4 * K + 16))
+        apart(f(Y=8 * K + 126))
+    f = lambda Y=32 * K, add=None: lib.hsl_mx4_matmul(  # noqa: E731
+        ref(d()), ref(view(codes=5 * K, scales=9 * K)), add, Y, 1, 64 * K, 1 << 40, None)
+    apart(f(Y=5 * K))
+    apart(f(Y=9 * K - 126))
+    apart(f(add=32 * K + 16))
+    apart(lib.hsl_mx_quantize(4 * K - 16, 1, 8, 64, 0, 4 * K, 8 * K, None))
+    apart(lib.hsl_mx_quantize(16 * K, 1, 8, 64, 0, 4 * K, 4 * K + 240, None))
+    apart(lib.hsl_mx_dequantize(ref(d()), 8 * K, 1, None))
+
+    def g(dY=16 * K, U=20 * K, V=24 * K, add=None, dU=32 * K, dV=36 * K, dX=None, ws=64 * K):
+        return lib.hsl_mx8_factor_grad(ref(d(elem=1)), dY, 8, U, V, 4, add, dU, dV, dX, 1, ws, 1 << 40, None)
+    apart(g(dU=20 * K))                                  # the factor itself
+    apart(g(dV=24 * K + 16))
+    apart(g(dU=36 * K))                                  # both gradients in one place
+    apart(g(dX=16 * K))
+    apart(g(dX=40 * K, add=40 * K + 4))
+    apart(g(ws=20 * K))
+    apart(g(ws=32 * K - 256))
 
 
 def test_binding_refuses_before_the_library():
