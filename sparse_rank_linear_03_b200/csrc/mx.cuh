@@ -91,13 +91,5 @@ __device__ __forceinline__ uint2 widen_int8(uint32_t w, uint32_t scale) {
   return v;
 }
 
-// The fp32 value of element j of a row, given the row's codes and scales.
-template <bool kInt8>
-__device__ __forceinline__ float value(const uint8_t* codes, const uint8_t* scales, int64_t j) {
-  const float s = scale_f32(scales[j >> 5]);
-  if (kInt8) return float(reinterpret_cast<const int8_t*>(codes)[j]) * 0.015625f * s;
-  return e2m1_f32((codes[j >> 1] >> ((j & 1) * 4)) & 15u) * s;
-}
-
 }  // namespace mx
 }  // namespace hsl

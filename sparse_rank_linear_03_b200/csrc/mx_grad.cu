@@ -80,13 +80,19 @@ __device__ __forceinline__ void sum_job(const SumJob& j, int64_t e) {
 #pragma unroll
   for (int q = 0; q < V; ++q) v[q] = 0.f;
   if (c < j.n) sum_splits<V>(j.part, j.splits, j.rows * j.n, row * j.n + c, v);  // (V = 4: n = pitch)
-  store_bf<V>(j.hi + e, v);
   if (j.lo) {
     float low[V];
 #pragma unroll
-    for (int q = 0; q < V; ++q) low[q] = v[q] - __bfloat162float(__float2bfloat16_rn(v[q]));
+    for (int q = 0; q < V; ++q) {
+      // (an infinity has no low part; a finite sum keeps a finite high part)
+      float hi = __bfloat162float(__float2bfloat16_rn(v[q]));
+      if (isinf(hi)) hi = __bfloat162float(__float2bfloat16_rz(v[q]));
+      low[q] = isinf(hi) ? 0.f : v[q] - hi;
+      v[q] = hi;
+    }
     store_bf<V>(j.lo + e, low);
   }
+  store_bf<V>(j.hi + e, v);
 }
 template <int V>
 __global__ void __launch_bounds__(256)

@@ -120,7 +120,8 @@ __global__ void __launch_bounds__(256)
     k_mx_simt(const MxOperand A, const MxOperand B, int64_t M, int64_t N, int64_t K, int64_t krange, const TO* add,
               TO* C, float* __restrict__ part) {
   __shared__ __align__(16) float sa[S_BK][68], sb[S_BK][68];
-  const int64_t i0 = int64_t(blockIdx.x) * S_BM, j0 = int64_t(blockIdx.y) * S_BN;
+  const unsigned tm = unsigned((M + S_BM - 1) / S_BM);
+  const int64_t i0 = int64_t(blockIdx.x % tm) * S_BM, j0 = int64_t(blockIdx.x / tm) * S_BN;
   const int64_t kbeg = int64_t(blockIdx.z) * krange, kend = min(K, kbeg + krange);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   float acc[4][4] = {}, sum[4][4] = {};
@@ -201,7 +202,8 @@ hsl_status run(const MxOperand& A, const MxOperand& B, int64_t M, int64_t N, int
   const int ranges = part ? ranges_of(M, N, K) : 1;
   const int64_t krange = ranges > 1 ? ((K + ranges - 1) / ranges + S_BK - 1) / S_BK * S_BK : K;
   const int64_t nz = ranges > 1 ? (K + krange - 1) / krange : 1;
-  const dim3 grid(unsigned((M + S_BM - 1) / S_BM), unsigned((N + S_BN - 1) / S_BN), unsigned(nz));
+  // (tiles in one dimension: the others end at 65535)
+  const dim3 grid(unsigned((M + S_BM - 1) / S_BM * ((N + S_BN - 1) / S_BN)), 1, unsigned(nz));
   note_launch();
   if (nz == 1) {
     k_mx_simt<KA, KB, TO, false><<<grid, 256, 0, s>>>(A, B, M, N, K, K, add, C, nullptr);
@@ -229,10 +231,6 @@ size_t mx_simt_workspace(int64_t M, int64_t N, int64_t K) {
 hsl_status mx_simt_run(const MxOperand& A, const MxOperand& B, int64_t M, int64_t N, int64_t K,
                        const void* add, void* C, hsl_dtype cdt, void* part, cudaStream_t s) {
   if (M <= 0 || N <= 0) return HSL_OK;
-  if ((N + S_BN - 1) / S_BN > 65535) {
-    set_message("this fp32 product takes at most 65535 x 64 columns");
-    return HSL_ERR_UNSUPPORTED;
-  }
   float* w = mx_simt_workspace(M, N, K) ? static_cast<float*>(part) : nullptr;
   const int ka = kind_of(A.kind, A.trans != 0), kb = kind_of(B.kind, B.trans != 0);
   if (cdt == HSL_F32) {

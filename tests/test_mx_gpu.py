@@ -267,6 +267,42 @@ def test_apply_infinities_and_nan(hsl, T):
     assert np.isnan(y[:, 3]).all() and np.isfinite(np.delete(y, 3, axis=1)).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,m,n,r", [(1, 24, 40, 8), (70, 136, 200, 24)])
+def test_factor_grad_infinities(hsl, T, m, n, r, dtype):
+    """Infinities in U, V and dY: exactly those gradients are not finite that are not by the
+    formulas (where the formula has a NaN or an infinity, either may come out), and those of
+    V alone, which Z alone carries to dU, come out as they are."""
+    X, x = blocks(hsl, 1 + np.abs(tokens(T, n, 1)), "int8")
+    rng = np.random.default_rng(2)
+    base = [1 + rng.random(s) for s in ((T, m), (m, r), (n, r))]
+    for at in ((0, (T - 1, 5)), (1, (7, 3)), (2, (4, 2))):
+        arrays = [a.copy() for a in base]
+        arrays[at[0]][at[1]] = -np.inf
+        dY, U, V = (tensor(a, dtype) for a in arrays)
+        with np.errstate(invalid="ignore"):
+            want = mx.factor_grad(x, f64(dY), f64(U), f64(V), None)
+        got = [f64(g) for g in hsl.mx8_factor_grad(X, dY, U, V, dx=True)]
+        for g, w in zip(got, want):
+            assert np.array_equal(np.isfinite(g), np.isfinite(w))
+        if at[0] == 2:
+            assert np.array_equal(np.isinf(got[0]), np.isinf(want[0])) and (got[0][:, 2] == -np.inf).all()
+    hsl.mx_check()
+
+
+def test_f32_product_with_millions_of_columns(hsl):
+    """More 64-column tiles than one grid dimension of 65535 holds."""
+    m, n, T = 65536 * 64 + 70, 32, 65
+    g = torch.Generator(device="cuda").manual_seed(3)
+    W = torch.randn(m, n, generator=g, device="cuda")
+    D = hsl.mx_quantize(W)
+    x = torch.randn(T, n, generator=g, device="cuda")
+    y = hsl.mx4_apply(D, x)
+    d = f64(hsl.mx_dequantize(D, "f32")[-5000:])
+    want, mag = mx.apply(d, f64(x)), mx.apply(np.abs(d), np.abs(f64(x)))
+    close(y[:, -5000:], want, mag, n, "f32")
+
+
 @pytest.mark.parametrize("T", [1, 6, 40])
 def test_apply_scales_at_the_ends(hsl, T):
     """Blocks whose power of two is very small or very large."""
