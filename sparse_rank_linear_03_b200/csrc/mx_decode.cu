@@ -677,17 +677,8 @@ hsl_status mx_decode_run(const MxOperand& D, int64_t m, int64_t n, const void* X
                                                        static_cast<int2*>(ws),
                                                        reinterpret_cast<uint4*>(static_cast<char*>(ws) + 256));
   if (hsl_status e = cuda_fail(cudaGetLastError(), "4-bit decode launch")) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(p.grid));
-  cfg.blockDim = dim3(DC_THREADS);
-  cfg.dynamicSmemBytes = size_t(p.bytes);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cuda_fail(cudaLaunchKernelEx(&cfg, fn, maps, a), "4-bit decode launch");
+  return cuda_fail(launch_chained(fn, true, dim3(unsigned(p.grid)), DC_THREADS, size_t(p.bytes), s, maps, a),
+                   "4-bit decode launch");
 }
 
 cudaError_t mx_decode_error_word(uint32_t** p) {

@@ -8,6 +8,7 @@ template <int V>
 __global__ void __launch_bounds__(256)
     k_mx_reduce(const float* __restrict__ part, int splits, int64_t count, const __nv_bfloat16* add,
                 __nv_bfloat16* C) {
+  pdl_wait();
   const int64_t e = (int64_t(blockIdx.x) * 256 + threadIdx.x) * V;
   if (e >= count) return;
   float v[V];
@@ -23,10 +24,10 @@ hsl_status reduce_run(const float* part, int splits, int64_t count, const __nv_b
                       cudaStream_t s) {
   note_launch();
   if (count % 4 == 0 && reinterpret_cast<uintptr_t>(C) % 8 == 0)
-    k_mx_reduce<4><<<blocks_of(count / 4), 256, 0, s>>>(part, splits, count, add, C);
-  else
-    k_mx_reduce<1><<<blocks_of(count), 256, 0, s>>>(part, splits, count, add, C);
-  return cuda_fail(cudaGetLastError(), "split sum launch");
+    return cuda_fail(launch_chained(k_mx_reduce<4>, true, dim3(blocks_of(count / 4)), 256, 0, s, part, splits, count,
+                                    add, C), "split sum launch");
+  return cuda_fail(launch_chained(k_mx_reduce<1>, true, dim3(blocks_of(count)), 256, 0, s, part, splits, count, add, C),
+                   "split sum launch");
 }
 }  // namespace
 
@@ -76,14 +77,14 @@ hsl_status mx_gemm_apply_run(bool trans, const MxOperand& D, int64_t m, int64_t 
       !block_maps(&maps, trans ? A_E2M1_M : A_E2M1_K, sh.MH, D, m))
     return map_failed();
   if (sh.splits > 1) {
-    if (hsl_status e = trans ? launch_gemm<A_E2M1_M, false, 1, OUT_T_PART>(sh.MH, maps, g, s)
-                             : launch_gemm<A_E2M1_K, false, 1, OUT_T_PART>(sh.MH, maps, g, s))
+    if (hsl_status e = trans ? launch_gemm<A_E2M1_M, false, 1, OUT_T_PART>(sh.MH, maps, g, K % 8 != 0, s)
+                             : launch_gemm<A_E2M1_K, false, 1, OUT_T_PART>(sh.MH, maps, g, K % 8 != 0, s))
       return e;
     return reduce_run(g.part, sh.splits, T * M, g.add, g.C, s);
   }
   if (!out_maps(&maps, &g, T, M, sh.MH)) return map_failed();
-  return trans ? launch_gemm<A_E2M1_M, false, 1, OUT_T>(sh.MH, maps, g, s)
-               : launch_gemm<A_E2M1_K, false, 1, OUT_T>(sh.MH, maps, g, s);
+  return trans ? launch_gemm<A_E2M1_M, false, 1, OUT_T>(sh.MH, maps, g, K % 8 != 0, s)
+               : launch_gemm<A_E2M1_K, false, 1, OUT_T>(sh.MH, maps, g, K % 8 != 0, s);
 }
 
 cudaError_t mx_gemm_error_word(uint32_t** p) {

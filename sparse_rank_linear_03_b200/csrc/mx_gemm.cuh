@@ -203,6 +203,7 @@ __device__ __forceinline__ void store_bf(__nv_bfloat16* p, const float (&v)[V]) 
 __global__ void __launch_bounds__(256)
     k_mx_pad_rows(const uint16_t* __restrict__ src, int64_t rows, int n, int pitch,
                   uint16_t* __restrict__ dst) {
+  pdl_trigger();
   const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
   if (e >= rows * pitch) return;
   const int64_t row = e / pitch;
@@ -301,19 +302,19 @@ int64_t tile_count(int mh, const GemmArgs& g) {
 }
 
 template <int AK, bool BMN, int TERMS, int MH, int OUT>
-hsl_status launch_gemm(const GemmMaps& maps, const GemmArgs& g, cudaStream_t s) {
+hsl_status launch_gemm(const GemmMaps& maps, const GemmArgs& g, bool chained, cudaStream_t s) {
   void (*fn)(const GemmMaps, const GemmArgs) = k_mx_gemm<AK, BMN, TERMS, MH, OUT>;
   const int bytes = tile_smem(AK, BMN, TERMS, MH, OUT == OUT_T, g);
   if (cudaError_t e = allow_dyn_smem(reinterpret_cast<const void*>(fn), bytes))
     return cuda_fail(e, "block product smem attribute");
   note_launch();
-  fn<<<unsigned(tile_count(MH, g)), G_THREADS, size_t(bytes), s>>>(maps, g);
-  return cuda_fail(cudaGetLastError(), "block product launch");
+  return cuda_fail(launch_chained(fn, chained, dim3(unsigned(tile_count(MH, g))), G_THREADS, size_t(bytes), s, maps, g),
+                   "block product launch");
 }
 template <int AK, bool BMN, int TERMS, int OUT>
-hsl_status launch_gemm(int mh, const GemmMaps& maps, const GemmArgs& g, cudaStream_t s) {
-  return mh == 2 ? launch_gemm<AK, BMN, TERMS, 2, OUT>(maps, g, s)
-                 : launch_gemm<AK, BMN, TERMS, 1, OUT>(maps, g, s);
+hsl_status launch_gemm(int mh, const GemmMaps& maps, const GemmArgs& g, bool chained, cudaStream_t s) {
+  return mh == 2 ? launch_gemm<AK, BMN, TERMS, 2, OUT>(maps, g, chained, s)
+                 : launch_gemm<AK, BMN, TERMS, 1, OUT>(maps, g, chained, s);
 }
 
 const auto kBF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;

@@ -41,7 +41,6 @@
     tc::mbar_init(&addf, 1);
     tc::fence_mbar_init();
     tc::prefetch_tmap(&maps.b0);
-    if (OUT == OUT_T && g.addt) tc::tma_prefetch_2d(&maps.add, i0, j0);  // into L2 for the epilogue
   }
   if (warp == 1) {
     tc::tmem_alloc(&tmem_slot, cols);
@@ -50,11 +49,15 @@
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
+  // Every CTA of the grid holds its TMEM when the next kernel's may start: none of those can take it first.
+  pdl_trigger();
+  pdl_wait();
   const uint32_t tmem = tmem_slot;
   volatile int* abrt = &abort_flag;
 
   if (warp == 0) {
     if (lane == 0) {
+      if (OUT == OUT_T && g.addt) tc::tma_prefetch_2d(&maps.add, i0, j0);  // into L2 for the epilogue
       int s = 0, issued = 0;
       uint32_t ph = 1;
       for (int kb = 0; kb < nk; ++kb) {

@@ -97,6 +97,8 @@ __device__ __forceinline__ void sum_job(const SumJob& j, int64_t e) {
 template <int V>
 __global__ void __launch_bounds__(256)
     k_mx_grad_sum(const SumJob a, const SumJob b, int na) {
+  pdl_trigger();
+  pdl_wait();
   if (int(blockIdx.x) < na) sum_job<V>(a, (int64_t(blockIdx.x) * 256 + threadIdx.x) * V);
   else sum_job<V>(b, (int64_t(blockIdx.x - na) * 256 + threadIdx.x) * V);
 }
@@ -105,9 +107,8 @@ hsl_status sum_run(const SumJob& a, const SumJob& b, bool vec, cudaStream_t s) {
   const unsigned na = blocks_of(a.rows * a.pitch / v), nb = blocks_of(b.rows * b.pitch / v);
   if (na + nb == 0) return HSL_OK;
   note_launch();
-  if (vec) k_mx_grad_sum<4><<<na + nb, 256, 0, s>>>(a, b, int(na));
-  else k_mx_grad_sum<1><<<na + nb, 256, 0, s>>>(a, b, int(na));
-  return cuda_fail(cudaGetLastError(), "split sum launch");
+  return cuda_fail(launch_chained(vec ? k_mx_grad_sum<4> : k_mx_grad_sum<1>, true, dim3(na + nb), 256, 0, s, a, b,
+                                  int(na)), "split sum launch");
 }
 
 struct GradPlan {
@@ -188,15 +189,15 @@ GradPlan grad_plan(int64_t T, int64_t m, int64_t n, int64_t r) {
 
 template <int MG>
 hsl_status launch_first(const GemmMaps& gm, const GemmArgs& g, const GemmMaps& zm, const GemmArgs& z,
-                        cudaStream_t s) {
+                        bool chained, cudaStream_t s) {
   void (*fn)(const GemmMaps, const GemmMaps, const GemmArgs, const GemmArgs, int) = k_mx_grad_first<MG>;
   const int bytes = std::max(tile_smem(A_BF16_K, true, 1, MG, false, g), tile_smem(A_INT8_K, true, 1, 1, false, z));
   if (cudaError_t e = allow_dyn_smem(reinterpret_cast<const void*>(fn), bytes))
     return cuda_fail(e, "factor gradient smem attribute");
   const int64_t ng = tile_count(MG, g), nz = tile_count(1, z);
   note_launch();
-  fn<<<unsigned(ng + nz), G_THREADS, size_t(bytes), s>>>(gm, zm, g, z, int(ng));
-  return cuda_fail(cudaGetLastError(), "factor gradient launch");
+  return cuda_fail(launch_chained(fn, chained, dim3(unsigned(ng + nz)), G_THREADS, size_t(bytes), s, gm, zm, g, z,
+                                  int(ng)), "factor gradient launch");
 }
 template <int MU, int MX>
 hsl_status launch_second(const GemmMaps& um, const GemmArgs& u, const GemmMaps& vm, const GemmArgs& v,
@@ -209,8 +210,8 @@ hsl_status launch_second(const GemmMaps& um, const GemmArgs& u, const GemmMaps& 
     return cuda_fail(e, "factor gradient smem attribute");
   const int64_t nu = tile_count(MU, u), nv = tile_count(1, v), nx = with_x ? tile_count(MX, x) : 0;
   note_launch();
-  fn<<<unsigned(nu + nv + nx), G_THREADS, size_t(bytes), s>>>(um, vm, xm, u, v, x, int(nu), int(nv));
-  return cuda_fail(cudaGetLastError(), "factor gradient launch");
+  return cuda_fail(launch_chained(fn, true, dim3(unsigned(nu + nv + nx)), G_THREADS, size_t(bytes), s, um, vm, xm, u, v,
+                                  x, int(nu), int(nv)), "factor gradient launch");
 }
 
 }  // namespace
@@ -267,7 +268,9 @@ hsl_status mx_gemm_grad_run(const MxOperand& X, int64_t T, int64_t n, const void
       !make_tmap_2d(&m0.b0, kBF, 2, U, m, r, p.rp, 64, 64, kSW) ||
       !make_tmap_2d(&m1.b0, kBF, 2, V, n, r, p.rp, 64, 64, kSW) || !block_maps(&m1, A_INT8_K, 1, X, T))
     return map_failed();
-  if (hsl_status e = p.g.MH == 2 ? launch_first<2>(m0, g, m1, z, s) : launch_first<1>(m0, g, m1, z, s)) return e;
+  const bool padded = m % 8 || r % 8;
+  if (hsl_status e = p.g.MH == 2 ? launch_first<2>(m0, g, m1, z, padded, s) : launch_first<1>(m0, g, m1, z, padded, s))
+    return e;
   const SumJob sg = {pa, p.g.splits, int(r), int(p.rp), T, gh, gl}, sz = {pb, p.z.splits, int(r), int(p.rp), T, zh, zl};
   if (hsl_status e = sum_run(sg, sz, r % 8 == 0, s)) return e;
 

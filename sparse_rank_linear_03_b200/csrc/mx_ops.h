@@ -8,6 +8,26 @@
 
 namespace hsl {
 
+// Launches of a chain of kernels.  A chained kernel may start as soon as every CTA of the one before has
+// called pdl_trigger, so that its launch and set-up overlap that kernel's end; it touches
+// global memory after pdl_wait only, when that kernel has ended and can be seen.
+// The first kernel of a call is never chained: what came before it on the stream is not ours.
+template <typename... P, typename... A>
+cudaError_t launch_chained(void (*fn)(P...), bool chained, dim3 grid, unsigned block, size_t smem, cudaStream_t s,
+                           const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = chained ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, fn, P(args)...);
+}
+
 // One factor of a product, stored as [i][k] (or [k][i] when trans).
 struct MxOperand {
   enum Kind : int32_t { kF32, kBF16, kE2M1, kInt8 };
