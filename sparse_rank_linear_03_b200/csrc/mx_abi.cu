@@ -210,7 +210,7 @@ hsl_status hsl_mx4_apply(const hsl_mx* D, const void* X, const void* add, void* 
   if (dtype == HSL_F32 && batch <= kMxDecodeF32Max)
     return mx_decode_f32_run(operand(D, false), D->rows, D->cols, X, add, Y, batch, s);
   return mx_simt_run(operand(X, dtype, D->cols, false), operand(D, false), batch, D->rows, D->cols,
-                     add, Y, dtype, ws, s);
+                     add, Y, dtype, ws, false, s);
 }
 
 hsl_status hsl_mx4_apply_t(const hsl_mx* D, const void* dY, const void* add, void* dX, int64_t batch,
@@ -231,7 +231,7 @@ hsl_status hsl_mx4_apply_t(const hsl_mx* D, const void* dY, const void* add, voi
   if (dtype == HSL_BF16 && D->rows > 0 && mx_gemm_supported(dY))
     return mx_gemm_apply_run(true, operand(D, true), D->rows, D->cols, dY, add, dX, batch, ws, s);
   return mx_simt_run(operand(dY, dtype, D->rows, false), operand(D, true), batch, D->cols, D->rows,
-                     add, dX, dtype, ws, s);
+                     add, dX, dtype, ws, false, s);
 }
 
 hsl_status hsl_mx4_matmul(const hsl_mx* A, const hsl_mx* B, const void* add, void* Y, hsl_dtype dtype,
@@ -252,7 +252,7 @@ hsl_status hsl_mx4_matmul(const hsl_mx* A, const hsl_mx* B, const void* add, voi
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (mx_matmul_supported())
     return mx_matmul_run(operand(A, false), A->rows, operand(B, false), B->rows, A->cols, add, Y, dtype, s);
-  return mx_simt_run(operand(A, false), operand(B, false), A->rows, B->rows, A->cols, add, Y, dtype, ws, s);
+  return mx_simt_run(operand(A, false), operand(B, false), A->rows, B->rows, A->cols, add, Y, dtype, ws, false, s);
 }
 
 hsl_status hsl_mx8_factor_grad(const hsl_mx* X, const void* dY, int64_t m, const void* U,
@@ -281,18 +281,18 @@ hsl_status hsl_mx8_factor_grad(const hsl_mx* X, const void* dY, int64_t m, const
   float* G = Z ? Z + T * r : nullptr;
   void* part = Z ? static_cast<char*>(ws) + zg_bytes(T, r) : nullptr;
   const MxOperand x = operand(X, false), xt = operand(X, true);
-  if (hsl_status e = mx_simt_run(x, operand(V, dtype, r, true), T, r, n, nullptr, Z, HSL_F32, part, s)) return e;
+  if (hsl_status e = mx_simt_run(x, operand(V, dtype, r, true), T, r, n, nullptr, Z, HSL_F32, part, false, s)) return e;
   if (hsl_status e = mx_simt_run(operand(dY, dtype, m, false), operand(U, dtype, r, true), T, r, m,
-                                 nullptr, G, HSL_F32, part, s))
+                                 nullptr, G, HSL_F32, part, T > 0, s))
     return e;
   if (hsl_status e = mx_simt_run(operand(dY, dtype, m, true), operand(Z, HSL_F32, r, true), m, r, T,
-                                 nullptr, dU, dtype, part, s))
+                                 nullptr, dU, dtype, part, T > 0, s))
     return e;
-  if (hsl_status e = mx_simt_run(xt, operand(G, HSL_F32, r, true), n, r, T, nullptr, dV, dtype, part, s))
+  if (hsl_status e = mx_simt_run(xt, operand(G, HSL_F32, r, true), n, r, T, nullptr, dV, dtype, part, true, s))
     return e;
   if (!dX) return HSL_OK;
   return mx_simt_run(operand(G, HSL_F32, r, false), operand(V, dtype, r, false), T, n, r, add, dX, dtype,
-                     part, s);
+                     part, true, s);
 }
 
 hsl_status hsl_mx_check(hsl_stream stream) {

@@ -44,10 +44,11 @@ hsl_status mx_quantize_run(const void* X, hsl_dtype dtype, int64_t rows, int64_t
                            void* codes, void* scales, cudaStream_t s);
 hsl_status mx_dequantize_run(const void* codes, const void* scales, int64_t rows, int64_t cols,
                              bool int8, void* X, hsl_dtype dtype, cudaStream_t s);
-// C[M][N] (row pitch N) = add + A Bᵀ in fp32; `part` holds mx_simt_workspace bytes
+// C[M][N] (row pitch N) = add + A Bᵀ in fp32; `part` holds mx_simt_workspace bytes; chained: behind another
+// kernel of the same call
 size_t mx_simt_workspace(int64_t M, int64_t N, int64_t K);
 hsl_status mx_simt_run(const MxOperand& A, const MxOperand& B, int64_t M, int64_t N, int64_t K,
-                       const void* add, void* C, hsl_dtype cdt, void* part, cudaStream_t s);
+                       const void* add, void* C, hsl_dtype cdt, void* part, bool chained, cudaStream_t s);
 
 // Tensor-core products (mx_gemm.cu, mx_grad.cu), bf16: X, dY, U, V on 16 bytes (mx_gemm_supported)
 bool mx_gemm_supported(const void* X);

@@ -120,6 +120,8 @@ __global__ void __launch_bounds__(256)
     k_mx_simt(const MxOperand A, const MxOperand B, int64_t M, int64_t N, int64_t K, int64_t krange, const TO* add,
               TO* C, float* __restrict__ part) {
   __shared__ __align__(16) float sa[S_BK][68], sb[S_BK][68];
+  pdl_trigger();
+  pdl_wait();
   const unsigned tm = unsigned((M + S_BM - 1) / S_BM);
   const int64_t i0 = int64_t(blockIdx.x % tm) * S_BM, j0 = int64_t(blockIdx.x / tm) * S_BN;
   const int64_t kbeg = int64_t(blockIdx.z) * krange, kend = min(K, kbeg + krange);
@@ -180,6 +182,8 @@ __global__ void __launch_bounds__(256)
 template <typename TO>
 __global__ void __launch_bounds__(256)
     k_mx_simt_sum(const float* __restrict__ part, int ranges, int64_t count, const TO* add, TO* C) {
+  pdl_trigger();
+  pdl_wait();
   const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
   if (e >= count) return;
   float v = 0.f;
@@ -198,7 +202,7 @@ int ranges_of(int64_t M, int64_t N, int64_t K) {
 
 template <int KA, int KB, typename TO>
 hsl_status run(const MxOperand& A, const MxOperand& B, int64_t M, int64_t N, int64_t K, const TO* add, TO* C,
-               float* part, cudaStream_t s) {
+               float* part, bool chained, cudaStream_t s) {
   const int ranges = part ? ranges_of(M, N, K) : 1;
   const int64_t krange = ranges > 1 ? ((K + ranges - 1) / ranges + S_BK - 1) / S_BK * S_BK : K;
   const int64_t nz = ranges > 1 ? (K + krange - 1) / krange : 1;
@@ -206,14 +210,15 @@ hsl_status run(const MxOperand& A, const MxOperand& B, int64_t M, int64_t N, int
   const dim3 grid(unsigned((M + S_BM - 1) / S_BM * ((N + S_BN - 1) / S_BN)), 1, unsigned(nz));
   note_launch();
   if (nz == 1) {
-    k_mx_simt<KA, KB, TO, false><<<grid, 256, 0, s>>>(A, B, M, N, K, K, add, C, nullptr);
-    return cuda_fail(cudaGetLastError(), "fp32 product launch");
+    return cuda_fail(launch_chained(k_mx_simt<KA, KB, TO, false>, chained, grid, 256, 0, s, A, B, M, N, K, K, add, C,
+                                    nullptr), "fp32 product launch");
   }
-  k_mx_simt<KA, KB, TO, true><<<grid, 256, 0, s>>>(A, B, M, N, K, krange, add, C, part);
-  if (hsl_status e = cuda_fail(cudaGetLastError(), "fp32 product launch")) return e;
+  if (hsl_status e = cuda_fail(launch_chained(k_mx_simt<KA, KB, TO, true>, chained, grid, 256, 0, s, A, B, M, N, K,
+                                              krange, add, C, part), "fp32 product launch"))
+    return e;
   note_launch();
-  k_mx_simt_sum<TO><<<unsigned((M * N + 255) / 256), 256, 0, s>>>(part, int(nz), M * N, add, C);
-  return cuda_fail(cudaGetLastError(), "split sum launch");
+  return cuda_fail(launch_chained(k_mx_simt_sum<TO>, true, dim3(unsigned((M * N + 255) / 256)), 256, 0, s, part,
+                                  int(nz), M * N, add, C), "split sum launch");
 }
 
 constexpr int kind_of(int kind, bool trans) { return kind * 2 + (trans ? 1 : 0); }
@@ -229,25 +234,25 @@ size_t mx_simt_workspace(int64_t M, int64_t N, int64_t K) {
 }
 
 hsl_status mx_simt_run(const MxOperand& A, const MxOperand& B, int64_t M, int64_t N, int64_t K,
-                       const void* add, void* C, hsl_dtype cdt, void* part, cudaStream_t s) {
+                       const void* add, void* C, hsl_dtype cdt, void* part, bool chained, cudaStream_t s) {
   if (M <= 0 || N <= 0) return HSL_OK;
   float* w = mx_simt_workspace(M, N, K) ? static_cast<float*>(part) : nullptr;
   const int ka = kind_of(A.kind, A.trans != 0), kb = kind_of(B.kind, B.trans != 0);
   if (cdt == HSL_F32) {
     const float* a = static_cast<const float*>(add);
     float* c = static_cast<float*>(C);
-    if (ka == F && kb == E) return run<F, E, float>(A, B, M, N, K, a, c, w, s);
-    if (ka == F && kb == ET) return run<F, ET, float>(A, B, M, N, K, a, c, w, s);
-    if (ka == I && kb == FT) return run<I, FT, float>(A, B, M, N, K, a, c, w, s);
-    if (ka == F && kb == FT) return run<F, FT, float>(A, B, M, N, K, a, c, w, s);
-    if (ka == FT && kb == FT) return run<FT, FT, float>(A, B, M, N, K, a, c, w, s);
-    if (ka == IT && kb == FT) return run<IT, FT, float>(A, B, M, N, K, a, c, w, s);
-    if (ka == F && kb == F) return run<F, F, float>(A, B, M, N, K, a, c, w, s);
-    return run<kAny, kAny, float>(A, B, M, N, K, a, c, w, s);
+    if (ka == F && kb == E) return run<F, E, float>(A, B, M, N, K, a, c, w, chained, s);
+    if (ka == F && kb == ET) return run<F, ET, float>(A, B, M, N, K, a, c, w, chained, s);
+    if (ka == I && kb == FT) return run<I, FT, float>(A, B, M, N, K, a, c, w, chained, s);
+    if (ka == F && kb == FT) return run<F, FT, float>(A, B, M, N, K, a, c, w, chained, s);
+    if (ka == FT && kb == FT) return run<FT, FT, float>(A, B, M, N, K, a, c, w, chained, s);
+    if (ka == IT && kb == FT) return run<IT, FT, float>(A, B, M, N, K, a, c, w, chained, s);
+    if (ka == F && kb == F) return run<F, F, float>(A, B, M, N, K, a, c, w, chained, s);
+    return run<kAny, kAny, float>(A, B, M, N, K, a, c, w, chained, s);
   }
   // bf16 that the tensor-core kernels do not take (pointers off 16 bytes)
   return run<kAny, kAny, __nv_bfloat16>(A, B, M, N, K, static_cast<const __nv_bfloat16*>(add),
-                                        static_cast<__nv_bfloat16*>(C), w, s);
+                                        static_cast<__nv_bfloat16*>(C), w, chained, s);
 }
 
 }  // namespace hsl
