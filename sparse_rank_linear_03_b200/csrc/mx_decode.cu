@@ -15,9 +15,8 @@
 //   power of two, is a column of its own (8 significant bits over 32 binades end at
 //   2^−23, fp16 reaches 2^−24).  Activations fit one window nearly always; there is room
 //   for two columns per token up to 4 tokens, and what does not fit takes
-//   another pass over D.  A kernel of its own makes the columns (k_mx_tokens; every CTA doing it
-//   for itself took 4 to 10 µs), while the main kernel's first copies of D are already
-//   under way.  At the end each column is scaled back.  Infinities
+//   another pass over D.  From two tokens on a kernel of its own makes the columns (k_mx_tokens),
+//   while the main kernel's first copies of D are already under way.  At the end each column is scaled back.  Infinities
 //   and NaN go to the first window as they are.  Block scales enter as 2^(e − 142), so
 //   that a column's sums lie as if its largest value were about 1.
 //
@@ -93,9 +92,11 @@ struct DcMaps {
 struct DcArgs {
   const int2* tokens;   // per token: largest exponent field, windows
   const uint4* columns;  // [window][token][cpieces] pieces of eight fp16
+  const __nv_bfloat16* X;  // kSelf
   const __nv_bfloat16* add;
   __nv_bfloat16* Y;
-  int m, nb, T;
+  int m, n, nb, T;
+  int vec;     // kSelf: rows of X start on 16 bytes
   int wcols;   // columns per token, at most
   int cpieces;  // pieces per column in global memory
   int slice;   // units of K whose columns are in shared memory at a time
@@ -185,6 +186,12 @@ __device__ __forceinline__ uint4 window_piece(const uint4& v, int top, int win, 
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// A token's largest exponent field and windows.
+__device__ __forceinline__ int2 windows_of(int hi, int lo) {
+  if (hi < 0) hi = lo = 127;  // nothing but zeros, infinities and NaN
+  return make_int2(hi, (hi - lo) / 32 + 1);
+}
+
 // A CTA per token: its exponents, then its windows as columns of fp16 (in global memory).
 constexpr int DC_TOKEN_THREADS = 512;
 constexpr int DC_TOKEN_KEEP = 4;  // pieces that a thread keeps in registers from the first pass
@@ -227,9 +234,10 @@ __global__ void __launch_bounds__(DC_TOKEN_THREADS)
     hi = max(hi, red[0][w]);
     lo = min(lo, red[1][w]);
   }
-  if (hi < 0) hi = lo = 127;  // nothing but zeros, infinities and NaN
-  const int windows = (hi - lo) / 32 + 1;
-  if (threadIdx.x == 0) tokens[tok] = make_int2(hi, windows);
+  const int2 of = windows_of(hi, lo);
+  hi = of.x;
+  const int windows = of.y;
+  if (threadIdx.x == 0) tokens[tok] = of;
   for (int w = 0; w < windows; ++w) {
     uint4* out = columns + (int64_t(w) * gridDim.x + tok) * pieces;
 #pragma unroll
@@ -258,7 +266,8 @@ constexpr int DC_RED = DC_WARPS * 16 * DC_RED_PITCH * 4;
 
 __device__ __forceinline__ void dc_sync() { asm volatile("barrier.sync 1, 512;" ::: "memory"); }  // the 16 warps
 
-template <int NT>
+// kSelf: one token, whose columns each CTA makes for itself.
+template <int NT, bool kSelf>
 __global__ void __launch_bounds__(DC_THREADS, 1)
     k_mx_decode(const __grid_constant__ DcMaps maps, const DcArgs a) {
   constexpr int kRows = 16;
@@ -268,7 +277,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   __shared__ uint64_t full[DC_MAX_STAGES], empty[DC_MAX_STAGES];
   __shared__ uint64_t xfull;
   __shared__ int abort_flag;
-  __shared__ int2 token[16];
+  __shared__ int2 token[16], range[DC_WARPS];
   __shared__ float unscale[2][16];  // per column: 2^k in two factors
   float* red = reinterpret_cast<float*>(smem);  // [slot][DC_WARPS][columns][DC_RED_PITCH]
   const int pieces = a.slice * (DC_UNIT / 8), cpitch = dc_col_pitch(a.slice);
@@ -309,7 +318,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
           for (int u = u0; u < uend; u += a.su, ++step) {
             // One stage goes out without knowing the passes.  More of them only hold up the kernel that
             // makes the columns (one token, 28672 × 8192: 37 against 35 µs with a ring full).
-            if (!told && step == 1) {
+            if (!told && step == (kSelf ? a.stages : 1)) {
               told = true;
               __syncthreads();
             }
@@ -361,8 +370,30 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   for (int u0 = 0; u0 < units; u0 += a.slice) {
     const int uend = min(u0 + a.slice, units);
     if (u0 == 0) {
-      pdl_wait();  // the columns are written
-      if (threadIdx.x < a.T) token[threadIdx.x] = __ldcg(a.tokens + threadIdx.x);
+      if (kSelf) {
+        int hi = -1, lo = 255;
+#pragma unroll 4
+        for (int c = threadIdx.x; c < a.cpieces; c += DC_WARPS * 32) {
+          int h, l;
+          exponents(load_piece(a.X, c * 8, a.n, a.vec), h, l);
+          hi = max(hi, h);
+          lo = min(lo, l);
+        }
+        hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+        lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+        if (lane == 0) range[warp] = make_int2(hi, lo);
+        dc_sync();
+        if (threadIdx.x == 0) {
+          for (int w = 1; w < DC_WARPS; ++w) {
+            hi = max(hi, range[w].x);
+            lo = min(lo, range[w].y);
+          }
+          token[0] = windows_of(hi, lo);
+        }
+      } else {
+        pdl_wait();  // the columns are written
+        if (threadIdx.x < a.T) token[threadIdx.x] = __ldcg(a.tokens + threadIdx.x);
+      }
     }
     __syncthreads();
     int windows = 1;
@@ -373,8 +404,15 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     for (int pass = 0; pass < passes; ++pass, ++round) {
       tc::fence_async_smem();
       dc_sync();  // the last round's columns are read
-      if (threadIdx.x == 0) {
-        const int have = min(pieces, a.cpieces - u0 * (DC_UNIT / 8));  // the last slice may be shorter
+      const int have = min(pieces, a.cpieces - u0 * (DC_UNIT / 8));  // the last slice may be shorter
+      if (kSelf) {
+        for (int c = 0; c < cols && pass * a.wcols + c < windows; ++c) {
+#pragma unroll 4
+          for (int e = threadIdx.x; e < have; e += DC_WARPS * 32)
+            xs[c * cpitch + e] = window_piece(load_piece(a.X, (u0 * (DC_UNIT / 8) + e) * 8, a.n, a.vec), token[0].x,
+                                              pass * a.wcols + c, windows == 1);
+        }
+      } else if (threadIdx.x == 0) {
         int count = 0;
         for (int c = 0; c < cols; ++c) count += pass * a.wcols + c % per_tok < token[c / per_tok].y;
         tc::mbar_expect_tx(&xfull, uint32_t(count * have * 16));
@@ -396,7 +434,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       for (int c = 0; c < cols; ++c)  // windows that a token does not have
         if (pass * a.wcols + c % per_tok >= token[c / per_tok].y)
           for (int e = threadIdx.x; e < pieces; e += DC_WARPS * 32) xs[c * cpitch + e] = make_uint4(0, 0, 0, 0);
-      if (!tc::mbar_wait(&xfull, round & 1, &g_mx_decode_err)) *abrt = 1;
+      if (!kSelf && !tc::mbar_wait(&xfull, round & 1, &g_mx_decode_err)) *abrt = 1;
       dc_sync();
       const bool first = u0 == 0 && pass == 0, last = uend == units && pass == passes - 1;
       // The warps' sums of several row tiles are kept before they are added up together: a
@@ -631,9 +669,15 @@ bool mx_decode_fits(int64_t T, int64_t m, int64_t n) {
   return T <= kMxDecodeMax && tmap_available() && decode_plan(T, m, n).stages >= 2;
 }
 
+// One token's columns cost a CTA less than a kernel that makes them for all, as the first stages of D are on
+// their way meanwhile (28672 × 8192: 32.8 against 34.8 µs); from two tokens on they cost as much or
+// more (2: 36.9 against 34.8 µs; 8: 57 against 43 µs).
+bool decode_self(int64_t T) { return T == 1; }
+
 // The workspace: per token its exponent and windows (256 bytes), then its columns: eight windows hold every
 // bf16 value.
 size_t mx_decode_workspace(int64_t T, int64_t n) {
+  if (decode_self(T)) return 0;
   return size_t(256 + 8 * T * ((mx::blocks(n) + 7) / 8) * DC_UNIT * 2);
 }
 
@@ -653,8 +697,12 @@ hsl_status mx_decode_run(const MxOperand& D, int64_t m, int64_t n, const void* X
     set_message("tensor map encoding failed");
     return HSL_ERR_CUDA;
   }
+  const bool self = decode_self(T);
   a.tokens = static_cast<const int2*>(ws);
-  a.columns = reinterpret_cast<const uint4*>(static_cast<const char*>(ws) + 256);
+  a.columns = self ? nullptr : reinterpret_cast<const uint4*>(static_cast<const char*>(ws) + 256);
+  a.X = static_cast<const __nv_bfloat16*>(X);
+  a.n = int(n);
+  a.vec = n % 8 == 0 && reinterpret_cast<uintptr_t>(X) % 16 == 0 ? 1 : 0;
   a.cpieces = int((mx::blocks(n) + 7) / 8) * (DC_UNIT / 8);
   a.add = static_cast<const __nv_bfloat16*>(add);
   a.Y = static_cast<__nv_bfloat16*>(Y);
@@ -668,16 +716,16 @@ hsl_status mx_decode_run(const MxOperand& D, int64_t m, int64_t n, const void* X
   a.tps = p.tps;
   a.stages = p.stages;
   a.ysum = p.ysum;
-  void (*fn)(const DcMaps, const DcArgs) = T <= 8 ? k_mx_decode<1> : k_mx_decode<2>;
+  void (*fn)(const DcMaps, const DcArgs) = self ? k_mx_decode<1, true> : T <= 8 ? k_mx_decode<1, false> : k_mx_decode<2, false>;
   if (cudaError_t e = allow_dyn_smem(reinterpret_cast<const void*>(fn), p.bytes))
     return cuda_fail(e, "4-bit decode smem attribute");
-  const int vec = n % 8 == 0 && reinterpret_cast<uintptr_t>(X) % 16 == 0 ? 1 : 0;
-  note_launch(2);
-  k_mx_tokens<<<unsigned(T), DC_TOKEN_THREADS, 0, s>>>(static_cast<const __nv_bfloat16*>(X), int(n), vec, a.cpieces,
-                                                       static_cast<int2*>(ws),
-                                                       reinterpret_cast<uint4*>(static_cast<char*>(ws) + 256));
-  if (hsl_status e = cuda_fail(cudaGetLastError(), "4-bit decode launch")) return e;
-  return cuda_fail(launch_chained(fn, true, dim3(unsigned(p.grid)), DC_THREADS, size_t(p.bytes), s, maps, a),
+  note_launch(self ? 1 : 2);
+  if (!self) {
+    k_mx_tokens<<<unsigned(T), DC_TOKEN_THREADS, 0, s>>>(a.X, int(n), a.vec, a.cpieces, static_cast<int2*>(ws),
+                                                         reinterpret_cast<uint4*>(static_cast<char*>(ws) + 256));
+    if (hsl_status e = cuda_fail(cudaGetLastError(), "4-bit decode launch")) return e;
+  }
+  return cuda_fail(launch_chained(fn, !self, dim3(unsigned(p.grid)), DC_THREADS, size_t(p.bytes), s, maps, a),
                    "4-bit decode launch");
 }
 
