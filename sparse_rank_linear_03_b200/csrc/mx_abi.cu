@@ -115,7 +115,7 @@ size_t workspace_bytes(hsl_mx_op op, int64_t T, int64_t m, int64_t n, int64_t r,
   if (T == 0 || m == 0) return simt_bytes(op, T, m, n, r);
   if (op == HSL_MX_OP_MATMUL) return mx_matmul_supported() ? 0 : simt_bytes(op, T, m, n, r);
   if (dt == HSL_F32) {
-    if (op == HSL_MX_OP_APPLY && T <= kMxDecodeF32Max) return 0;
+    if (op == HSL_MX_OP_APPLY && T <= kMxDecodeF32Max) return mx_decode_f32_workspace(T, m, n);
     return simt_bytes(op, T, m, n, r);
   }
   if (op == HSL_MX_OP_APPLY && mx_decode_fits(T, m, n)) return mx_decode_workspace(T, n);
@@ -208,7 +208,7 @@ hsl_status hsl_mx4_apply(const hsl_mx* D, const void* X, const void* add, void* 
   if (dtype == HSL_BF16 && mx_gemm_supported(X))
     return mx_gemm_apply_run(false, operand(D, false), D->rows, D->cols, X, add, Y, batch, ws, s);
   if (dtype == HSL_F32 && batch <= kMxDecodeF32Max)
-    return mx_decode_f32_run(operand(D, false), D->rows, D->cols, X, add, Y, batch, s);
+    return mx_decode_f32_run(operand(D, false), D->rows, D->cols, X, add, Y, batch, ws, s);
   return mx_simt_run(operand(X, dtype, D->cols, false), operand(D, false), batch, D->rows, D->cols,
                      add, Y, dtype, ws, false, s);
 }

@@ -7,15 +7,15 @@
 // does takes about half an integer instruction:
 //
 //   cvt turns two codes into two fp16 values, which mma.sync (m16n8k16, fp32 sums)
-//   multiplies with the tokens, 16 rows of D × 8 or 16 columns.  Each block has its own
+//   multiplies with the tokens, 16 rows of D × 8 columns.  Each block has its own
 //   MMAs, and its scale multiplies their 4 sums per lane (fp32 FMA).
 //
 //   The tokens become fp16 without losing a bit: a token's values are sorted into
 //   windows of 32 binades below its largest, and each window, scaled by its own
 //   power of two, is a column of its own (8 significant bits over 32 binades end at
 //   2^−23, fp16 reaches 2^−24).  Activations fit one window nearly always; there is room
-//   for two columns per token up to 4 tokens, and what does not fit takes
-//   another pass over D.  From two tokens on a kernel of its own makes the columns (k_mx_tokens),
+//   for two columns per token up to 4 tokens (and not too long ones), and what does not fit
+//   takes another pass over D.  From two tokens on a kernel of its own makes the columns (k_mx_tokens),
 //   while the main kernel's first copies of D are already under way.  At the end each column is scaled back.  Infinities
 //   and NaN go to the first window as they are.  Block scales enter as 2^(e − 142), so
 //   that a column's sums lie as if its largest value were about 1.
@@ -29,7 +29,7 @@
 //   up in warp order, several row tiles at a time.  Where the columns do not fit, K is taken in slices; the rows'
 //   sums stay in shared memory from slice to slice and pass to pass.
 //
-// f32 (k_mx_decode_f32): a lane per row, tokens broadcast from shared memory, fp32 FMA.
+// f32 (k_mx_decode_f32): a lane per row, tokens broadcast from shared memory, fp32 FMA, K in ranges.
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -260,14 +260,14 @@ __device__ uint32_t g_mx_decode_err;
 
 constexpr int DC_MAX_STAGES = 8;
 constexpr int DC_THREADS = (DC_WARPS + 1) * 32;
-// Room for the warps' sums: of one row tile with 16 columns, of more with fewer columns.
+// Room for the warps' sums: of two row tiles with eight columns, of more with fewer columns.
 constexpr int DC_RED_PITCH = 20;  // a column's 16 rows, spread over the banks
 constexpr int DC_RED = DC_WARPS * 16 * DC_RED_PITCH * 4;
 
 __device__ __forceinline__ void dc_sync() { asm volatile("barrier.sync 1, 512;" ::: "memory"); }  // the 16 warps
 
 // kSelf: one token, whose columns each CTA makes for itself.
-template <int NT, bool kSelf>
+template <bool kSelf>
 __global__ void __launch_bounds__(DC_THREADS, 1)
     k_mx_decode(const __grid_constant__ DcMaps maps, const DcArgs a) {
   constexpr int kRows = 16;
@@ -277,8 +277,8 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   __shared__ uint64_t full[DC_MAX_STAGES], empty[DC_MAX_STAGES];
   __shared__ uint64_t xfull;
   __shared__ int abort_flag;
-  __shared__ int2 token[16], range[DC_WARPS];
-  __shared__ float unscale[2][16];  // per column: 2^k in two factors
+  __shared__ int2 token[8], range[DC_WARPS];
+  __shared__ float unscale[2][8];  // per column: 2^k in two factors
   float* red = reinterpret_cast<float*>(smem);  // [slot][DC_WARPS][columns][DC_RED_PITCH]
   const int pieces = a.slice * (DC_UNIT / 8), cpitch = dc_col_pitch(a.slice);
   uint4* xs = reinterpret_cast<uint4*>(smem + DC_RED);
@@ -441,13 +441,10 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       // meeting of the warps per tile costs more than the tile's copies.
       const int slots = DC_RED / (DC_WARPS * DC_RED_PITCH * 4 * cols);
       int slot = 0, local = 0;
-      // Columns g, 8 + g at this lane's words (the last column where there are fewer: those sums
-      // are not used)
-      const uint4* xb[NT];
-#pragma unroll
-      for (int q = 0; q < NT; ++q) xb[q] = xs + min(q * 8 + g, cols - 1) * cpitch + t;
+      // Column g at this lane's words (the last column where there are fewer: those sums are not used)
+      const uint4* xb = xs + min(g, cols - 1) * cpitch + t;
       for (int grp = blockIdx.x; grp < groups; grp += gridDim.x) {
-        float acc[NT][4] = {};
+        float acc[4] = {};
         for (int u = u0; u < uend; u += a.su) {
           const bool got = tc::mbar_try(&full[s], ph) ||
                            (!*abrt && tc::mbar_wait(&full[s], ph, &g_mx_decode_err));
@@ -483,17 +480,14 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
               uint32_t v0[4], v1[4];
               widen_word(w0[b], v0);
               widen_word(w1[b], v1);
-#pragma unroll
-              for (int q = 0; q < NT; ++q) {
-                const uint4 x = xb[q][xu + b * 4];
-                float c[4] = {0.f, 0.f, 0.f, 0.f};
-                mma16816(c, v0[0], v1[0], v0[1], v1[1], x.x, x.y);
-                mma16816(c, v0[2], v1[2], v0[3], v1[3], x.z, x.w);
-                acc[q][0] = fmaf(s0[b], c[0], acc[q][0]);
-                acc[q][1] = fmaf(s0[b], c[1], acc[q][1]);
-                acc[q][2] = fmaf(s1[b], c[2], acc[q][2]);
-                acc[q][3] = fmaf(s1[b], c[3], acc[q][3]);
-              }
+              const uint4 x = xb[xu + b * 4];
+              float c[4] = {0.f, 0.f, 0.f, 0.f};
+              mma16816(c, v0[0], v1[0], v0[1], v1[1], x.x, x.y);
+              mma16816(c, v0[2], v1[2], v0[3], v1[3], x.z, x.w);
+              acc[0] = fmaf(s0[b], c[0], acc[0]);
+              acc[1] = fmaf(s0[b], c[1], acc[1]);
+              acc[2] = fmaf(s1[b], c[2], acc[2]);
+              acc[3] = fmaf(s1[b], c[3], acc[3]);
             }
           }
           tc::fence_async_smem();  // the loads are done before a copy may overwrite what they read
@@ -507,15 +501,13 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         if (slot == 0 && local) dc_sync();  // the last sums are read
         float* out = red + (slot * DC_WARPS + warp) * cols * DC_RED_PITCH + g;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int col = n * 8 + 2 * t + q;
-            if (col < cols) {
-              out[col * DC_RED_PITCH] = acc[n][q];
-              out[col * DC_RED_PITCH + 8] = acc[n][2 + q];
-            }
+        for (int q = 0; q < 2; ++q) {
+          const int col = 2 * t + q;
+          if (col < cols) {
+            out[col * DC_RED_PITCH] = acc[q];
+            out[col * DC_RED_PITCH + 8] = acc[2 + q];
           }
+        }
         ++slot;
         if (slot < slots && grp + int(gridDim.x) < groups) continue;
         dc_sync();
@@ -556,27 +548,31 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
 // ---- f32 ------------------------------------------------------------------------
 constexpr int DF_WARPS = 8;
 constexpr int DF_TOK = 8;      // tokens of a pass
-constexpr int DF_SLAB = 1024;  // values of K staged at a time: 128 per warp
+constexpr int DF_SLAB = 512;   // values of K staged at a time: 64 per warp
 
 // A CTA takes 32 rows (a lane each) × up to 8 tokens; its eight warps divide each slab of K.
-// A row's 16 bytes of codes are read by one lane; four blocks later the
-// lane has used the whole 64 bytes, which stay in L1 meanwhile.
+// A row's 16 bytes of codes are read by one lane, which uses a whole 32-byte sector with its two blocks.  What
+// bounds it is widening and FMA issue once per 8 tokens, and below that latency: K goes in ranges to
+// about five CTAs per SM, whose sums a second kernel adds in order (4096 × 4096, 8 tokens: 54 µs
+// in one range, 30 in eight; one token 20 µs; slabs of 1024 values cost 2 to 10 µs more).
 __global__ void __launch_bounds__(DF_WARPS * 32)
     k_mx_decode_f32(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t cpitch,
                     int64_t spitch, const float* __restrict__ X, const float* add, float* Y, int m, int n,
-                    int nb, int T) {
+                    int nb, int T, int krange, float* __restrict__ part) {
+  pdl_trigger();
   __shared__ __align__(16) float xs[DF_TOK][DF_SLAB];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int i = blockIdx.x * 32 + lane, row = min(i, m - 1);
   const int t0 = blockIdx.y * DF_TOK, nt = min(DF_TOK, T - t0);
   float acc[DF_TOK] = {};
-  for (int k0 = 0; k0 < n; k0 += DF_SLAB) {
-    uint4 c[4];
+  const int kend = min(n, int(blockIdx.z + 1) * krange);
+  for (int k0 = blockIdx.z * krange; k0 < kend; k0 += DF_SLAB) {
+    uint4 c[2];
     uint32_t s = 0;
-    const int b0 = k0 / 32 + warp * 4;
-    if (b0 < nb) s = __ldg(reinterpret_cast<const uint32_t*>(scales + int64_t(row) * spitch + b0));
+    const int b0 = k0 / 32 + warp * 2;
+    if (b0 < nb) s = __ldg(reinterpret_cast<const uint16_t*>(scales + int64_t(row) * spitch + b0));
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+    for (int q = 0; q < 2; ++q)
       c[q] = b0 + q < nb ? __ldg(reinterpret_cast<const uint4*>(codes + int64_t(row) * cpitch + int64_t(b0 + q) * 16))
                          : make_uint4(0, 0, 0, 0);
     __syncthreads();
@@ -586,7 +582,7 @@ __global__ void __launch_bounds__(DF_WARPS * 32)
     }
     __syncthreads();
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < 2; ++q) {
       if (b0 + q >= nb) break;
       const float scale = mx::scale_f32((s >> (8 * q)) & 0xFFu);
       const uint32_t w[4] = {c[q].x, c[q].y, c[q].z, c[q].w};
@@ -599,7 +595,7 @@ __global__ void __launch_bounds__(DF_WARPS * 32)
 #pragma unroll
         for (int tok = 0; tok < DF_TOK; ++tok) {
           if (tok >= nt) break;
-          const float4 x = *reinterpret_cast<const float4*>(&xs[tok][warp * 128 + q * 32 + z * 4]);
+          const float4 x = *reinterpret_cast<const float4*>(&xs[tok][warp * 64 + q * 32 + z * 4]);
           part[tok] = fmaf(d[0], x.x, part[tok]);
           part[tok] = fmaf(d[1], x.y, part[tok]);
           part[tok] = fmaf(d[2], x.z, part[tok]);
@@ -621,8 +617,12 @@ __global__ void __launch_bounds__(DF_WARPS * 32)
 #pragma unroll
     for (int w = 0; w < DF_WARPS; ++w) v += red[(w * DF_TOK + warp) * 32 + lane];
     const int64_t at = int64_t(t0 + warp) * m + i;
-    if (add) v += add[at];
-    Y[at] = v;
+    if (part) {
+      part[int64_t(blockIdx.z) * T * m + at] = v;
+    } else {
+      if (add) v += add[at];
+      Y[at] = v;
+    }
   }
 }
 static_assert(DF_WARPS * DF_TOK * 32 <= DF_TOK * DF_SLAB, "the sums fit where the tokens were");
@@ -631,13 +631,12 @@ static_assert(DF_WARPS * DF_TOK * 32 <= DF_TOK * DF_SLAB, "the sums fit where th
 struct DcPlan {
   int wcols, slice, su, tps, stages, ysum, ring, bytes, grid;
 };
-DcPlan decode_plan(int64_t T, int64_t m, int64_t n) {
+DcPlan decode_plan(int64_t T, int64_t m, int64_t n, int wcols) {
   DcPlan p = {};
-  p.wcols = T <= 4 ? 2 : 1;
+  p.wcols = wcols;
   const int rows = 16;
   const int units = int((mx::blocks(n) + 7) / 8);
   const int64_t tiles = (m + rows - 1) / rows;
-  const int red = DC_RED;
   // the widest slice (all of K at best) that leaves room for two stages at least; with
   // more than one, slices of whole stages of 16 units, or of an even number of units (a
   // copy of scales starts on 16 bytes)
@@ -651,16 +650,24 @@ DcPlan decode_plan(int64_t T, int64_t m, int64_t n) {
     const int64_t ysum = (groups + p.grid - 1) / p.grid * p.tps * T * rows * 4;
     const int64_t xs = T * p.wcols * dc_col_pitch(p.slice) * 16;
     const int stage = dc_stage_bytes(p.su, p.tps * rows);
-    const int64_t left = DC_SMEM_MAX - round_up(red + xs, 1024) - ysum;
+    const int64_t left = DC_SMEM_MAX - round_up(DC_RED + xs, 1024) - ysum;
     if (left < 2 * stage) continue;
     p.stages = int(std::min<int64_t>(DC_MAX_STAGES, left / stage));
-    p.ring = int(round_up(red + xs, 1024));
+    p.ring = int(round_up(DC_RED + xs, 1024));
     p.ysum = p.ring + p.stages * stage;
     p.bytes = p.ysum + int(ysum) + 1024;
     return p;
   }
   p.stages = 0;
   return p;
+}
+// Two columns per token up to 4 tokens, unless their room costs stages or slices of K that one column
+// would not.
+DcPlan decode_plan(int64_t T, int64_t m, int64_t n) {
+  const DcPlan one = decode_plan(T, m, n, 1);
+  if (T > 4) return one;
+  const DcPlan two = decode_plan(T, m, n, 2);
+  return two.slice == one.slice && two.stages >= std::min(one.stages, 3) ? two : one;
 }
 
 }  // namespace
@@ -716,7 +723,7 @@ hsl_status mx_decode_run(const MxOperand& D, int64_t m, int64_t n, const void* X
   a.tps = p.tps;
   a.stages = p.stages;
   a.ysum = p.ysum;
-  void (*fn)(const DcMaps, const DcArgs) = self ? k_mx_decode<1, true> : T <= 8 ? k_mx_decode<1, false> : k_mx_decode<2, false>;
+  void (*fn)(const DcMaps, const DcArgs) = self ? k_mx_decode<true> : k_mx_decode<false>;
   if (cudaError_t e = allow_dyn_smem(reinterpret_cast<const void*>(fn), p.bytes))
     return cuda_fail(e, "4-bit decode smem attribute");
   note_launch(self ? 1 : 2);
@@ -733,15 +740,34 @@ cudaError_t mx_decode_error_word(uint32_t** p) {
   return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_mx_decode_err);
 }
 
+// Ranges of K, each whole slabs: about five CTAs per SM.  Two slabs stay in one range, as the second launch and the
+// scratch cost more than a slab (1024 × 1024, one token: 14.3 against 10.9 µs).
+static int decode_f32_ranges(int64_t T, int64_t m, int64_t n, int64_t* krange) {
+  const int64_t ctas = (m + 31) / 32 * ((T + DF_TOK - 1) / DF_TOK), slabs = (n + DF_SLAB - 1) / DF_SLAB;
+  if (slabs <= 2) return *krange = slabs * DF_SLAB, 1;
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(slabs, (740 + ctas - 1) / ctas));
+  const int64_t per = (slabs + want - 1) / want;
+  *krange = per * DF_SLAB;
+  return int((slabs + per - 1) / per);
+}
+size_t mx_decode_f32_workspace(int64_t T, int64_t m, int64_t n) {
+  int64_t krange;
+  const int ranges = decode_f32_ranges(T, m, n, &krange);
+  return ranges > 1 ? size_t(ranges) * size_t(T * m) * 4 : 0;
+}
 hsl_status mx_decode_f32_run(const MxOperand& D, int64_t m, int64_t n, const void* X, const void* add,
-                             void* Y, int64_t T, cudaStream_t s) {
-  const dim3 grid(unsigned((m + 31) / 32), unsigned((T + DF_TOK - 1) / DF_TOK));
+                             void* Y, int64_t T, void* ws, cudaStream_t s) {
+  int64_t krange;
+  const int ranges = decode_f32_ranges(T, m, n, &krange);
+  const dim3 grid(unsigned((m + 31) / 32), unsigned((T + DF_TOK - 1) / DF_TOK), unsigned(ranges));
+  float* part = ranges > 1 ? static_cast<float*>(ws) : nullptr;
   note_launch();
   k_mx_decode_f32<<<grid, DF_WARPS * 32, 0, s>>>(static_cast<const uint8_t*>(D.p), D.scales, D.pitch, D.spitch,
                                                  static_cast<const float*>(X), static_cast<const float*>(add),
                                                  static_cast<float*>(Y), int(m), int(n), int(mx::blocks(n)),
-                                                 int(T));
-  return cuda_fail(cudaGetLastError(), "4-bit f32 decode launch");
+                                                 int(T), int(krange), part);
+  if (hsl_status e = cuda_fail(cudaGetLastError(), "4-bit f32 decode launch")) return e;
+  return part ? mx_simt_sum_run(part, ranges, T * m, static_cast<const float*>(add), static_cast<float*>(Y), s) : HSL_OK;
 }
 
 }  // namespace hsl

@@ -49,6 +49,8 @@ hsl_status mx_dequantize_run(const void* codes, const void* scales, int64_t rows
 size_t mx_simt_workspace(int64_t M, int64_t N, int64_t K);
 hsl_status mx_simt_run(const MxOperand& A, const MxOperand& B, int64_t M, int64_t N, int64_t K,
                        const void* add, void* C, hsl_dtype cdt, void* part, bool chained, cudaStream_t s);
+// C = add + Σ of `ranges` partial results in part [range][count], chained
+hsl_status mx_simt_sum_run(const float* part, int ranges, int64_t count, const float* add, float* C, cudaStream_t s);
 
 // Tensor-core products (mx_gemm.cu, mx_grad.cu), bf16: X, dY, U, V on 16 bytes (mx_gemm_supported)
 bool mx_gemm_supported(const void* X);
@@ -62,14 +64,19 @@ hsl_status mx_gemm_grad_run(const MxOperand& X, int64_t T, int64_t n, const void
 cudaError_t mx_gemm_error_word(uint32_t** p);
 cudaError_t mx_grad_error_word(uint32_t** p);
 // A few tokens (mx_decode.cu), any alignment of X.  bf16: as many as mx_decode_fits says.
-constexpr int64_t kMxDecodeMax = 16, kMxDecodeF32Max = 64;
+// To 8 tokens, the columns of one register MMA: 28672 × 8192 at 8 tokens 44 µs, the tensor-core kernel 79; 11008 × 4096
+// 21 against 26.  With two MMAs per block, at 16 tokens, it took 99 and 28 µs, the tensor-core kernel 80 and 26.
+// f32 to 32: 4096 × 4096 at 32 tokens 78 µs, the tiled product 88; at 64 tokens 143 and 94 µs; 512 × 4096 at 32
+// tokens 18 and 20, at 64 29 and 20 µs.
+constexpr int64_t kMxDecodeMax = 8, kMxDecodeF32Max = 32;
 bool mx_decode_fits(int64_t T, int64_t m, int64_t n);
 cudaError_t mx_decode_error_word(uint32_t** p);
 size_t mx_decode_workspace(int64_t T, int64_t n);
 hsl_status mx_decode_run(const MxOperand& D, int64_t m, int64_t n, const void* X, const void* add, void* Y,
                          int64_t T, void* ws, cudaStream_t s);
 hsl_status mx_decode_f32_run(const MxOperand& D, int64_t m, int64_t n, const void* X, const void* add,
-                             void* Y, int64_t T, cudaStream_t s);
+                             void* Y, int64_t T, void* ws, cudaStream_t s);
+size_t mx_decode_f32_workspace(int64_t T, int64_t m, int64_t n);
 // Both factors in e2m1 blocks (mx_matmul.cu): Y[T][m] = A Bᵀ (+ add)
 bool mx_matmul_supported();
 hsl_status mx_matmul_run(const MxOperand& A, int64_t T, const MxOperand& B, int64_t m, int64_t n,

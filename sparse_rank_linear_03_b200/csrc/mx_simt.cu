@@ -233,6 +233,12 @@ size_t mx_simt_workspace(int64_t M, int64_t N, int64_t K) {
   return r > 1 ? size_t(r) * size_t(M * N) * 4 : 0;
 }
 
+hsl_status mx_simt_sum_run(const float* part, int ranges, int64_t count, const float* add, float* C, cudaStream_t s) {
+  note_launch();
+  return cuda_fail(launch_chained(k_mx_simt_sum<float>, true, dim3(unsigned((count + 255) / 256)), 256, 0, s, part, ranges,
+                                  count, add, C), "split sum launch");
+}
+
 hsl_status mx_simt_run(const MxOperand& A, const MxOperand& B, int64_t M, int64_t N, int64_t K,
                        const void* add, void* C, hsl_dtype cdt, void* part, bool chained, cudaStream_t s) {
   if (M <= 0 || N <= 0) return HSL_OK;
