@@ -117,6 +117,30 @@ def test_quantize_unaligned_input(hsl):
     assert np.array_equal(q.codes.cpu().numpy(), c) and np.array_equal(q.scales.cpu().numpy(), s)
 
 
+@pytest.mark.parametrize("elem", ["e2m1", "int8"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,cols", [(1, 16), (2, 47), (3, 49), (40, 77), (7, 1003), (3, 4096)])
+def test_rows_at_every_offset(hsl, rows, cols, elem, dtype):
+    """Rows that start anywhere: the matrix at every offset inside 16 bytes and odd row lengths;
+    what lies before and behind it is neither read into the blocks nor written."""
+    x = tokens(rows, cols, cols).astype(np.float32)
+    for off in range(16 // TDT[dtype].itemsize + 1):
+        buf = torch.full((off + rows * cols + 24,), 3.0e30, dtype=TDT[dtype], device="cuda")
+        X = buf[off:off + rows * cols].view(rows, cols)
+        X.copy_(torch.from_numpy(x))
+        c, s = mx.quantize(X.float().cpu().numpy(), elem)
+        q = hsl.mx_quantize(X, elem)
+        assert np.array_equal(q.codes.cpu().numpy().view(np.uint8), c.view(np.uint8))
+        assert np.array_equal(q.scales.cpu().numpy(), s)
+        X.zero_()
+        assert hsl.lib.hsl_mx_dequantize(q._ref, X.data_ptr(), hsl.DTYPE[dtype],
+                                         torch.cuda.current_stream().cuda_stream) == 0
+        want = torch.from_numpy(mx.values(c, s, cols, elem)).to(TDT[dtype]).cuda()
+        assert torch.equal(X, want)
+        assert (buf[:off] == buf[-1]).all() and (buf[off + rows * cols:] == buf[-1]).all()
+        assert buf[-1].item() > 2.9e30
+
+
 def test_quantize_no_rows(hsl):
     q = hsl.mx_quantize(torch.empty(0, 40, device="cuda"))
     assert q.rows == 0 and hsl.mx_dequantize(q, "f32").shape == (0, 40)
