@@ -91,5 +91,17 @@ __device__ __forceinline__ uint2 widen_int8(uint32_t w, uint32_t scale) {
   return v;
 }
 
+// For rows that start anywhere: w becomes the NW words that start at byte `sh` (0 to 15) of its NW + 4, with the
+// shift in binary steps so that no register is addressed by a variable.
+template <int NW>
+__device__ __forceinline__ void shift_bytes(uint32_t (&w)[NW + 4], uint32_t sh) {
+#pragma unroll
+  for (int i = 0; i < NW + 2; ++i) w[i] = sh & 8 ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < NW + 1; ++i) w[i] = sh & 4 ? w[i + 1] : w[i];
+#pragma unroll
+  for (int i = 0; i < NW; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], (sh & 3) * 8);
+}
+
 }  // namespace mx
 }  // namespace hsl

@@ -123,6 +123,14 @@
     }
     __syncwarp();
   } else if (warp == 1) {
+    if (OUT == OUT_T && g.add && !g.addt) {  // into L2 for the epilogue, line by line
+      const int rows = min(g.BN, g.N - j0), len = min(128 * MH, g.M - i0);
+      for (int e = lane; e < rows * 5; e += 32) {
+        const int at = e % 5 * 64;
+        const __nv_bfloat16* p = g.add + int64_t(j0 + e / 5) * g.M + i0;
+        if (at < len + 63) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + min(at, len - 1)));
+      }
+    }
     if (tc::elect_one()) {
       const uint32_t idesc = tc::idesc_bf16(128, g.BN) | (a_is_mmajor(AK) ? 1u << 15 : 0u) |
                              (BMN ? 1u << 16 : 0u);
@@ -284,11 +292,13 @@
 #pragma unroll
               for (int q = 0; q < 32; ++q)
                 if (c0 + q < g.BN) v[q] += __bfloat162float(stg[(c0 + q) * (128 * MH) + R]);
-            } else if (g.add && i < g.M) {
+            } else if (g.add && i < g.M && jn > 0) {
               const __nv_bfloat16* p = g.add + int64_t(j0 + c0) * g.M + i;
+              __nv_bfloat16 av[32];  // all loads on their way before the first is used
 #pragma unroll
-              for (int q = 0; q < 32; ++q)
-                if (q < jn) v[q] += __bfloat162float(p[int64_t(q) * g.M]);
+              for (int q = 0; q < 32; ++q) av[q] = p[int64_t(min(q, jn - 1)) * g.M];
+#pragma unroll
+              for (int q = 0; q < 32; ++q) v[q] += __bfloat162float(av[q]);
             }
             if (g.cstore) {
 #pragma unroll

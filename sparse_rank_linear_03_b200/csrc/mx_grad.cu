@@ -5,7 +5,8 @@
 // Five skinny products in two launches (first Z and G, then the three that use them),
 // each launch one grid whose CTAs take tiles of one product or another: alone, most of
 // them have fewer tiles than SMs or leave a last round half empty (28672 × 8192, rank
-// 256, 4096 tokens: 317 µs as five launches).  Z and G are summed over their
+// 256, 4096 tokens: 317 µs as five launches, 260 so).  The second launch takes two thirds of
+// that: two terms per product, and 96 KB from L2 per 256 × 256 × 64 step.  Z and G are summed over their
 // splits into bf16 pairs (hi + lo, 16 significant bits), which the second
 // products take as two terms.
 #include "mx_gemm.cuh"

@@ -6,8 +6,9 @@
 // each 32-term piece of a dot product by the two blocks' powers of two, with fp32
 // sums: the definition itself, no widening.  With 256 tokens or more the tokens are the M
 // side of the MMA and the features its N side: a TMEM lane then holds neighbouring
-// values of an output row, which go out in 16-byte pieces.  With fewer, the features are
-// the M side, so that no accumulator row is idle.
+// values of an output row, which go out in 16-byte pieces (1000 × 1023, 300 tokens: 8.2 µs, 16.7 the
+// other way round).  With fewer, the features are the M side, so that no accumulator row is
+// idle (28672 × 8192: 35 µs at 16 tokens and 45 at 200, 55 and 53 the other way round).
 //
 //   warp 0 lane 0   TMA of the code tiles: 128·MH rows of the M side, BN of the N side, 256
 //                   values (128 bytes) each, 128-byte swizzle
@@ -19,10 +20,11 @@
 //                   pair is selected by the instruction descriptor
 //   warps 2-9       epilogue: tcgen05.ld, add, round, store
 //
-// Bound by the copies into shared memory: at 4 bits a 128 × 256 × 256 step takes the
-// MMA 512 cycles and brings 48 KB, so the tile is 256 × 192 (two accumulators
-// sharing the N side's tile): 56 KB per 768 cycles.  The two accumulators take 384
-// TMEM columns, the scales of the stages the rest.  Every wait is bounded.
+// Bound by shared memory: at 4 bits a 128 × 256 × 256 step takes the MMA 512 cycles and brings
+// 48 KB, so the tile is 256 × 192 (two accumulators sharing the N side's tile): 56 KB per
+// 768 cycles, and each MMA reads its operands again.  The two accumulators take 384
+// TMEM columns, the scales of the stages the rest.  28672 × 8192 at 4096 tokens: 377 µs,
+// 5.1 PFLOP/s (450 µs in a row of calls, where the power limit slows the clock).  Every wait is bounded.
 #include <cuda.h>
 
 #include <algorithm>
@@ -82,10 +84,13 @@ __device__ __forceinline__ uint32_t idesc_mxf4(int M, int N, uint32_t sf) {
          (uint32_t(M >> 4) << 24) | (sf << 29);
 }
 
-// kRows: C is [M][N] (tokens on the M side), else [N][M].
-template <typename TO, int MH, bool kRows>
+// How C is stored: [N][M], or [M][N] (tokens on the M side) in tiles, or, where rows do not start on 16 bytes
+// or are fp32, row by row by way of shared memory.
+enum MmOut { kCols, kTiles, kEach };
+template <typename TO, int MH, MmOut kOut>
 __global__ void __launch_bounds__(F_THREADS, 1)
     k_mx_matmul(const __grid_constant__ MmMaps maps, const MmArgs g) {
+  constexpr bool kRows = kOut != kCols;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   // (an offset, not a rounded integer: the compiler still knows that this is shared memory)
   unsigned char* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -303,8 +308,8 @@ __global__ void __launch_bounds__(F_THREADS, 1)
         const int jn = min(32, min(g.BN - c0, g.N - j0 - c0));
         if (kRows) {
           const int64_t at = int64_t(i) * g.N + j0 + c0;
-          if (add && i < g.M) {
-            if (jn == 32 && g.cstore && sizeof(TO) == 2) {
+          if (kOut == kTiles && add && i < g.M) {
+            if (jn == 32) {
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 const uint4 w = *reinterpret_cast<const uint4*>(add + at + q * 8);
@@ -319,7 +324,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
                 if (q < jn) v[q] += VT<TO>::f(add[at + q]);
             }
           }
-          if (g.cstore) {
+          if (kOut == kTiles) {
             // 64-column tiles of 128 rows in the 128-byte swizzle
             unsigned char* row = smem + ((R >> 7) * (g.BN >> 6) + (c >> 1)) * 16384 + (R & 127) * 128;
 #pragma unroll
@@ -333,10 +338,13 @@ __global__ void __launch_bounds__(F_THREADS, 1)
               *reinterpret_cast<uint4*>(row + ((((c & 1) * 4 + q) ^ (R & 7)) << 4)) =
                   make_uint4(w[0], w[1], w[2], w[3]);
             }
-          } else if (i < g.M) {
+          } else {
+            // a lane has a row: through shared memory, fp32, an odd number of words per row, so that rows can be
+            // stored (and add read) along their length (4096 × 7298 × 9440: 201 µs, 481 with a row per lane)
+            float* row = reinterpret_cast<float*>(smem) + R * (g.BN + 1) + c0;
 #pragma unroll
             for (int q = 0; q < 32; ++q)
-              if (q < jn) C[at + q] = VT<TO>::from_f(v[q]);
+              if (c0 + q < g.BN) row[q] = v[q];
           }
         } else {
           const int64_t at = int64_t(j0 + c0) * g.M + i;
@@ -359,7 +367,21 @@ __global__ void __launch_bounds__(F_THREADS, 1)
     } else {
       *abrt = 1;
     }
-    if (g.cstore) {
+    if (kOut == kEach) {
+      asm volatile("barrier.sync 1, 256;" ::: "memory");  // the eight epilogue warps, always
+      const int cols = min(g.BN, g.N - j0);
+      const TO* add = static_cast<const TO*>(g.add);
+      TO* C = static_cast<TO*>(g.C);
+      if (ok && !*abrt)
+        for (int r = warp - 2; r < kM && i0 + r < g.M; r += 8) {
+          const float* row = reinterpret_cast<const float*>(smem) + r * (g.BN + 1);
+          const int64_t at = int64_t(i0 + r) * g.N + j0;
+#pragma unroll 4
+          for (int q = lane; q < cols; q += 32)
+            C[at + q] = VT<TO>::from_f(add ? row[q] + VT<TO>::f(add[at + q]) : row[q]);
+        }
+    }
+    if (kOut == kTiles || (kOut == kCols && g.cstore)) {
       tc::fence_async_smem();
       asm volatile("barrier.sync 1, 256;" ::: "memory");  // the eight epilogue warps, always
       if (tid == 0 && ok && !*abrt) {
@@ -384,11 +406,12 @@ __global__ void __launch_bounds__(F_THREADS, 1)
   }
 }
 
-template <typename TO, int MH, bool kRows>
+template <typename TO, int MH, MmOut kOut>
 hsl_status launch_mm(const MmMaps& maps, const MmArgs& g, cudaStream_t s) {
-  void (*fn)(const MmMaps, const MmArgs) = k_mx_matmul<TO, MH, kRows>;
+  void (*fn)(const MmMaps, const MmArgs) = k_mx_matmul<TO, MH, kOut>;
   const int stage = (MH * 128 + g.BN) * 128, scale = (MH * 128 + g.BN) * 16;
-  const int bytes = std::max(g.stages * stage + F_SRING * scale, MH * 128 * g.BN * 2) + 1024;
+  const int tile = kOut == kEach ? MH * 128 * (g.BN + 1) * 4 : MH * 128 * g.BN * 2;  // the epilogue's
+  const int bytes = std::max(g.stages * stage + F_SRING * scale, tile) + 1024;
   if (cudaError_t e = allow_dyn_smem(reinterpret_cast<const void*>(fn), bytes))
     return cuda_fail(e, "4-bit product smem attribute");
   const int64_t tiles = int64_t((g.M + 128 * MH - 1) / (128 * MH)) * ((g.N + g.BN - 1) / g.BN);
@@ -448,13 +471,14 @@ hsl_status mx_matmul_run(const MxOperand& A, int64_t T, const MxOperand& B, int6
     set_message("tensor map encoding failed");
     return HSL_ERR_CUDA;
   }
-  if (dtype == HSL_F32) {
-    if (rows) return mh == 2 ? launch_mm<float, 2, true>(maps, g, s) : launch_mm<float, 1, true>(maps, g, s);
-    return mh == 2 ? launch_mm<float, 2, false>(maps, g, s) : launch_mm<float, 1, false>(maps, g, s);
-  }
   using bf = __nv_bfloat16;
-  if (rows) return mh == 2 ? launch_mm<bf, 2, true>(maps, g, s) : launch_mm<bf, 1, true>(maps, g, s);
-  return mh == 2 ? launch_mm<bf, 2, false>(maps, g, s) : launch_mm<bf, 1, false>(maps, g, s);
+  if (!rows) {
+    if (dtype == HSL_F32) return mh == 2 ? launch_mm<float, 2, kCols>(maps, g, s) : launch_mm<float, 1, kCols>(maps, g, s);
+    return mh == 2 ? launch_mm<bf, 2, kCols>(maps, g, s) : launch_mm<bf, 1, kCols>(maps, g, s);
+  }
+  if (dtype == HSL_F32) return mh == 2 ? launch_mm<float, 2, kEach>(maps, g, s) : launch_mm<float, 1, kEach>(maps, g, s);
+  if (aligned) return mh == 2 ? launch_mm<bf, 2, kTiles>(maps, g, s) : launch_mm<bf, 1, kTiles>(maps, g, s);
+  return mh == 2 ? launch_mm<bf, 2, kEach>(maps, g, s) : launch_mm<bf, 1, kEach>(maps, g, s);
 }
 
 cudaError_t mx_matmul_error_word(uint32_t** p) {

@@ -115,18 +115,6 @@ __device__ __forceinline__ uint32_t int8_codes(float a, float b, float c, float 
   return __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
 }
 
-// w[i] .. from byte `sh` on (0 to 15): NW words out of NW + 4, with the shift in binary steps so that no register
-// is addressed by a variable.
-template <int NW>
-__device__ __forceinline__ void shift_bytes(uint32_t (&w)[NW + 4], uint32_t sh) {
-#pragma unroll
-  for (int i = 0; i < NW + 2; ++i) w[i] = sh & 8 ? w[i + 2] : w[i];
-#pragma unroll
-  for (int i = 0; i < NW + 1; ++i) w[i] = sh & 4 ? w[i + 1] : w[i];
-#pragma unroll
-  for (int i = 0; i < NW; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], (sh & 3) * 8);
-}
-
 // kVec: every half block is whole and 16-byte aligned (cols % 16 == 0, aligned base).  Otherwise a whole half
 // block is put together from the aligned pieces around it, as long as these lie inside X
 // (22859 × 10275 bf16 to int8: 180 µs; value by value 236).
@@ -166,7 +154,7 @@ __global__ void __launch_bounds__(Q_THREADS)
           const uint4 x = __ldg(reinterpret_cast<const uint4*>(low) + j);
           w[4 * j] = x.x; w[4 * j + 1] = x.y; w[4 * j + 2] = x.z; w[4 * j + 3] = x.w;
         }
-        shift_bytes<4 * NV>(w, sh);
+        mx::shift_bytes<4 * NV>(w, sh);
       } else {
 #pragma unroll
       for (int j = 0; j < 16; ++j)
@@ -312,7 +300,7 @@ __global__ void __launch_bounds__(Q_THREADS)
     const bool before = lane > 0 && at[k] > 0 && mine * kSize >= d;  // the lane before stores those
     const bool after = d == 0 || (next > 0 && next * kSize >= d);    // the last piece is whole
     if (mine == 16) {
-      shift_bytes<4 * NV>(w, uint32_t(d));
+      mx::shift_bytes<4 * NV>(w, uint32_t(d));
       char* q = reinterpret_cast<char*>(p) + d;
 #pragma unroll
       for (int j = 0; j < NV; ++j)
