@@ -136,7 +136,10 @@ GradPlan grad_plan(int64_t T, int64_t m, int64_t n, int64_t r) {
     auto pieces = [&](int64_t work, int64_t t, int64_t nk) {
       return std::max<int64_t>(1, std::min<int64_t>(148 * work / (cg + cz) / t, nk / 4));
     };
-    const int64_t sg = pieces(cg, tg, nkg), sz = pieces(cz, tz, nkz);
+    int64_t sg = pieces(cg, tg, nkg), sz = pieces(cz, tz, nkz);
+    // (a product of little work has a piece per tile all the same: a few CTAs above 148 would be a round of their own)
+    if (tg * sg + tz * sz > 148 && tz * sz < 148) sg = std::max<int64_t>(1, std::min(sg, (148 - tz * sz) / tg));
+    if (tg * sg + tz * sz > 148 && tg * sg < 148) sz = std::max<int64_t>(1, std::min(sz, (148 - tg * sg) / tz));
     const int64_t time = std::max((nkg + sg - 1) / sg * per, (nkz + sz - 1) / sz * (cz / (tz * nkz))) +
                          (cg + cz) / 148;
     if (time < best) {
