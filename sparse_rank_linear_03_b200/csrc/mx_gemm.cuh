@@ -179,14 +179,22 @@ template <int V>
 __device__ __forceinline__ void sum_splits(const float* part, int splits, int64_t stride, int64_t at, float (&v)[V]) {
 #pragma unroll
   for (int j = 0; j < V; ++j) v[j] = 0.f;
-#pragma unroll 8
-  for (int s = 0; s < splits; ++s) {
-    const float* p = part + int64_t(s) * stride + at;
-    if (V == 4) {
-      const float4 q = __ldcs(reinterpret_cast<const float4*>(p));
-      v[0] += q.x; v[1 % V] += q.y; v[2 % V] += q.z; v[3 % V] += q.w;
-    } else {
-      v[0] += p[0];
+  for (int s0 = 0; s0 < splits; s0 += 8) {  // eight loads on their way at a time
+    float4 q[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (s0 + j >= splits) continue;
+      const float* p = part + int64_t(s0 + j) * stride + at;
+      if (V == 4) q[j] = __ldcs(reinterpret_cast<const float4*>(p));
+      else q[j].x = __ldcs(p);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (s0 + j >= splits) continue;
+      v[0] += q[j].x;
+      if (V == 4) {
+        v[1 % V] += q[j].y; v[2 % V] += q[j].z; v[3 % V] += q[j].w;
+      }
     }
   }
 }
@@ -261,9 +269,11 @@ bool rings_fit(int ak, bool bmn, int terms, int mh, int bn, int stages) {
          G_SMEM_BUDGET;
 }
 // Cycles of a K-block as measured: widening 256 rows 1040, 128 rows 720 (its chain of waits does not
-// shrink with the rows); copies and MMAs 5 per column and accumulator pair, 3 for one.
+// shrink with the rows); copies and MMAs 5 per column and accumulator pair, 3 for one; with few
+// columns a bf16 A's own bytes, 64 per cycle (2048 tokens, 11008 × 4096, rank 64).
 int64_t kblock_cycles(int ak, int terms, int mh, int bn) {
-  return std::max<int64_t>(a_is_blocks(ak) ? (mh == 2 ? 1040 : 720) : 0, int64_t(terms) * bn * (mh == 2 ? 5 : 3));
+  return std::max<int64_t>(a_is_blocks(ak) ? (mh == 2 ? 1040 : 720) : (mh * 16384 + terms * bn * 128) / 64,
+                           int64_t(terms) * bn * (mh == 2 ? 5 : 3));
 }
 
 // Tile and split of an M × N × K product.

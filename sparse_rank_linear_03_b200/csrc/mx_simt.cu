@@ -187,8 +187,15 @@ __global__ void __launch_bounds__(256)
   const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
   if (e >= count) return;
   float v = 0.f;
-#pragma unroll 8
-  for (int s = 0; s < ranges; ++s) v += part[int64_t(s) * count + e];
+  for (int s0 = 0; s0 < ranges; s0 += 8) {  // eight loads on their way at a time
+    float q[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (s0 + j < ranges) q[j] = __ldcs(part + int64_t(s0 + j) * count + e);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (s0 + j < ranges) v += q[j];
+  }
   if (add) v += VT<TO>::f(add[e]);
   C[e] = VT<TO>::from_f(v);
 }
