@@ -29,6 +29,8 @@
 //   up in warp order, several row tiles at a time.  Where the columns do not fit, K is taken in slices; the rows'
 //   sums stay in shared memory from slice to slice and pass to pass.
 //
+//   28672 × 8192: 30 µs at one token (4.2 TB/s over the whole call, launch and tail included), 44 at eight.
+//
 // f32 (k_mx_decode_f32): a lane per row, tokens broadcast from shared memory, fp32 FMA, K in ranges.
 #include <cuda.h>
 #include <cuda_fp16.h>

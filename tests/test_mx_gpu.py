@@ -268,6 +268,36 @@ def test_apply_tokens_of_any_range(hsl, T, m, n):
     hsl.mx_check()
 
 
+@pytest.mark.parametrize("T,m,n", [(1, 40, 28672), (2, 2400, 28672), (3, 17, 30001), (4, 48, 16384), (8, 40, 11008),
+                                   (7, 33, 28672)])
+def test_apply_long_tokens_of_any_range(hsl, T, m, n):
+    """The same where the columns of all tokens, or two per token, do not fit a CTA's shared memory."""
+    test_apply_tokens_of_any_range(hsl, T, m, n)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [7, 8, 9, 16, 31, 32, 33, 65])
+@pytest.mark.parametrize("m,n", [(70, 1500), (1000, 4200)])
+def test_apply_where_kernels_change(hsl, T, m, n, dtype):
+    D, d = blocks(hsl, weights(m, n, T), "e2m1")
+    t, add = tensor(tokens(T, n, T + 1), dtype), tensor(tokens(T, m, T + 2), dtype)
+    want, mag = mx.apply(d, f64(t)) + f64(add), mx.apply(np.abs(d), np.abs(f64(t))) + np.abs(f64(add))
+    close(hsl.mx4_apply(D, t, add=add), want, mag, n, dtype)
+    close(hsl.mx4_apply(D, t, Y=add, add=add), want, mag, n, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,m,n", [(256, 65, 96), (300, 257, 130), (513, 1023, 64), (270, 520, 300)])
+def test_matmul_rows_off_sixteen_bytes(hsl, T, m, n, dtype):
+    A, a = blocks(hsl, tokens(T, n, 5), "e2m1")
+    B, b = blocks(hsl, weights(m, n, 6), "e2m1")
+    add = tensor(tokens(T, m, 7), dtype)
+    want, mag = a @ b.T + f64(add), np.abs(a) @ np.abs(b).T + np.abs(f64(add))
+    close(hsl.mx4_matmul(A, B, dtype=dtype, add=add), want, mag, n, dtype)
+    close(hsl.mx4_matmul(A, B, dtype=dtype), want - f64(add), mag, n, dtype)
+    close(hsl.mx4_matmul(A, B, Y=add, dtype=dtype, add=add), want, mag, n, dtype)
+
+
 @pytest.mark.parametrize("T", [1, 3, 17, 70])
 def test_apply_infinities_and_nan(hsl, T):
     """An infinity or a NaN in a token reaches its outputs and no other token's; a NaN block
