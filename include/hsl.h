@@ -389,10 +389,10 @@ hsl_status hsl_mx4_matmul(const hsl_mx* A, const hsl_mx* B, const void* add, voi
  *   Z = X V, G = dY U;  dU = dYᵀ Z, dV = Xᵀ G, dX = G Vᵀ (+ add)
  * X [T][n] blocks (T = X.rows; T = 0 writes zeros to dU and dV), dY [T][m],
  * U and dU [m][r], V and dV [n][r], dX and add [T][n] of dtype; dX may be NULL
- * (then add must be), add may be NULL or dX itself.  1 ≤ r ≤ 256.  Z and G are
- * kept to 16 bits of significand or more, sums in fp32.  With an infinity in dY,
- * U or V, what is infinite by the formulas may come out as a NaN (and nothing else
- * is touched).
+ * (then add must be), add may be NULL or dX itself.  1 ≤ r ≤ 256.  Sums are fp32,
+ * and so are Z and G (bf16: below 2^−109 to the nearest multiple of about 2^−133).
+ * With an infinity in dY, U or V, what is infinite by the formulas may come out as a
+ * NaN (and nothing else is touched).
  * [HSS] §Implementation and operational patterns, backward pass (the gradients
  * of U and V, as derived from the forward decomposition). */
 hsl_status hsl_mx8_factor_grad(const hsl_mx* X, const void* dY, int64_t m, const void* U,

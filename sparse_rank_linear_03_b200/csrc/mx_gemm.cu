@@ -73,7 +73,7 @@ hsl_status mx_gemm_apply_run(bool trans, const MxOperand& D, int64_t m, int64_t 
   g.add = static_cast<const __nv_bfloat16*>(add);
   g.C = static_cast<__nv_bfloat16*>(Y);
   g.part = reinterpret_cast<float*>(w);
-  if (!make_tmap_2d(&maps.b0, kBF, 2, X, T, K, kp, 64, sh.BN, kSW) ||
+  if (!make_tmap_2d(&maps.b[0], kBF, 2, X, T, K, kp, 64, sh.BN, kSW) ||
       !block_maps(&maps, trans ? A_E2M1_M : A_E2M1_K, sh.MH, D, m))
     return map_failed();
   if (sh.splits > 1) {

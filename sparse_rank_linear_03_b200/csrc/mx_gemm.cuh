@@ -1,11 +1,11 @@
 // Products on the tensor cores with one factor held in microscaled blocks.
 //
-//   C = A · (B0 + B1)ᵀ (+ add),   A [M][K], B [N][K], fp32 sums in TMEM
+//   C = A · (B0 + B1 + B2)ᵀ (+ add),   A [M][K], B [N][K], fp32 sums in TMEM
 //
 // A is the large factor: a 4-bit weight matrix, an 8-bit checkpoint, or a bf16
 // matrix, each either stored as [M][K] or used transposed from [K][M].  B is a bf16
-// matrix (tokens, factors), stored as [N][K] or [K][N]; B1 is the low part of a
-// value held as a bf16 pair.  The same tile serves the forward product (M = features,
+// matrix (tokens, factors), stored as [N][K] or [K][N], or an fp32 matrix held as three bf16
+// parts.  The same tile serves the forward product (M = features,
 // N = tokens), its input gradient (the same matrix, transposed) and the skinny
 // products of the factors' gradients (N = r).
 //
@@ -53,6 +53,7 @@ __device__ uint32_t g_mx_gemm_err;
 constexpr int G_BK = 64;
 constexpr int G_THREADS = 608;   // 19 warps: copies, MMA, 2 × 8 widening (all 16 in the epilogue), code copies
 constexpr int G_MAX_STAGES = 8;
+constexpr int G_MAX_TERMS = 12;
 constexpr int G_SMEM_BUDGET = 224 * 1024;  // stages and code tiles; barriers and alignment take 2 KB more
 
 enum AKind { A_BF16_K, A_BF16_M, A_E2M1_K, A_E2M1_M, A_INT8_K, A_INT8_M };
@@ -64,8 +65,7 @@ constexpr bool a_is_int8(int a) { return a == A_INT8_K || a == A_INT8_M; }
 
 struct GemmMaps {
   CUtensorMap a;   // bf16 A: box {64, 128} (K-major) or {64, 64}
-  CUtensorMap b0;  // B: box {64, BN} (K-major) or {64, 64}
-  CUtensorMap b1;  // low part
+  CUtensorMap b[3];  // B, or its parts: box {64, BN} (K-major) or {64, 64}
   CUtensorMap c;   // OUT_T: box {128·MH, BN}
   CUtensorMap add; // like c
   CUtensorMap q;   // codes: box {CodeTile::kInner bytes, CodeTile::kRows}
@@ -78,6 +78,7 @@ struct GemmArgs {
   int M, N, nk;      // nk: K-blocks of 64
   int BN, stages, splits;
   int codes;         // code tiles in flight
+  int terms;         // tiles of B in flight, where B has several terms
   int cstore;        // OUT_T: tiled store possible
   int addt;          // OUT_T: add comes as a tile as well
   const __nv_bfloat16* add;
@@ -243,30 +244,35 @@ unsigned blocks_of(int64_t count) { return unsigned((count + 255) / 256); }
 
 // ---- host ---------------------------------------------------------------------
 struct GemmShape {
-  int BN, MH, splits, stages, codes;
+  int BN, MH, splits, stages, codes, terms;
 };
 
 int code_bytes(int ak, int mh) {
   if (!a_is_blocks(ak)) return 0;
   return 128 * mh * (a_is_int8(ak) ? 64 : 32) + (a_is_mmajor(ak) ? 1024 : 0);
 }
-int stage_bytes(bool bmn, int terms, int mh, int bn) {
-  return mh * 16384 + terms * (bmn ? (bn + 63) / 64 * 8192 : bn * 128);
-}
+int a_bytes(int mh) { return mh * 16384; }
+int b_bytes(bool bmn, int bn) { return bmn ? (bn + 63) / 64 * 8192 : bn * 128; }
 
-// Stages and code tiles of a tile shape.  Code tiles are small and come from farther away than
-// anything else: four of them in flight at least, then as many stages as fit (two at
-// least: a pair of terms with an 8-bit factor leaves room for them only with one
-// accumulator), then more code tiles, an even number.
-void fit_rings(GemmShape* s, int ak, bool bmn, int terms) {
-  const int code = code_bytes(ak, s->MH), stage = stage_bytes(bmn, terms, s->MH, s->BN);
-  s->codes = code ? 4 : 0;
-  s->stages = std::min(G_MAX_STAGES, (G_SMEM_BUDGET - s->codes * code) / stage);
-  if (code) s->codes = std::min(G_MAX_STAGES, (G_SMEM_BUDGET - s->stages * stage) / code) & ~1;
-}
+// Whether a shape has room for so many stages; with several terms, for all of their tiles but those that the
+// last of these stages needs behind its first.
 bool rings_fit(int ak, bool bmn, int terms, int mh, int bn, int stages) {
-  return stages * stage_bytes(bmn, terms, mh, bn) + (a_is_blocks(ak) ? 4 : 0) * code_bytes(ak, mh) <=
-         G_SMEM_BUDGET;
+  const int tiles = terms > 1 ? terms * (stages - 1) + 1 : stages;
+  return tiles <= G_MAX_TERMS && stages * a_bytes(mh) + tiles * b_bytes(bmn, bn) +
+                                         (a_is_blocks(ak) ? 4 : 0) * code_bytes(ak, mh) <=
+                                     G_SMEM_BUDGET;
+}
+// Stages, code tiles and tiles of B's terms of a tile shape.  Code tiles are small and come from farther away
+// than anything else: four of them in flight at least, then as many stages as fit (two at least), then more code
+// tiles, an even number.
+void fit_rings(GemmShape* s, int ak, bool bmn, int terms) {
+  const int code = code_bytes(ak, s->MH), b = b_bytes(bmn, s->BN);
+  s->stages = 2;
+  while (s->stages < G_MAX_STAGES && rings_fit(ak, bmn, terms, s->MH, s->BN, s->stages + 1)) ++s->stages;
+  int left = G_SMEM_BUDGET - s->stages * a_bytes(s->MH) - (code ? 4 : 0) * code;
+  s->terms = terms > 1 ? std::min({terms * s->stages, left / b, G_MAX_TERMS}) : 0;
+  left -= (terms > 1 ? s->terms : s->stages) * b;
+  s->codes = code ? std::min(G_MAX_STAGES, 4 + left / code) & ~1 : 0;
 }
 // Cycles of a K-block as measured: widening 256 rows 1040, 128 rows 720 (its chain of waits does not
 // shrink with the rows); copies and MMAs 5 per column and accumulator pair, 3 for one; with few
@@ -323,7 +329,8 @@ GemmShape shape_of(int ak, int64_t M, int64_t N, int64_t K, bool bmn, int terms,
 }
 
 int tile_smem(int ak, bool bmn, int terms, int mh, bool staged, const GemmArgs& g) {
-  int bytes = g.stages * stage_bytes(bmn, terms, mh, g.BN) + g.codes * code_bytes(ak, mh);
+  int bytes = g.stages * a_bytes(mh) + (terms > 1 ? g.terms : g.stages) * b_bytes(bmn, g.BN) +
+              g.codes * code_bytes(ak, mh);
   if (staged) bytes = std::max(bytes, mh * 128 * g.BN * 2);  // the epilogue's tile
   return bytes + 1024;
 }

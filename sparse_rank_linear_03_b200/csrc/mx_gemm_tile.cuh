@@ -7,8 +7,12 @@
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   // (an offset, not a rounded integer: the compiler still knows that this is shared memory)
   unsigned char* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
-  __shared__ uint64_t full[G_MAX_STAGES], empty[G_MAX_STAGES], accf, addf;
+  __shared__ uint64_t full[G_MAX_STAGES], empty[G_MAX_STAGES], accf[2], drained[2], quiet, addf;
   __shared__ uint64_t raw[G_MAX_STAGES], taken[G_MAX_STAGES];  // code tile landed, read
+  // One term of B comes with its stage.  Several have a ring of their own, a tile of one term each, so that
+  // what is in flight need not be whole K-blocks.
+  constexpr bool kTerms = TERMS > 1;
+  __shared__ uint64_t tfull[kTerms ? G_MAX_TERMS : 1], tempty[kTerms ? G_MAX_TERMS : 1];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
 
@@ -22,25 +26,45 @@
   const int bgroups = (g.BN + 63) / 64;
   const int kB = BMN ? bgroups * 8192 : g.BN * 128;
   using Code = CodeTile<AK, MH>;
-  const int kStage = kA + TERMS * kB;
-  unsigned char* cring = smem + g.stages * kStage;
-  uint32_t cols = MH == 2 ? 64 : 32;  // whole 32-column reads past 2 × 16 columns stay inside
-  while (cols < uint32_t(MH * g.BN)) cols *= 2;
+  const int kStage = kA + (kTerms ? 0 : kB);
+  unsigned char* tring = smem + g.stages * kStage;
+  unsigned char* cring = tring + (kTerms ? g.terms * kB : 0);
+  // The tensor unit cuts every sum off towards zero.  Over the hundreds of inexact terms of a gradient that
+  // adds up to 2^−16 of the result (28672 × 8192, 4096 tokens), so there a chain of kChunk K-blocks goes to one of
+  // two accumulators in turn, and the sixteen warps add the other to fp32 sums in registers, rounded to nearest.
+  constexpr bool kFold = OUT == OUT_R;
+  constexpr int kChunk = TERMS > 1 ? 2 : 4;
+  constexpr int kSteps = kFold ? MH : 1;  // 32-column pieces of an accumulator per warp, at BN <= 128
+  const int nchunks = (nk + kChunk - 1) / kChunk, aset = MH * g.BN;  // columns of a set of accumulators
+  // (whole 32-column reads from the last accumulator stay inside)
+  const uint32_t need = uint32_t((kFold ? 2 : 1) * aset - g.BN + (g.BN + 31) / 32 * 32);
+  uint32_t cols = 32;
+  while (cols < need) cols *= 2;
 
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int s = 0; s < g.stages; ++s) {
-      tc::mbar_init(&full[s], a_is_blocks(AK) ? 1 + 8 : 1);  // copies, and the eight widening warps
+      // copies, and the eight widening warps
+      tc::mbar_init(&full[s], a_is_blocks(AK) ? (kTerms ? 0 : 1) + 8 : 1);
       tc::mbar_init(&empty[s], 1);
     }
+    if (kTerms)
+      for (int s = 0; s < g.terms; ++s) {
+        tc::mbar_init(&tfull[s], 1);
+        tc::mbar_init(&tempty[s], 1);
+      }
     for (int s = 0; s < g.codes; ++s) {
       tc::mbar_init(&raw[s], 1);
       tc::mbar_init(&taken[s], 8);
     }
-    tc::mbar_init(&accf, 1);
+    for (int p = 0; p < 2; ++p) {
+      tc::mbar_init(&accf[p], 1);
+      tc::mbar_init(&drained[p], 16);
+    }
+    tc::mbar_init(&quiet, 1);
     tc::mbar_init(&addf, 1);
     tc::fence_mbar_init();
-    tc::prefetch_tmap(&maps.b0);
+    tc::prefetch_tmap(&maps.b[0]);
   }
   if (warp == 1) {
     tc::tmem_alloc(&tmem_slot, cols);
@@ -58,43 +82,60 @@
   if (warp == 0) {
     if (lane == 0) {
       if (OUT == OUT_T && g.addt) tc::tma_prefetch_2d(&maps.add, i0, j0);  // into L2 for the epilogue
-      int s = 0, issued = 0;
-      uint32_t ph = 1;
-      for (int kb = 0; kb < nk; ++kb) {
-        if (!g_wait(&empty[s], ph, abrt)) break;
-        unsigned char* a = smem + s * kStage;
-        unsigned char* b = a + kA;
-        const int k0 = (kb0 + kb) * G_BK;
-        tc::mbar_expect_tx(&full[s], (a_is_blocks(AK) ? 0 : kA) + TERMS * kB);
-        if (AK == A_BF16_K) {
-#pragma unroll
-          for (int h = 0; h < MH; ++h)
-            tc::tma_load_2d(a + h * 16384, &maps.a, k0, i0 + h * 128, &full[s]);
-        } else if (AK == A_BF16_M) {
-#pragma unroll
-          for (int h = 0; h < 2 * MH; ++h)
-            tc::tma_load_2d(a + h * 8192, &maps.a, i0 + h * 64, k0, &full[s]);
+      int s = 0, issued = 0, ts = 0, tissued = 0;
+      uint32_t ph = 1, tph = 1;
+      auto copy_b = [&](unsigned char* b, int t, int k0, uint64_t* bar) {
+        if (BMN) {
+          for (int q = 0; q < bgroups; ++q) tc::tma_load_2d(b + q * 8192, &maps.b[t], j0 + q * 64, k0, bar);
+        } else {
+          tc::tma_load_2d(b, &maps.b[t], k0, j0, bar);
         }
+      };
+      constexpr bool kCopies = !a_is_blocks(AK) || !kTerms;  // something here belongs to a stage
+      for (int kb = 0; kb < nk; ++kb) {
+        const int k0 = (kb0 + kb) * G_BK;
+        if (kCopies) {
+          if (!g_wait(&empty[s], ph, abrt)) break;
+          unsigned char* a = smem + s * kStage;
+          tc::mbar_expect_tx(&full[s], (a_is_blocks(AK) ? 0 : kA) + (kTerms ? 0 : kB));
+          if (AK == A_BF16_K) {
 #pragma unroll
-        for (int t = 0; t < TERMS; ++t) {
-          const CUtensorMap* map = t ? &maps.b1 : &maps.b0;
-          if (BMN) {
-            for (int q = 0; q < bgroups; ++q)
-              tc::tma_load_2d(b + t * kB + q * 8192, map, j0 + q * 64, k0, &full[s]);
-          } else {
-            tc::tma_load_2d(b + t * kB, map, k0, j0, &full[s]);
+            for (int h = 0; h < MH; ++h)
+              tc::tma_load_2d(a + h * 16384, &maps.a, k0, i0 + h * 128, &full[s]);
+          } else if (AK == A_BF16_M) {
+#pragma unroll
+            for (int h = 0; h < 2 * MH; ++h)
+              tc::tma_load_2d(a + h * 8192, &maps.a, i0 + h * 64, k0, &full[s]);
+          }
+          if (!kTerms) copy_b(a + kA, 0, k0, &full[s]);
+          ++issued;
+          if (++s == g.stages) {
+            s = 0;
+            ph ^= 1;
           }
         }
-        ++issued;
-        if (++s == g.stages) {
-          s = 0;
-          ph ^= 1;
+        if (kTerms) {
+          bool live = true;
+#pragma unroll
+          for (int t = 0; t < TERMS; ++t) {
+            if (!live || !(live = g_wait(&tempty[ts], tph, abrt))) break;
+            tc::mbar_expect_tx(&tfull[ts], kB);
+            copy_b(tring + ts * kB, t, k0, &tfull[ts]);
+            ++tissued;
+            if (++ts == g.terms) {
+              ts = 0;
+              tph ^= 1;
+            }
+          }
+          if (!live) break;
         }
       }
       // the copies in flight have landed before the CTA's shared memory is given up
-      for (int q = 0; q < g.stages && q < issued; ++q) {
-        const int last = (issued - 1 - q) / g.stages;  // uses of stage q before its last one
-        if (*abrt) tc::mbar_wait(&full[q], uint32_t(last) & 1, &g_mx_gemm_err);
+      if (*abrt) {
+        for (int q = 0; q < g.stages && q < issued; ++q)  // (uses of stage q before its last one)
+          tc::mbar_wait(&full[q], uint32_t((issued - 1 - q) / g.stages) & 1, &g_mx_gemm_err);
+        for (int q = 0; kTerms && q < g.terms && q < tissued; ++q)
+          tc::mbar_wait(&tfull[q], uint32_t((tissued - 1 - q) / g.terms) & 1, &g_mx_gemm_err);
       }
     }
     __syncwarp();
@@ -134,37 +175,108 @@
     if (tc::elect_one()) {
       const uint32_t idesc = tc::idesc_bf16(128, g.BN) | (a_is_mmajor(AK) ? 1u << 15 : 0u) |
                              (BMN ? 1u << 16 : 0u);
-      int s = 0;
-      uint32_t ph = 0;
+      int s = 0, ts = 0;
+      uint32_t ph = 0, tph = 0;
+      bool live = true;
       for (int kb = 0; kb < nk; ++kb) {
+        const int chunk = kFold ? kb / kChunk : 0;
+        const bool first = kFold ? kb % kChunk == 0 : kb == 0;
+        if (kFold && first && !g_wait(&drained[chunk & 1], ((chunk >> 1) + 1) & 1, abrt)) break;
         if (!g_wait(&full[s], ph, abrt)) break;
         tc::tc_fence_after();
         unsigned char* a = smem + s * kStage;
+        const uint32_t acc = tmem + uint32_t((chunk & 1) * aset);
 #pragma unroll
         for (int t = 0; t < TERMS; ++t) {
-          const uint64_t bd = BMN ? desc_mn_sw128(a + kA + t * kB) : tc::desc_sw128(a + kA + t * kB);
+          if (kTerms) {
+            if (!live || !(live = g_wait(&tfull[ts], tph, abrt))) break;
+            tc::tc_fence_after();
+          }
+          unsigned char* b = kTerms ? tring + ts * kB : a + kA;
+          const uint64_t bd = BMN ? desc_mn_sw128(b) : tc::desc_sw128(b);
 #pragma unroll
           for (int h = 0; h < MH; ++h) {
             const uint64_t ad =
                 a_is_mmajor(AK) ? desc_mn_sw128(a + h * 16384) : tc::desc_sw128(a + h * 16384);
 #pragma unroll
             for (int k = 0; k < G_BK / 16; ++k)
-              tc::mma_bf16(tmem + h * g.BN, tc::desc_advance(ad, k * (a_is_mmajor(AK) ? 2048 : 32)),
+              tc::mma_bf16(acc + h * g.BN, tc::desc_advance(ad, k * (a_is_mmajor(AK) ? 2048 : 32)),
                            tc::desc_advance(bd, k * (BMN ? 2048 : 32)), idesc,
-                           (kb > 0 || k > 0 || t > 0) ? 1u : 0u);
+                           (!first || k > 0 || t > 0) ? 1u : 0u);
+          }
+          if (kTerms) {
+            tc::mma_commit(&tempty[ts]);
+            if (++ts == g.terms) {
+              ts = 0;
+              tph ^= 1;
+            }
           }
         }
+        if (!live) break;
         tc::mma_commit(&empty[s]);
+        if (kFold && (kb % kChunk == kChunk - 1 || kb == nk - 1)) tc::mma_commit(&accf[chunk & 1]);
         if (++s == g.stages) {
           s = 0;
           ph ^= 1;
         }
       }
-      tc::mma_commit(&accf);
+      if (!kFold) tc::mma_commit(&accf[0]);
+      if (kFold && *abrt) {  // nothing may write to TMEM when it is given back
+        tc::mma_commit(&quiet);
+        tc::mbar_wait(&quiet, 0, &g_mx_gemm_err);
+      }
     }
     __syncwarp();
   } else {
     const int tid = (threadIdx.x - 64) & 255, group = (warp - 2) >> 3;
+    // accumulators: warp w reaches TMEM lanes 32 (w mod 4) onwards; the four groups of four
+    // warps divide the accumulators and their columns, in steps of 32 (the last step may reach past BN,
+    // inside the allocation)
+    int R, i, c_lo, c_hi;
+    uint32_t tb;
+    auto place = [&] {  // (called where it is first needed: these registers are dear to the widening)
+      const int grp = (warp - 2) >> 2;
+      const int half = MH == 2 ? grp & 1 : 0;
+      R = half * 128 + (((warp & 3) << 5) | lane);
+      i = i0 + R;
+      tb = tmem + (uint32_t((warp & 3) * 32) << 16) + uint32_t(half * g.BN);
+      const int steps = (g.BN + 31) / 32;
+      constexpr int kShare = 4 / MH;  // groups of four warps per accumulator
+      c_lo = steps * (grp / MH) / kShare;
+      c_hi = steps * (grp / MH + 1) / kShare;
+    };
+    if (kFold) place();
+    float sum[kSteps][32];
+    if (kFold) {
+#pragma unroll
+      for (int q = 0; q < kSteps; ++q)
+#pragma unroll
+        for (int z = 0; z < 32; ++z) sum[q][z] = 0.f;
+    }
+    int folded = 0;
+    bool live = true;
+    // adds the chunks before `end` to the sums
+    auto fold = [&](int end) {
+      for (; live && folded < end; ++folded) {
+        const int p = folded & 1;
+        live = __all_sync(0xFFFFFFFFu, g_wait(&accf[p], (folded >> 1) & 1, abrt));
+        if (!live) break;
+        tc::tc_fence_after();
+#pragma unroll
+        for (int q = 0; q < 2 * kSteps; ++q) {
+          const int c0 = c_lo * 32 + q * 16;
+          if (c0 >= min(c_hi * 32, g.BN)) continue;
+          float v[16];
+          tc::tmem_ld16(tb + uint32_t(p * aset + c0), v);
+#pragma unroll
+          for (int z = 0; z < 16; ++z) sum[q >> 1][(q & 1) * 16 + z] += v[z];
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&drained[p]);
+      }
+      return live;
+    };
     if (a_is_blocks(AK)) {
       constexpr bool kInt8 = a_is_int8(AK);
       // MH = 2: tile row tid, both blocks; MH = 1: two threads share a tile row
@@ -187,6 +299,8 @@
       const uint32_t smem32 = tc::smem_u32(smem) + trow * 128 + ((trow & 7) << 4);
       for (int kb = group; kb < nk; kb += 2) {
         Block<kInt8> blk[MH];
+        // (behind the widening of a chunk the MMAs of the one before are done, or soon will be)
+        if (kFold && !fold(kb / kChunk - 1)) break;
         if (!g_wait(&raw[cs], cph, abrt)) break;
         const unsigned char* q = cring + cs * Code::kBytes;
 #pragma unroll
@@ -242,10 +356,8 @@
         }
       }
     }
-    // epilogue: warp w reaches TMEM lanes 32 (w mod 4) onwards; the four groups of four
-    // warps divide the accumulators and their columns
     __syncwarp();
-    bool ok = tc::mbar_wait(&accf, 0, &g_mx_gemm_err) && !*abrt;
+    bool ok = (kFold ? fold(nchunks) : tc::mbar_wait(&accf[0], 0, &g_mx_gemm_err)) && !*abrt;
     __nv_bfloat16* stg = reinterpret_cast<__nv_bfloat16*>(smem);
     if (OUT == OUT_T && g.addt && ok) {
       // the tile of add into the idle ring, where each value is replaced by the result (loads of
@@ -258,25 +370,18 @@
     }
     if (ok) {
       tc::tc_fence_after();
-      const int grp = (warp - 2) >> 2;
-      const int acc = MH == 2 ? grp & 1 : 0;
-      const int L = ((warp & 3) << 5) | lane;
-      const int R = acc * 128 + L;
-      const int i = i0 + R;
-      const uint32_t tb = tmem + (uint32_t((warp & 3) * 32) << 16) + uint32_t(acc * g.BN);
-      // columns in steps of 32 (the last step may reach past BN, inside the allocation)
-      const int steps = (g.BN + 31) / 32;
-      constexpr int kShare = 4 / MH;  // groups of four warps per accumulator
-      const int part = grp / MH;
-      const int c_lo = steps * part / kShare, c_hi = steps * (part + 1) / kShare;
-#pragma unroll 1
-      for (int c = c_lo; c < c_hi; ++c) {
-        const int c0 = c * 32;
+      if (!kFold) place();
+      const int mine = kFold ? kSteps : c_hi - c_lo;
+#pragma unroll (kFold ? kSteps : 1)
+      for (int q32 = 0; q32 < mine; ++q32) {
+        const int c0 = (c_lo + q32) * 32;
+        if (kFold && c_lo + q32 >= c_hi) break;
         float v[32];
-        tc::tmem_ld32(tb + c0, v);
-        if (nk == 0) {
+        if (kFold) {
 #pragma unroll
-          for (int q = 0; q < 32; ++q) v[q] = 0.f;
+          for (int q = 0; q < 32; ++q) v[q] = sum[kFold ? q32 : 0][q];
+        } else {
+          tc::tmem_ld32(tb + c0, v);
         }
         const int jn = min(32, min(g.BN - c0, g.N - j0 - c0));  // columns of this step in the tile
         if (OUT == OUT_T || OUT == OUT_T_PART) {

@@ -4,15 +4,21 @@
 //
 // Five skinny products in two launches (first Z and G, then the three that use them),
 // each launch one grid whose CTAs take tiles of one product or another: alone, most of
-// them have fewer tiles than SMs or leave a last round half empty (28672 × 8192, rank
-// 256, 4096 tokens: 317 µs as five launches, 260 so).  The second launch takes two thirds of
-// that: two terms per product, and 96 KB from L2 per 256 × 256 × 64 step.  Z and G are summed over their
-// splits into bf16 pairs (hi + lo, 16 significant bits), which the second
-// products take as two terms.
+// them have fewer tiles than SMs or leave a last round half empty.  Z and G are fp32 sums over their
+// splits and stay so: three bf16 parts, which the second products take as three terms.  Sums over tokens, features
+// and columns leave the tensor unit every 8 to 24 of its steps (kFold in mx_gemm_tile.cuh); that and the three
+// parts bring the results from 2^−16 of their size to the error of fp32 sums.  28672 × 8192, rank 256, 4096
+// tokens: 431 µs, of which the second launch takes 270 (301 µs with two parts and sums that stay in the tensor
+// unit: tiles of 256 columns instead of 128 then have room); 4096 × 4096, rank 128, 500 tokens: 30.2 (26.0) µs.
+// What bounds the second launch: 80 KB from L2 per 256 × 128 × 64 step of three terms, 7 TB/s in all.
 #include "mx_gemm.cuh"
 
 namespace hsl {
 namespace {
+
+// Z and G are fp32 sums and stay so: hi + mid + lo, three bf16 whose bits together are the 24 of an fp32 value
+// (below 2^−109 the last of them pass the end of bf16's range: each part is off by 2^−134 at most).
+constexpr int Z_TERMS = 3;
 
 // Each branch is the tile of one product (mx_gemm_tile.cuh).
 template <int MG>
@@ -40,7 +46,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     k_mx_grad_second(const __grid_constant__ GemmMaps um, const __grid_constant__ GemmMaps vm,
                      const __grid_constant__ GemmMaps xm, const __grid_constant__ GemmArgs ua,
                      const __grid_constant__ GemmArgs va, const __grid_constant__ GemmArgs xa, int nu, int nv) {
-  constexpr int TERMS = 2;
+  constexpr int TERMS = Z_TERMS;
   if (int(blockIdx.x) < nu) {
     constexpr bool BMN = true;
     constexpr int AK = A_BF16_M, MH = MU, OUT = OUT_R;
@@ -65,12 +71,13 @@ __global__ void __launch_bounds__(G_THREADS, 1)
   }
 }
 
-// A sum over splits, and where it goes: a bf16 pair with rows padded to `pitch`, or bf16.
+// A sum over splits, and where it goes: Z_TERMS bf16 matrices, `apart` elements from one to the next, with rows
+// padded to `pitch`; or one (apart = 0, pitch = n).
 struct SumJob {
   const float* part;
   int splits, n, pitch;
-  int64_t rows;
-  __nv_bfloat16 *hi, *lo;  // lo: nullptr for a plain result (pitch = n)
+  int64_t rows, apart;
+  __nv_bfloat16* out;
 };
 template <int V>
 __device__ __forceinline__ void sum_job(const SumJob& j, int64_t e) {
@@ -81,19 +88,22 @@ __device__ __forceinline__ void sum_job(const SumJob& j, int64_t e) {
 #pragma unroll
   for (int q = 0; q < V; ++q) v[q] = 0.f;
   if (c < j.n) sum_splits<V>(j.part, j.splits, j.rows * j.n, row * j.n + c, v);  // (V = 4: n = pitch)
-  if (j.lo) {
-    float low[V];
+  if (j.apart) {
 #pragma unroll
-    for (int q = 0; q < V; ++q) {
-      // (an infinity has no low part; a finite sum keeps a finite high part)
-      float hi = __bfloat162float(__float2bfloat16_rn(v[q]));
-      if (isinf(hi)) hi = __bfloat162float(__float2bfloat16_rz(v[q]));
-      low[q] = isinf(hi) ? 0.f : v[q] - hi;
-      v[q] = hi;
+    for (int t = 0; t < Z_TERMS - 1; ++t) {
+      // (an infinity has no low parts; a finite sum keeps a finite high part)
+      float hi[V];
+#pragma unroll
+      for (int q = 0; q < V; ++q) {
+        hi[q] = __bfloat162float(__float2bfloat16_rn(v[q]));
+        if (isinf(hi[q])) hi[q] = __bfloat162float(__float2bfloat16_rz(v[q]));
+        v[q] = isinf(hi[q]) ? 0.f : v[q] - hi[q];
+      }
+      store_bf<V>(j.out + t * j.apart + e, hi);
     }
-    store_bf<V>(j.lo + e, low);
+    e += (Z_TERMS - 1) * j.apart;
   }
-  store_bf<V>(j.hi + e, v);
+  store_bf<V>(j.out + e, v);
 }
 template <int V>
 __global__ void __launch_bounds__(256)
@@ -115,39 +125,49 @@ hsl_status sum_run(const SumJob& a, const SumJob& b, bool vec, cudaStream_t s) {
 struct GradPlan {
   int64_t rp, mp;  // padded pitches of r- and m-wide rows
   GemmShape z, g, u, v, x;
-  size_t off_dy, off_u, off_v, off_zh, off_zl, off_gh, off_gl, off_pa, off_pb, total;
+  int64_t zpart;   // elements of one part of Z or G
+  size_t off_dy, off_u, off_v, off_z, off_g, off_pa, off_pb, total;
 };
 GradPlan grad_plan(int64_t T, int64_t m, int64_t n, int64_t r) {
   GradPlan p;
   p.rp = round_up(r, 8);
   p.mp = round_up(m, 8);
-  const int bn = int(round_up(r, 16));
-  auto tiles = [](int64_t rows, int mh) { return (rows + 128 * mh - 1) / (128 * mh); };
+  // columns of a tile: two sets of accumulators of up to 2 × 128 in TMEM
+  const int64_t ntn = (r + 127) / 128;
+  const int bn = int(round_up((r + ntn - 1) / ntn, 16));
+  auto tiles = [&](int64_t rows, int mh) { return (rows + 128 * mh - 1) / (128 * mh) * ntn; };
   const int64_t nkg = (m + 63) / 64, nkz = (n + 63) / 64, nkt = (T + 63) / 64;
 
-  // First launch: the SMs are shared out by work, K split accordingly, at least 4 K-blocks a
-  // piece.
+  // First launch: pieces of G, at least 4 K-blocks each, in one round of CTAs, and pieces of Z beside and behind
+  // them: shares of the SMs by work, or a whole round of G with Z in smaller pieces that take the SMs as
+  // they come free, whichever is done earlier (28672 × 8192, rank 256, 4096 tokens: 64 CTAs of G and 64 of Z
+  // leave most SMs idle while G's end, 128 and 192 keep them busy).
   p.z.MH = 1;
   p.z.BN = p.g.BN = bn;
-  const int64_t tz = tiles(T, 1), cz = tz * nkz * kblock_cycles(A_INT8_K, 1, 1, bn);
+  const int64_t tz = tiles(T, 1), perz = kblock_cycles(A_INT8_K, 1, 1, bn);
   int64_t best = INT64_MAX;
   for (int mh = 1; mh <= 2; ++mh) {
-    const int64_t tg = tiles(T, mh), per = kblock_cycles(A_BF16_K, 1, mh, bn), cg = tg * nkg * per;
-    auto pieces = [&](int64_t work, int64_t t, int64_t nk) {
-      return std::max<int64_t>(1, std::min<int64_t>(148 * work / (cg + cz) / t, nk / 4));
-    };
-    int64_t sg = pieces(cg, tg, nkg), sz = pieces(cz, tz, nkz);
-    // (a product of little work has a piece per tile all the same: a few CTAs above 148 would be a round of their own)
-    if (tg * sg + tz * sz > 148 && tz * sz < 148) sg = std::max<int64_t>(1, std::min(sg, (148 - tz * sz) / tg));
-    if (tg * sg + tz * sz > 148 && tg * sg < 148) sz = std::max<int64_t>(1, std::min(sz, (148 - tg * sg) / tz));
-    const int64_t time = std::max((nkg + sg - 1) / sg * per, (nkz + sz - 1) / sz * (cz / (tz * nkz))) +
-                         (cg + cz) / 148;
-    if (time < best) {
+    const int64_t tg = tiles(T, mh), perg = kblock_cycles(A_BF16_K, 1, mh, bn);
+    const int64_t cg = tg * nkg * perg, cz = tz * nkz * perz, topg = std::max<int64_t>(1, nkg / 4),
+                  topz = std::max<int64_t>(1, nkz / 4);
+    auto consider = [&](int64_t sg, int64_t sz) {
+      sg = std::max<int64_t>(1, std::min(sg, topg));
+      sz = std::max<int64_t>(1, std::min(sz, topz));
+      const int64_t ng = tg * sg, nz = tz * sz;  // a piece takes its K-blocks and about 3000 cycles
+      const int64_t lg = (nkg + sg - 1) / sg * perg + 3000, lz = (nkz + sz - 1) / sz * perz + 3000;
+      const int64_t span = ng + nz <= 148 ? std::max(lg, lz)
+                                          : std::max((ng * lg + nz * lz) / 148, lg) + (ng <= 148 ? lz : lg + lz) / 2;
+      const int64_t time = span + (sg + sz) * T * r * 8 / 3500;  // and its sums' way through HBM
+      if (time >= best) return;
       best = time;
       p.g.MH = mh;
       p.g.splits = int(sg);
       p.z.splits = int(sz);
-    }
+    };
+    const int64_t share = std::max<int64_t>(1, 148 * cg / (cg + cz) / tg);
+    consider(share, (148 - std::min<int64_t>(148, tg * share)) / tz);
+    consider((148 - std::min<int64_t>(148, tz)) / tg, 1);
+    for (int64_t sz = 1; sz <= 8; sz *= 2) consider(148 / tg, sz);
   }
   fit_rings(&p.g, A_BF16_K, true, 1);
   fit_rings(&p.z, A_INT8_K, true, 1);
@@ -156,20 +176,21 @@ GradPlan grad_plan(int64_t T, int64_t m, int64_t n, int64_t r) {
   // the pieces up, about 6000 cycles, and the pieces' traffic.
   p.v.MH = 1;
   p.u.BN = p.v.BN = bn;
-  p.x = shape_of(A_BF16_K, n, T, r, false, 2, false);
-  p.u.MH = tiles(m, 2) * kblock_cycles(A_BF16_M, 2, 2, bn) < tiles(m, 1) * kblock_cycles(A_BF16_M, 2, 1, bn) &&
-                   tiles(m, 2) >= 74 && rings_fit(A_BF16_M, true, 2, 2, bn, 2)
+  p.x = shape_of(A_BF16_K, n, T, r, false, Z_TERMS, false);
+  p.u.MH = tiles(m, 2) * kblock_cycles(A_BF16_M, Z_TERMS, 2, bn) <
+                       tiles(m, 1) * kblock_cycles(A_BF16_M, Z_TERMS, 1, bn) &&
+                   tiles(m, 2) >= 74 && rings_fit(A_BF16_M, true, Z_TERMS, 2, bn, 2)
                ? 2
                : 1;
   auto split_t = [&](int ak, int mh, int64_t rows) {
-    const int64_t t = tiles(rows, mh), per = kblock_cycles(ak, 2, mh, bn);
+    const int64_t t = tiles(rows, mh), per = kblock_cycles(ak, Z_TERMS, mh, bn);
     const int64_t s = std::max<int64_t>(1, std::min<int64_t>(74 / t, nkt / 4));
     return (nkt - (nkt + s - 1) / s) * per > 6000 + s * rows * r * 8 / 3500 ? int(s) : 1;
   };
   p.u.splits = split_t(A_BF16_M, p.u.MH, m);
   p.v.splits = split_t(A_INT8_M, 1, n);
-  fit_rings(&p.u, A_BF16_M, true, 2);
-  fit_rings(&p.v, A_INT8_M, true, 2);
+  fit_rings(&p.u, A_BF16_M, true, Z_TERMS);
+  fit_rings(&p.v, A_INT8_M, true, Z_TERMS);
 
   size_t o = 0;
   auto take = [&](int64_t bytes) {
@@ -180,10 +201,9 @@ GradPlan grad_plan(int64_t T, int64_t m, int64_t n, int64_t r) {
   p.off_dy = take(m % 8 ? T * p.mp * 2 : 0);
   p.off_u = take(r % 8 ? m * p.rp * 2 : 0);
   p.off_v = take(r % 8 ? n * p.rp * 2 : 0);
-  p.off_zh = take(T * p.rp * 2);
-  p.off_zl = take(T * p.rp * 2);
-  p.off_gh = take(T * p.rp * 2);
-  p.off_gl = take(T * p.rp * 2);
+  p.zpart = up16(T * p.rp * 2) / 2;
+  p.off_z = take(Z_TERMS * p.zpart * 2);
+  p.off_g = take(Z_TERMS * p.zpart * 2);
   // partial sums of G, then of dU; of Z, then of dV
   p.off_pa = take(std::max(p.g.splits * T * r * 4, p.u.splits > 1 ? p.u.splits * m * r * 4 : 0));
   p.off_pb = take(std::max(p.z.splits * T * r * 4, p.v.splits > 1 ? p.v.splits * n * r * 4 : 0));
@@ -208,8 +228,8 @@ hsl_status launch_second(const GemmMaps& um, const GemmArgs& u, const GemmMaps& 
                          const GemmMaps& xm, const GemmArgs& x, bool with_x, cudaStream_t s) {
   void (*fn)(const GemmMaps, const GemmMaps, const GemmMaps, const GemmArgs, const GemmArgs, const GemmArgs, int,
              int) = k_mx_grad_second<MU, MX>;
-  int bytes = std::max(tile_smem(A_BF16_M, true, 2, MU, false, u), tile_smem(A_INT8_M, true, 2, 1, false, v));
-  if (with_x) bytes = std::max(bytes, tile_smem(A_BF16_K, false, 2, MX, true, x));
+  int bytes = std::max(tile_smem(A_BF16_M, true, Z_TERMS, MU, false, u), tile_smem(A_INT8_M, true, Z_TERMS, 1, false, v));
+  if (with_x) bytes = std::max(bytes, tile_smem(A_BF16_K, false, Z_TERMS, MX, true, x));
   if (cudaError_t e = allow_dyn_smem(reinterpret_cast<const void*>(fn), bytes))
     return cuda_fail(e, "factor gradient smem attribute");
   const int64_t nu = tile_count(MU, u), nv = tile_count(1, v), nx = with_x ? tile_count(MX, x) : 0;
@@ -239,10 +259,8 @@ hsl_status mx_gemm_grad_run(const MxOperand& X, int64_t T, int64_t n, const void
     U = w + p.off_u;
     V = w + p.off_v;
   }
-  __nv_bfloat16* zh = reinterpret_cast<__nv_bfloat16*>(w + p.off_zh);
-  __nv_bfloat16* zl = reinterpret_cast<__nv_bfloat16*>(w + p.off_zl);
-  __nv_bfloat16* gh = reinterpret_cast<__nv_bfloat16*>(w + p.off_gh);
-  __nv_bfloat16* gl = reinterpret_cast<__nv_bfloat16*>(w + p.off_gl);
+  __nv_bfloat16* zp = reinterpret_cast<__nv_bfloat16*>(w + p.off_z);
+  __nv_bfloat16* gp = reinterpret_cast<__nv_bfloat16*>(w + p.off_g);
   float* pa = reinterpret_cast<float*>(w + p.off_pa);
   float* pb = reinterpret_cast<float*>(w + p.off_pb);
 
@@ -258,6 +276,7 @@ hsl_status mx_gemm_grad_run(const MxOperand& X, int64_t T, int64_t n, const void
     g.BN = sh.BN;
     g.stages = sh.stages;
     g.codes = sh.codes;
+    g.terms = sh.terms;
     g.splits = sh.splits;
     return g;
   };
@@ -269,13 +288,14 @@ hsl_status mx_gemm_grad_run(const MxOperand& X, int64_t T, int64_t n, const void
   g.part = pa;
   z.part = pb;
   if (!make_tmap_2d(&m0.a, kBF, 2, dY, T, m, p.mp, 64, 128, kSW) ||
-      !make_tmap_2d(&m0.b0, kBF, 2, U, m, r, p.rp, 64, 64, kSW) ||
-      !make_tmap_2d(&m1.b0, kBF, 2, V, n, r, p.rp, 64, 64, kSW) || !block_maps(&m1, A_INT8_K, 1, X, T))
+      !make_tmap_2d(&m0.b[0], kBF, 2, U, m, r, p.rp, 64, 64, kSW) ||
+      !make_tmap_2d(&m1.b[0], kBF, 2, V, n, r, p.rp, 64, 64, kSW) || !block_maps(&m1, A_INT8_K, 1, X, T))
     return map_failed();
   const bool padded = m % 8 || r % 8;
   if (hsl_status e = p.g.MH == 2 ? launch_first<2>(m0, g, m1, z, padded, s) : launch_first<1>(m0, g, m1, z, padded, s))
     return e;
-  const SumJob sg = {pa, p.g.splits, int(r), int(p.rp), T, gh, gl}, sz = {pb, p.z.splits, int(r), int(p.rp), T, zh, zl};
+  const SumJob sg = {pa, p.g.splits, int(r), int(p.rp), T, p.zpart, gp};
+  const SumJob sz = {pb, p.z.splits, int(r), int(p.rp), T, p.zpart, zp};
   if (hsl_status e = sum_run(sg, sz, r % 8 == 0, s)) return e;
 
   GemmArgs u = args(p.u, m, r, T), v = args(p.v, n, r, T), x = args(p.x, n, T, r);
@@ -288,20 +308,19 @@ hsl_status mx_gemm_grad_run(const MxOperand& X, int64_t T, int64_t n, const void
   result(&v, dV, pb);
   memset(&m0, 0, sizeof(m0));
   memset(&m1, 0, sizeof(m1));
-  if (!make_tmap_2d(&m0.a, kBF, 2, dY, T, m, p.mp, 64, 64, kSW) ||
-      !make_tmap_2d(&m0.b0, kBF, 2, zh, T, r, p.rp, 64, 64, kSW) ||
-      !make_tmap_2d(&m0.b1, kBF, 2, zl, T, r, p.rp, 64, 64, kSW) ||
-      !make_tmap_2d(&m1.b0, kBF, 2, gh, T, r, p.rp, 64, 64, kSW) ||
-      !make_tmap_2d(&m1.b1, kBF, 2, gl, T, r, p.rp, 64, 64, kSW) || !block_maps(&m1, A_INT8_M, 1, X, T))
+  if (!make_tmap_2d(&m0.a, kBF, 2, dY, T, m, p.mp, 64, 64, kSW) || !block_maps(&m1, A_INT8_M, 1, X, T))
     return map_failed();
   if (dX) {  // rows of V are the M side, tokens the N side
     x.add = static_cast<const __nv_bfloat16*>(add);
     x.C = static_cast<__nv_bfloat16*>(dX);
-    if (!make_tmap_2d(&m2.a, kBF, 2, V, n, r, p.rp, 64, 128, kSW) ||
-        !make_tmap_2d(&m2.b0, kBF, 2, gh, T, r, p.rp, 64, p.x.BN, kSW) ||
-        !make_tmap_2d(&m2.b1, kBF, 2, gl, T, r, p.rp, 64, p.x.BN, kSW) || !out_maps(&m2, &x, T, n, p.x.MH))
+    if (!make_tmap_2d(&m2.a, kBF, 2, V, n, r, p.rp, 64, 128, kSW) || !out_maps(&m2, &x, T, n, p.x.MH))
       return map_failed();
   }
+  for (int t = 0; t < Z_TERMS; ++t)
+    if (!make_tmap_2d(&m0.b[t], kBF, 2, zp + t * p.zpart, T, r, p.rp, 64, 64, kSW) ||
+        !make_tmap_2d(&m1.b[t], kBF, 2, gp + t * p.zpart, T, r, p.rp, 64, 64, kSW) ||
+        (dX && !make_tmap_2d(&m2.b[t], kBF, 2, gp + t * p.zpart, T, r, p.rp, 64, p.x.BN, kSW)))
+      return map_failed();
   const bool wx = dX != nullptr;
   hsl_status e;
   if (p.u.MH == 2)
@@ -309,8 +328,8 @@ hsl_status mx_gemm_grad_run(const MxOperand& X, int64_t T, int64_t n, const void
   else
     e = p.x.MH == 2 ? launch_second<1, 2>(m0, u, m1, v, m2, x, wx, s) : launch_second<1, 1>(m0, u, m1, v, m2, x, wx, s);
   if (e) return e;
-  const SumJob su = {pa, p.u.splits, int(r), int(r), p.u.splits > 1 ? m : 0, static_cast<__nv_bfloat16*>(dU), nullptr};
-  const SumJob sv = {pb, p.v.splits, int(r), int(r), p.v.splits > 1 ? n : 0, static_cast<__nv_bfloat16*>(dV), nullptr};
+  const SumJob su = {pa, p.u.splits, int(r), int(r), p.u.splits > 1 ? m : 0, 0, static_cast<__nv_bfloat16*>(dU)};
+  const SumJob sv = {pb, p.v.splits, int(r), int(r), p.v.splits > 1 ? n : 0, 0, static_cast<__nv_bfloat16*>(dV)};
   const bool vec = r % 4 == 0 && reinterpret_cast<uintptr_t>(dU) % 8 == 0 && reinterpret_cast<uintptr_t>(dV) % 8 == 0;
   return sum_run(su, sv, vec, s);
 }
