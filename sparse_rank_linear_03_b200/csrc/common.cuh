@@ -59,6 +59,21 @@ __device__ __forceinline__ uint4 ld_nc16(const void* p) {
                : "l"(p));
   return v;
 }
+// Ordinary loads for what an earlier kernel of the same chain of launches may have written: the read-only loads above
+// are defined only for memory that nobody writes while the kernel is there, and a chained kernel is there
+// before the one ahead of it has ended.  Volatile, so that they stay behind the wait for that kernel.
+__device__ __forceinline__ uint4 ld_chained16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_chained4(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
 __device__ __forceinline__ void st_stream16(void* p, uint4 v) {
   asm volatile("st.global.cs.v4.u32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(v.x), "r"(v.y),
                "r"(v.z), "r"(v.w)

@@ -43,15 +43,15 @@ __device__ __forceinline__ Raw load4(const MxOperand& o, int64_t r, int64_t c, i
   Raw v = {{0, 0, 0, 0}, 0};
   if (c >= cols) return v;
   const int kind = kind_at<KIND>(o);
-  if (kind == MxOperand::kF32) {
+  if (kind == MxOperand::kF32) {  // (Z and G of the factor gradients are the call's own: no read-only loads)
     const uint32_t* p = static_cast<const uint32_t*>(o.p) + r * o.pitch + c;
     if (o.vec && c + 4 <= cols) {
-      const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+      const uint4 q = ld_chained16(p);
       v.w[0] = q.x; v.w[1] = q.y; v.w[2] = q.z; v.w[3] = q.w;
     } else {
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        if (c + q < cols) v.w[q] = __ldg(p + q);
+        if (c + q < cols) v.w[q] = ld_chained4(p + q);
     }
   } else if (kind == MxOperand::kBF16) {
     const uint16_t* p = static_cast<const uint16_t*>(o.p) + r * o.pitch + c;
