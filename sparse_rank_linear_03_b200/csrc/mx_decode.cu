@@ -17,8 +17,12 @@
 //   for two columns per token up to 4 tokens (and not too long ones), and what does not fit
 //   takes another pass over D.  From two tokens on a kernel of its own makes the columns (k_mx_tokens),
 //   while the main kernel's first copies of D are already under way.  At the end each column is scaled back.  Infinities
-//   and NaN go to the first window as they are.  Block scales enter as 2^(e − 142), so
-//   that a column's sums lie as if its largest value were about 1.
+//   and NaN go to the first window as they are.  Block scales enter as 2^(e − 110): a column's smallest product,
+//   2^−25, then keeps its bits at every e.  At the other end sums of blocks with e of about 200 and more
+//   (weights of 2^70) may overflow although the result, for small tokens, does not.  That always shows, as an
+//   infinity or a NaN, and such outputs are summed again at the end, as they are, by the warp that issued the
+//   copies (dc_again).  (A look at each unit's scales with a second loop for such units took 33 µs where this takes
+//   29, and so did the same repair as a call from the sixteen warps.)
 //
 //   One CTA per SM keeps the columns in shared memory and walks over tiles of 16 rows.
 //   Codes and scales come in tiled copies, one of each per stage, a ring of stages ahead of
@@ -62,7 +66,7 @@ __device__ __forceinline__ void widen_word(uint32_t w, uint32_t (&v)[4]) {
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
       : "r"(w));
 }
-// Four scale bytes (one word) → 2^(e − 142) in fp32: the conversion gives 2^(e − 127) as bf16 pairs
+// Four scale bytes (one word) → 2^(e − 110) in fp32 (infinite from e = 238 on): the conversion gives 2^(e − 127) as bf16 pairs
 // (2^−127 a subnormal, 255 a NaN), which widen by shifts.
 __device__ __forceinline__ void widen_scales(uint32_t w, float* s) {
   uint32_t p[2];
@@ -72,7 +76,7 @@ __device__ __forceinline__ void widen_scales(uint32_t w, float* s) {
       "cvt.rn.bf16x2.ue8m0x2 %1, b;\n\t}"
       : "=r"(p[0]), "=r"(p[1])
       : "r"(w));
-  constexpr float k = 1.0f / 32768.0f;
+  constexpr float k = 131072.0f;
   s[0] = bf_lo(p[0]) * k;
   s[1] = bf_hi(p[0]) * k;
   s[2] = bf_lo(p[1]) * k;
@@ -86,14 +90,36 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// 2^k, −126 <= k <= 127.
+__device__ __forceinline__ float pow2(int k) { return __uint_as_float(uint32_t(127 + k) << 23); }
+
+// One output's sum by a warp, straight from the token: every product takes its block's power of two in
+// two factors, so that only what is past fp32 itself overflows.  (Inlined: a call costs the kernel 2 µs.)
+__device__ __forceinline__ float dc_again(const uint8_t* codes, const uint8_t* scales, const __nv_bfloat16* x, int n,
+                                       int nb) {
+  float v = 0.f;
+  for (int b = threadIdx.x & 31; b < nb; b += 32) {
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(codes) + b);
+    const int e = __ldg(scales + b), s = e - 127;
+    const float f0 = e == 255 ? __uint_as_float(0x7FC00000u) : pow2(s >> 1), f1 = pow2((s + 1) >> 1);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    for (int j = 0; j < min(32, n - b * 32); ++j)
+      v = fmaf(__bfloat162float(x[b * 32 + j]) * f0, mx::e2m1_f32((w[j >> 3] >> ((j & 7) * 4)) & 15u) * f1, v);
+  }
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+  return v;
+}
+
 struct DcMaps {
   CUtensorMap c3;  // codes as [unit][row][128 bytes]: box {128, 16·tps, su}
   CUtensorMap c2;  // codes as [row][bytes]: box {128, 16·tps} (stages with the row's ragged end)
   CUtensorMap s;   // scales: box {128, 16·tps}
 };
 struct DcArgs {
-  const int2* tokens;   // per token: largest exponent field, windows
+  const int2* tokens;   // per token: largest exponent field (+ kNotFinite), windows
   const uint4* columns;  // [window][token][cpieces] pieces of eight fp16
+  const uint8_t *codes, *scales;  // for dc_again
+  int64_t pitch, spitch;
   const __nv_bfloat16* X;  // kSelf
   const __nv_bfloat16* add;
   __nv_bfloat16* Y;
@@ -135,8 +161,8 @@ __device__ __forceinline__ uint4 load_piece(const __nv_bfloat16* x, int col, int
   return v;
 }
 // Largest and smallest exponent field of a piece's finite values that are not zero (-1 and 255 if
-// there is none), two values at a time.
-__device__ __forceinline__ void exponents(const uint4& v, int& hi, int& lo) {
+// there is none), two values at a time.  Whether there is an infinity or a NaN.
+__device__ __forceinline__ bool exponents(const uint4& v, int& hi, int& lo) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t h = 0, l = 0xFFFFFFFFu;
 #pragma unroll
@@ -161,6 +187,7 @@ __device__ __forceinline__ void exponents(const uint4& v, int& hi, int& lo) {
     hi = int(top >> 7);
     lo = int((low + 1) >> 7);
   }
+  return top >= 0x7F80u;
 }
 // The values of a piece that belong to window `win` of a token whose largest exponent field is
 // `top`, scaled by 2^(142 − top + 32 win) to fp16; zeros elsewhere.
@@ -189,9 +216,10 @@ __device__ __forceinline__ uint4 window_piece(const uint4& v, int top, int win, 
 }
 
 // A token's largest exponent field and windows.
-__device__ __forceinline__ int2 windows_of(int hi, int lo) {
+constexpr int kNotFinite = 0x100;  // beside the exponent field: there is an infinity or a NaN
+__device__ __forceinline__ int2 windows_of(int hi, int lo, bool odd) {
   if (hi < 0) hi = lo = 127;  // nothing but zeros, infinities and NaN
-  return make_int2(hi, (hi - lo) / 32 + 1);
+  return make_int2(hi + (odd ? kNotFinite : 0), (hi - lo) / 32 + 1);
 }
 
 // A CTA per token: its exponents, then its windows as columns of fp16 (in global memory).
@@ -206,6 +234,7 @@ __global__ void __launch_bounds__(DC_TOKEN_THREADS)
   const __nv_bfloat16* x = X + int64_t(tok) * n;
   uint4 kept[DC_TOKEN_KEEP];
   int hi = -1, lo = 255;
+  bool odd = false;
 #pragma unroll
   for (int k = 0; k < DC_TOKEN_KEEP; ++k) {
     const int c = threadIdx.x + k * DC_TOKEN_THREADS;
@@ -214,13 +243,13 @@ __global__ void __launch_bounds__(DC_TOKEN_THREADS)
 #pragma unroll
   for (int k = 0; k < DC_TOKEN_KEEP; ++k) {
     int h, l;
-    exponents(kept[k], h, l);
+    odd |= exponents(kept[k], h, l);
     hi = max(hi, h);
     lo = min(lo, l);
   }
   for (int c = threadIdx.x + DC_TOKEN_KEEP * DC_TOKEN_THREADS; c < pieces; c += DC_TOKEN_THREADS) {
     int h, l;
-    exponents(load_piece(x, c * 8, n, vec), h, l);
+    odd |= exponents(load_piece(x, c * 8, n, vec), h, l);
     hi = max(hi, h);
     lo = min(lo, l);
   }
@@ -230,14 +259,14 @@ __global__ void __launch_bounds__(DC_TOKEN_THREADS)
     red[0][warp] = hi;
     red[1][warp] = lo;
   }
-  __syncthreads();
+  odd = __syncthreads_or(odd);
 #pragma unroll
   for (int w = 0; w < DC_TOKEN_THREADS / 32; ++w) {
     hi = max(hi, red[0][w]);
     lo = min(lo, red[1][w]);
   }
-  const int2 of = windows_of(hi, lo);
-  hi = of.x;
+  const int2 of = windows_of(hi, lo, odd);
+  hi = of.x & 0xFF;
   const int windows = of.y;
   if (threadIdx.x == 0) tokens[tok] = of;
   for (int w = 0; w < windows; ++w) {
@@ -281,6 +310,8 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   __shared__ int abort_flag;
   __shared__ int2 token[8], range[DC_WARPS];
   __shared__ float unscale[2][8];  // per column: 2^k in two factors
+  __shared__ int odd_token;        // kSelf: there is an infinity or a NaN
+  __shared__ int again;            // some outputs are to be summed again: those marked 1 in ysum
   float* red = reinterpret_cast<float*>(smem);  // [slot][DC_WARPS][columns][DC_RED_PITCH]
   const int pieces = a.slice * (DC_UNIT / 8), cpitch = dc_col_pitch(a.slice);
   uint4* xs = reinterpret_cast<uint4*>(smem + DC_RED);
@@ -295,6 +326,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
 
   if (threadIdx.x == 0) {
     abort_flag = 0;
+    odd_token = again = 0;
     for (int i = 0; i < a.stages; ++i) {
       tc::mbar_init(&full[i], 1);
       tc::mbar_init(&empty[i], DC_WARPS);
@@ -361,6 +393,20 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     if (lane == 0 && *abrt)
       for (int q = 0; q < a.stages && q < issued; ++q)  // copies in flight land first
         tc::mbar_wait(&full[q], uint32_t((issued - 1 - q) / a.stages) & 1, &g_mx_decode_err);
+    // when the sums are done: those to be done again, if any
+    __syncwarp();
+    asm volatile("barrier.sync 2, 544;" ::: "memory");
+    if (!again) return;
+    for (int grp = blockIdx.x, local = 0; grp < groups; grp += gridDim.x, ++local)
+      for (int e = 0; e < kRows * a.T * a.tps; ++e) {
+        const int row = (grp * a.tps + (e >> 4) / a.T) * kRows + (e & 15), tok = (e >> 4) % a.T;
+        if (row >= a.m || ysum[int64_t(local) * a.tps * a.T * kRows + e] != 1.f) continue;
+        float v = dc_again(a.codes + row * a.pitch, a.scales + row * a.spitch, a.X + int64_t(tok) * a.n, a.n, a.nb);
+        const int64_t at = int64_t(tok) * a.m + row;
+        if (a.add) v += __bfloat162float(a.add[at]);
+        __syncwarp();  // (add may be Y)
+        if (lane == 0) a.Y[at] = __float2bfloat16_rn(v);
+      }
     return;
   }
 
@@ -374,23 +420,25 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     if (u0 == 0) {
       if (kSelf) {
         int hi = -1, lo = 255;
+        bool odd = false;
 #pragma unroll 4
         for (int c = threadIdx.x; c < a.cpieces; c += DC_WARPS * 32) {
           int h, l;
-          exponents(load_piece(a.X, c * 8, a.n, a.vec), h, l);
+          odd |= exponents(load_piece(a.X, c * 8, a.n, a.vec), h, l);
           hi = max(hi, h);
           lo = min(lo, l);
         }
         hi = __reduce_max_sync(0xFFFFFFFFu, hi);
         lo = __reduce_min_sync(0xFFFFFFFFu, lo);
         if (lane == 0) range[warp] = make_int2(hi, lo);
+        if (odd) odd_token = 1;
         dc_sync();
         if (threadIdx.x == 0) {
           for (int w = 1; w < DC_WARPS; ++w) {
             hi = max(hi, range[w].x);
             lo = min(lo, range[w].y);
           }
-          token[0] = windows_of(hi, lo);
+          token[0] = windows_of(hi, lo, odd_token != 0);
         }
       } else {
         pdl_wait();  // the columns are written
@@ -411,7 +459,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         for (int c = 0; c < cols && pass * a.wcols + c < windows; ++c) {
 #pragma unroll 4
           for (int e = threadIdx.x; e < have; e += DC_WARPS * 32)
-            xs[c * cpitch + e] = window_piece(load_piece(a.X, (u0 * (DC_UNIT / 8) + e) * 8, a.n, a.vec), token[0].x,
+            xs[c * cpitch + e] = window_piece(load_piece(a.X, (u0 * (DC_UNIT / 8) + e) * 8, a.n, a.vec), token[0].x & 0xFF,
                                               pass * a.wcols + c, windows == 1);
         }
       } else if (threadIdx.x == 0) {
@@ -427,11 +475,12 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       }
       if (threadIdx.x < cols) {
         const int tok = threadIdx.x / per_tok;
-        const int k = token[tok].x - 127 - 32 * (pass * a.wcols + int(threadIdx.x) % per_tok);
+        const int k = (token[tok].x & 0xFF) - 127 - 32 * (pass * a.wcols + int(threadIdx.x) % per_tok);
         // (a column past the token's windows is all zeros: any factor will do)
-        const int k0 = max(k, -252) / 2, k1 = max(k, -252) - k0;
-        unscale[0][threadIdx.x] = __uint_as_float(uint32_t(127 + k0) << 23);
-        unscale[1][threadIdx.x] = __uint_as_float(uint32_t(127 + k1) << 23);
+        // (2^(e − 110) and the columns' 2^15 together are 2^32 more than 2^(e − 127))
+        const int k0 = max(k - 32, -252) / 2, k1 = max(k - 32, -252) - k0;
+        unscale[0][threadIdx.x] = pow2(k0);
+        unscale[1][threadIdx.x] = pow2(k1);
       }
       for (int c = 0; c < cols; ++c)  // windows that a token does not have
         if (pass * a.wcols + c % per_tok >= token[c / per_tok].y)
@@ -537,6 +586,12 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
             *keep = v;
             continue;
           }
+          const bool odd = !(fabsf(v) < INFINITY) && token[tok].x < kNotFinite;
+          *keep = odd ? 1.f : 0.f;
+          if (odd) {
+            again = 1;
+            continue;
+          }
           if (a.add) v += plus;
           a.Y[at] = __float2bfloat16_rn(v);
         }
@@ -545,6 +600,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       }
     }
   }
+  asm volatile("barrier.arrive 2, 544;" ::: "memory");  // the copying warp may look at the marks
 }
 
 // ---- f32 ------------------------------------------------------------------------
@@ -713,6 +769,10 @@ hsl_status mx_decode_run(const MxOperand& D, int64_t m, int64_t n, const void* X
   a.n = int(n);
   a.vec = n % 8 == 0 && reinterpret_cast<uintptr_t>(X) % 16 == 0 ? 1 : 0;
   a.cpieces = int((mx::blocks(n) + 7) / 8) * (DC_UNIT / 8);
+  a.codes = static_cast<const uint8_t*>(D.p);
+  a.scales = D.scales;
+  a.pitch = D.pitch;
+  a.spitch = D.spitch;
   a.add = static_cast<const __nv_bfloat16*>(add);
   a.Y = static_cast<__nv_bfloat16*>(Y);
   a.m = int(m);
