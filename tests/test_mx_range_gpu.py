@@ -7,7 +7,7 @@ import torch
 
 from oracle import mx
 
-from test_mx_gpu import blocks, close, f64, tensor, tokens, weights
+from test_mx_gpu import blocks, chain, close, f64, tensor, tokens, weights
 
 pytestmark = pytest.mark.gpu
 
@@ -96,3 +96,53 @@ def test_apply_the_largest_weights(hsl, T):
     x = tensor(np.full((T, 40), 2.0 ** -100), "bf16")
     want = mx.apply(d, f64(x))
     close(hsl.mx4_apply(D, x), want, want, 40, "bf16")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("T", [1, 3, 40])
+def test_apply_f32(hsl, T, kind):
+    m, n = 130, 1100
+    p = powers(kind, -(-n // 32), m)
+    D, d = blocks(hsl, scaled(weights(m, n, m), p), "e2m1")
+    x = tensor(scaled(tokens(T, n, T), -p), "f32")
+    close(hsl.mx4_apply(D, x), mx.apply(d, f64(x)), mx.apply(np.abs(d), np.abs(f64(x))), n, "f32")
+
+
+@pytest.mark.parametrize("kind", ["high", "low"])
+@pytest.mark.parametrize("T,m,n,dtype", [(1, 48, 320, "bf16"), (33, 1001, 777, "bf16"), (300, 256, 512, "bf16"),
+                                         (3, 100, 96, "f32")])
+def test_apply_t(hsl, T, m, n, kind, dtype):
+    p = powers(kind, -(-n // 32), 0)
+    D, d = blocks(hsl, scaled(weights(m, n, m), p), "e2m1")
+    dy = tensor(scaled(tokens(T, m, T), np.full(-(-m // 32), -p[0])), dtype)
+    close(hsl.mx4_apply_t(D, dy), mx.apply_t(d, f64(dy)), mx.apply_t(np.abs(d), np.abs(f64(dy))), m, dtype)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("T,m,n,dtype", [(1, 48, 320, "bf16"), (33, 1001, 777, "f32"), (300, 256, 2048, "bf16"),
+                                         (300, 257, 520, "f32")])
+def test_matmul(hsl, T, m, n, kind, dtype):
+    p = powers(kind, -(-n // 32), T)
+    B, b = blocks(hsl, scaled(weights(m, n, m), p), "e2m1")
+    A, a = blocks(hsl, scaled(tokens(T, n, T), -p), "e2m1")
+    close(hsl.mx4_matmul(A, B, dtype=dtype), mx.apply(b, a), mx.apply(np.abs(b), np.abs(a)), n, dtype)
+
+
+@pytest.mark.parametrize("kind", ["high", "low", "mixed"])
+@pytest.mark.parametrize("T,m,n,r", [(1, 40, 64, 8), (77, 300, 777, 100), (300, 256, 512, 64)])
+def test_factor_grad(hsl, T, m, n, r, kind):
+    """X at one end, V and dY U at the other, so that Z, G, dU and dV are all far from it (`mixed`: dV goes with
+    the blocks of X).  dX = G V^T leaves the range here."""
+    p = powers(kind, -(-n // 32), T)
+    X, x = blocks(hsl, scaled(tokens(T, n, T), p), "int8")
+    rng = np.random.default_rng(r)
+    back = -np.repeat(p, 32)[:n, None] * 100 // 126
+    V = tensor(np.ldexp(rng.standard_normal((n, r)), back), "bf16")
+    s = 0 if kind == "mixed" else int(back[0, 0]) // 2
+    dY, U = (tensor(np.ldexp(rng.standard_normal(sh), s), "bf16") for sh in ((T, m), (m, r)))
+    y, u, v = f64(dY), f64(U), f64(V)
+    a = np.abs
+    dU, dV = hsl.mx8_factor_grad(X, dY, U, V)
+    wU, wV, _ = mx.factor_grad(x, y, u, v)
+    close(dU, wU, a(y).T @ a(x @ v), T, "bf16", a(y).T @ (chain(n) * (a(x) @ a(v))) * 1.01)
+    close(dV, wV, a(x).T @ a(y @ u), T, "bf16", a(x).T @ (chain(m) * (a(y) @ a(u))) * 1.01)
