@@ -63,3 +63,23 @@ def test_bf16_factor_gradients_off_sixteen_bytes(hsl):
                                       ("apply_t", 7, 1001, 777)])
 def test_f32_products_in_ranges(hsl, op, T, m, n):
     repeat(hsl, op, "f32", T, m, n, 0)
+
+
+@pytest.mark.parametrize("op,T,m,n", [
+    ("apply", 1, 4096, 11008), ("apply", 2, 28672, 8192), ("apply", 8, 28672, 8192),   # columns, then the product
+    ("apply", 8, 333, 28672), ("apply", 33, 1001, 777), ("apply_t", 33, 1001, 777),    # padded rows, K ranges, sum
+    ("apply", 300, 11008, 4095), ("apply_t", 300, 4095, 11008)])
+def test_bf16_products_handed_on(hsl, op, T, m, n):
+    repeat(hsl, op, "bf16", T, m, n, 0)
+
+
+@pytest.mark.parametrize("T,m,n,r", [(500, 4097, 4096, 100), (300, 1001, 777, 17), (2048, 4100, 1030, 256), (1, 4099, 513, 8)])
+def test_bf16_factor_gradients_of_odd_sizes(hsl, T, m, n, r):
+    """Up to three paddings, Z and G with their sum, three products with theirs."""
+    repeat(hsl, "factor_grad", "bf16", T, m, n, r)
+
+
+@pytest.mark.parametrize("T,m,n,dtype", [(300, 4097, 2048, "bf16"), (513, 11007, 4100, "bf16"), (300, 4096, 2048, "f32"),
+                                         (40, 4096, 8192, "bf16"), (200, 1001, 777, "f32")])
+def test_matmul_of_odd_rows(hsl, T, m, n, dtype):
+    repeat(hsl, "matmul", dtype, T, m, n, 0)
