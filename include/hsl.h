@@ -401,7 +401,9 @@ hsl_status hsl_mx8_factor_grad(const hsl_mx* X, const void* dY, int64_t m, const
 
 /* Synchronise s and return, then clear, the device-side error of the microscaled
  * operators on the current device: HSL_ERR_TIMEOUT if a bounded device wait of
- * any of them gave up (its output is then incomplete), HSL_OK if none did.
+ * any of them gave up (its output is then incomplete), HSL_OK if none did.  The
+ * calls have no handle, so that the error is the device's: the first check after
+ * it has it, on whatever stream or thread.  No report is lost.
  * [HSS] §Risks and mitigations, risk 1, as hsl_check. */
 hsl_status hsl_mx_check(hsl_stream s);
 

@@ -70,8 +70,8 @@ cudaError_t prefer_carveout(const void* func, int percent) {
 }
 
 // HSL_FAULT_INJECT=alloc makes every device allocation fail; =zwait makes the
-// batch-1 2:4 decode's wait for z give up (host-side failure testing; no
-// device fault is involved).
+// batch-1 2:4 decode's wait for z give up; =mxwait makes hsl_mx_check find what
+// such a wait leaves (host-side failure testing; no device fault is involved).
 bool fault_injected(const char* what) {
   const char* v = std::getenv("HSL_FAULT_INJECT");
   return v && std::strcmp(v, what) == 0;

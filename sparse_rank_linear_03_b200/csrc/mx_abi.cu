@@ -2,6 +2,7 @@
 // workspace layout and the choice of kernel.  Nothing is kept between calls: all
 // data, the workspace included, is the caller's.
 #include <algorithm>
+#include <atomic>
 #include <cstdio>
 #include <initializer_list>
 
@@ -133,6 +134,19 @@ hsl_status check_workspace(const void* ws, size_t have, size_t need) {
   }
   if (!aligned16(ws)) return bad_arg("workspace must be 16-byte aligned");
   return HSL_OK;
+}
+
+// The error words of the kernels' files, read and cleared in one step each, so that no report falls between the two.
+struct ErrorWords {
+  uint32_t* p[4];
+};
+constexpr unsigned kTakeSlots = 64;  // checks under way at a time
+__device__ uint32_t g_mx_taken[kTakeSlots];
+__global__ void k_mx_take(const ErrorWords w, uint32_t* out, bool inject) {
+  if (inject) set_error(w.p[0], kErrTimeout);
+  uint32_t all = 0;
+  for (uint32_t* p : w.p) all |= atomicExch(p, 0u);
+  *out = all;
 }
 
 }  // namespace
@@ -298,20 +312,23 @@ hsl_status hsl_mx8_factor_grad(const hsl_mx* X, const void* dY, int64_t m, const
 hsl_status hsl_mx_check(hsl_stream stream) {
   set_message("");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaError_t e = cudaStreamSynchronize(s)) return cuda_fail(e, "stream synchronize");
-  uint32_t* words[4] = {};
-  if (cudaError_t e = mx_gemm_error_word(&words[0])) return cuda_fail(e, "error word address");
-  if (cudaError_t e = mx_matmul_error_word(&words[1])) return cuda_fail(e, "error word address");
-  if (cudaError_t e = mx_decode_error_word(&words[2])) return cuda_fail(e, "error word address");
-  if (cudaError_t e = mx_grad_error_word(&words[3])) return cuda_fail(e, "error word address");
+  ErrorWords w = {};
+  uint32_t* taken = nullptr;
+  if (cudaError_t e = mx_gemm_error_word(&w.p[0])) return cuda_fail(e, "error word address");
+  if (cudaError_t e = mx_matmul_error_word(&w.p[1])) return cuda_fail(e, "error word address");
+  if (cudaError_t e = mx_decode_error_word(&w.p[2])) return cuda_fail(e, "error word address");
+  if (cudaError_t e = mx_grad_error_word(&w.p[3])) return cuda_fail(e, "error word address");
+  if (cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void**>(&taken), g_mx_taken))
+    return cuda_fail(e, "error word address");
+  static std::atomic<unsigned> next{0};
+  taken += next++ % kTakeSlots;
+  // HSL_FAULT_INJECT=mxwait: as if a wait had given up (host-side failure testing)
+  note_launch();
+  k_mx_take<<<1, 1, 0, s>>>(w, taken, fault_injected("mxwait"));
+  if (cudaError_t e = cudaGetLastError()) return cuda_fail(e, "error check launch");
   uint32_t all = 0;
-  for (uint32_t* p : words) {
-    uint32_t v = 0;
-    if (cudaError_t e = cudaMemcpy(&v, p, 4, cudaMemcpyDeviceToHost)) return cuda_fail(e, "error word read");
-    if (v == 0) continue;
-    all |= v;
-    if (cudaError_t e = cudaMemset(p, 0, 4)) return cuda_fail(e, "error word clear");
-  }
+  if (cudaError_t e = cudaMemcpyAsync(&all, taken, 4, cudaMemcpyDeviceToHost, s)) return cuda_fail(e, "error word read");
+  if (cudaError_t e = cudaStreamSynchronize(s)) return cuda_fail(e, "stream synchronize");
   if (all == 0) return HSL_OK;
   set_message("a bounded device wait gave up");
   return HSL_ERR_TIMEOUT;

@@ -622,6 +622,6 @@ def mx8_factor_grad(X: MX, dY: torch.Tensor, U: torch.Tensor, V: torch.Tensor, d
 
 def mx_check(device=None, stream=None) -> None:
     """Synchronise the stream and raise if a device wait of the microscaled operators gave up
-    on the device (hsl_mx_check)."""
+    on the device, on whatever stream, since the last check (hsl_mx_check)."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     _ok(_mx_call(dev, stream, lib.hsl_mx_check), "hsl_mx_check")
