@@ -321,8 +321,9 @@ hsl_status hsl_set_permutation(hsl_handle h, const int32_t* row_order, const int
  * the sizes of a call (16-byte aligned; contents need not survive the call, and
  * calls that may overlap need one each).  The device of the pointers and the
  * stream must be current.  All are asynchronous on s, allocate nothing and can
- * be captured.  Outputs and scratch may not overlap each other or an input (but
- * `add` may be the output itself).  Rows, columns and batches are at most 2^30. */
+ * be captured.  X, Y and the other plain matrices start on a whole element.
+ * Outputs and scratch may not overlap each other or an input (but `add` may be
+ * the output itself).  Rows, columns and batches are at most 2^30. */
 typedef enum { HSL_MX_E2M1 = 0, HSL_MX_INT8 = 1 } hsl_mx_elem;
 typedef struct {
   const void* codes;
@@ -353,7 +354,7 @@ hsl_status hsl_mx_workspace(hsl_mx_op op, int64_t batch, int64_t m, int64_t n, i
  *   s = 2^(floor(log2 max|x|) − emax), emax = 2 (e2m1) or 0 (int8), exponent
  *       clamped to −127..127;   q = x/s rounded to nearest even, saturating.
  * Every code is determined by this (division by s is exact).  A block of zeros
- * gets e = 0 and zero codes; a block with a NaN or an infinity e = 255 and zero
+ * gets e = 0 and codes that stand for 0 (in e2m1 −0 keeps its sign bit); a block with a NaN or an infinity e = 255 and zero
  * codes.  rows = 0 is a no-op.
  * [SQZ] §2–4 (the low-bit dense part); the rule is that of the OCP
  * specification, §6.3. */

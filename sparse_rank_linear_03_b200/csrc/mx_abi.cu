@@ -70,6 +70,12 @@ Span codes_of(const hsl_mx* q) {
 }
 Span scales_of(const hsl_mx* q) { return {q->scales, q->rows * mx::scale_pitch(q->cols)}; }
 int64_t size_of(hsl_dtype d) { return d == HSL_F32 ? 4 : 2; }
+// Matrices start on a whole element (the kernels load elements at least).
+hsl_status check_whole(std::initializer_list<const void*> ps, hsl_dtype d) {
+  for (const void* p : ps)
+    if (reinterpret_cast<uintptr_t>(p) % size_of(d)) return bad_arg("a matrix does not start on a whole element");
+  return HSL_OK;
+}
 // add may be the output itself
 Span add_of(const void* add, const void* out, int64_t bytes) { return {add == out ? nullptr : add, bytes}; }
 
@@ -174,6 +180,7 @@ hsl_status hsl_mx_quantize(const void* X, hsl_dtype dtype, int64_t rows, int64_t
   if (hsl_status e = check_mx(&q, -1, "the result")) return e;
   if (rows == 0) return HSL_OK;
   if (!X) return bad_arg("X is NULL");
+  if (hsl_status e = check_whole({X}, dtype)) return e;
   if (hsl_status e = check_apart({codes_of(&q), scales_of(&q)}, {{X, rows * cols * size_of(dtype)}})) return e;
   return mx_quantize_run(X, dtype, rows, cols, elem == HSL_MX_INT8, codes, scales,
                          static_cast<cudaStream_t>(s));
@@ -185,6 +192,7 @@ hsl_status hsl_mx_dequantize(const hsl_mx* q, void* X, hsl_dtype dtype, hsl_stre
   if (hsl_status e = check_mx(q, -1, "the matrix")) return e;
   if (q->rows == 0) return HSL_OK;
   if (!X) return bad_arg("X is NULL");
+  if (hsl_status e = check_whole({X}, dtype)) return e;
   if (hsl_status e = check_apart({{X, q->rows * q->cols * size_of(dtype)}}, {codes_of(q), scales_of(q)})) return e;
   return mx_dequantize_run(q->codes, q->scales, q->rows, q->cols, q->elem == HSL_MX_INT8, X, dtype,
                            static_cast<cudaStream_t>(s));
@@ -210,6 +218,7 @@ hsl_status hsl_mx4_apply(const hsl_mx* D, const void* X, const void* add, void* 
   if (batch < 0 || batch > kMaxSize) return bad_arg("batch out of range");
   if (batch == 0 || D->rows == 0) return HSL_OK;
   if (!X || !Y) return bad_arg("X/Y is NULL");
+  if (hsl_status e = check_whole({X, add, Y}, dtype)) return e;
   const size_t need = workspace_bytes(HSL_MX_OP_APPLY, batch, D->rows, D->cols, 0, dtype);
   if (hsl_status e = check_workspace(ws, ws_bytes, need)) return e;
   const int64_t xb = batch * D->cols * size_of(dtype), yb = batch * D->rows * size_of(dtype);
@@ -235,6 +244,7 @@ hsl_status hsl_mx4_apply_t(const hsl_mx* D, const void* dY, const void* add, voi
   if (batch < 0 || batch > kMaxSize) return bad_arg("batch out of range");
   if (batch == 0) return HSL_OK;
   if (!dX || (D->rows > 0 && !dY)) return bad_arg("dY/dX is NULL");
+  if (hsl_status e = check_whole({dY, add, dX}, dtype)) return e;
   const size_t need = workspace_bytes(HSL_MX_OP_APPLY_T, batch, D->rows, D->cols, 0, dtype);
   if (hsl_status e = check_workspace(ws, ws_bytes, need)) return e;
   const int64_t xb = batch * D->cols * size_of(dtype), yb = batch * D->rows * size_of(dtype);
@@ -257,6 +267,7 @@ hsl_status hsl_mx4_matmul(const hsl_mx* A, const hsl_mx* B, const void* add, voi
   if (A->cols != B->cols) return bad_arg("A and B must have the same number of columns");
   if (A->rows == 0 || B->rows == 0) return HSL_OK;
   if (!Y) return bad_arg("Y is NULL");
+  if (hsl_status e = check_whole({add, Y}, dtype)) return e;
   const size_t need = workspace_bytes(HSL_MX_OP_MATMUL, A->rows, B->rows, A->cols, 0, dtype);
   if (hsl_status e = check_workspace(ws, ws_bytes, need)) return e;
   const int64_t yb = A->rows * B->rows * size_of(dtype);
@@ -281,6 +292,7 @@ hsl_status hsl_mx8_factor_grad(const hsl_mx* X, const void* dY, int64_t m, const
   if (add && !dX) return bad_arg("add without dX");
   const int64_t T = X->rows, n = X->cols;
   if (T > 0 && !dY) return bad_arg("dY is NULL");
+  if (hsl_status e = check_whole({dY, U, V, add, dU, dV, dX}, dtype)) return e;
   const size_t need = workspace_bytes(HSL_MX_OP_FACTOR_GRAD, T, m, n, r, dtype);
   if (hsl_status e = check_workspace(ws, ws_bytes, need)) return e;
   const int64_t eb = size_of(dtype), ub = m * r * eb, vb = n * r * eb, xb = T * n * eb;
