@@ -53,7 +53,6 @@ __device__ uint32_t g_mx_gemm_err;
 constexpr int G_BK = 64;
 constexpr int G_THREADS = 608;   // 19 warps: copies, MMA, 2 × 8 widening (all 16 in the epilogue), code copies
 constexpr int G_MAX_STAGES = 8;
-constexpr int G_MAX_TERMS = 12;
 constexpr int G_SMEM_BUDGET = 224 * 1024;  // stages and code tiles; barriers and alignment take 2 KB more
 
 enum AKind { A_BF16_K, A_BF16_M, A_E2M1_K, A_E2M1_M, A_INT8_K, A_INT8_M };
@@ -78,7 +77,6 @@ struct GemmArgs {
   int M, N, nk;      // nk: K-blocks of 64
   int BN, stages, splits;
   int codes;         // code tiles in flight
-  int terms;         // tiles of B in flight, where B has several terms
   int cstore;        // OUT_T: tiled store possible
   int addt;          // OUT_T: add comes as a tile as well
   const __nv_bfloat16* add;
@@ -244,35 +242,30 @@ unsigned blocks_of(int64_t count) { return unsigned((count + 255) / 256); }
 
 // ---- host ---------------------------------------------------------------------
 struct GemmShape {
-  int BN, MH, splits, stages, codes, terms;
+  int BN, MH, splits, stages, codes;
 };
 
 int code_bytes(int ak, int mh) {
   if (!a_is_blocks(ak)) return 0;
   return 128 * mh * (a_is_int8(ak) ? 64 : 32) + (a_is_mmajor(ak) ? 1024 : 0);
 }
-int a_bytes(int mh) { return mh * 16384; }
-int b_bytes(bool bmn, int bn) { return bmn ? (bn + 63) / 64 * 8192 : bn * 128; }
-
-// Whether a shape has room for so many stages; with several terms, for all of their tiles but those that the
-// last of these stages needs behind its first.
-bool rings_fit(int ak, bool bmn, int terms, int mh, int bn, int stages) {
-  const int tiles = terms > 1 ? terms * (stages - 1) + 1 : stages;
-  return tiles <= G_MAX_TERMS && stages * a_bytes(mh) + tiles * b_bytes(bmn, bn) +
-                                         (a_is_blocks(ak) ? 4 : 0) * code_bytes(ak, mh) <=
-                                     G_SMEM_BUDGET;
+int stage_bytes(bool bmn, int terms, int mh, int bn) {
+  return mh * 16384 + terms * (bmn ? (bn + 63) / 64 * 8192 : bn * 128);
 }
-// Stages, code tiles and tiles of B's terms of a tile shape.  Code tiles are small and come from farther away
-// than anything else: four of them in flight at least, then as many stages as fit (two at least), then more code
+
+// Stages and code tiles of a tile shape.  Code tiles are small and come from farther away than
+// anything else: four of them in flight at least, then as many stages as fit (two at
+// least: three terms leave room for them only with narrow tiles), then more code
 // tiles, an even number.
 void fit_rings(GemmShape* s, int ak, bool bmn, int terms) {
-  const int code = code_bytes(ak, s->MH), b = b_bytes(bmn, s->BN);
-  s->stages = 2;
-  while (s->stages < G_MAX_STAGES && rings_fit(ak, bmn, terms, s->MH, s->BN, s->stages + 1)) ++s->stages;
-  int left = G_SMEM_BUDGET - s->stages * a_bytes(s->MH) - (code ? 4 : 0) * code;
-  s->terms = terms > 1 ? std::min({terms * s->stages, left / b, G_MAX_TERMS}) : 0;
-  left -= (terms > 1 ? s->terms : s->stages) * b;
-  s->codes = code ? std::min(G_MAX_STAGES, 4 + left / code) & ~1 : 0;
+  const int code = code_bytes(ak, s->MH), stage = stage_bytes(bmn, terms, s->MH, s->BN);
+  s->codes = code ? 4 : 0;
+  s->stages = std::min(G_MAX_STAGES, (G_SMEM_BUDGET - s->codes * code) / stage);
+  if (code) s->codes = std::min(G_MAX_STAGES, (G_SMEM_BUDGET - s->stages * stage) / code) & ~1;
+}
+bool rings_fit(int ak, bool bmn, int terms, int mh, int bn, int stages) {
+  return stages * stage_bytes(bmn, terms, mh, bn) + (a_is_blocks(ak) ? 4 : 0) * code_bytes(ak, mh) <=
+         G_SMEM_BUDGET;
 }
 // Cycles of a K-block as measured: widening 256 rows 1040, 128 rows 720 (its chain of waits does not
 // shrink with the rows); copies and MMAs 5 per column and accumulator pair, 3 for one; with few
@@ -297,6 +290,7 @@ GemmShape shape_of(int ak, int64_t M, int64_t N, int64_t K, bool bmn, int terms,
     int64_t best = INT64_MAX, at = ntn;
     for (int64_t c = ntn; c <= 2 * ntn; ++c) {
       const int64_t bn = round_up((N + c - 1) / c, 16);
+      if (!rings_fit(ak, bmn, terms, 2, int(bn), 2)) continue;  // (128 columns always do)
       const int64_t cost = (t2 * c + 147) / 148 * std::max<int64_t>(bn, 160) *
                            (rings_fit(ak, bmn, terms, 2, int(bn), 3) ? 4 : 5);
       if (cost < best) {
@@ -329,8 +323,7 @@ GemmShape shape_of(int ak, int64_t M, int64_t N, int64_t K, bool bmn, int terms,
 }
 
 int tile_smem(int ak, bool bmn, int terms, int mh, bool staged, const GemmArgs& g) {
-  int bytes = g.stages * a_bytes(mh) + (terms > 1 ? g.terms : g.stages) * b_bytes(bmn, g.BN) +
-              g.codes * code_bytes(ak, mh);
+  int bytes = g.stages * stage_bytes(bmn, terms, mh, g.BN) + g.codes * code_bytes(ak, mh);
   if (staged) bytes = std::max(bytes, mh * 128 * g.BN * 2);  // the epilogue's tile
   return bytes + 1024;
 }

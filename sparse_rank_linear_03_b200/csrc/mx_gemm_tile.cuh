@@ -9,10 +9,6 @@
   unsigned char* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ uint64_t full[G_MAX_STAGES], empty[G_MAX_STAGES], accf[2], drained[2], quiet, addf;
   __shared__ uint64_t raw[G_MAX_STAGES], taken[G_MAX_STAGES];  // code tile landed, read
-  // One term of B comes with its stage.  Several have a ring of their own, a tile of one term each, so that
-  // what is in flight need not be whole K-blocks.
-  constexpr bool kTerms = TERMS > 1;
-  __shared__ uint64_t tfull[kTerms ? G_MAX_TERMS : 1], tempty[kTerms ? G_MAX_TERMS : 1];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
 
@@ -26,9 +22,8 @@
   const int bgroups = (g.BN + 63) / 64;
   const int kB = BMN ? bgroups * 8192 : g.BN * 128;
   using Code = CodeTile<AK, MH>;
-  const int kStage = kA + (kTerms ? 0 : kB);
-  unsigned char* tring = smem + g.stages * kStage;
-  unsigned char* cring = tring + (kTerms ? g.terms * kB : 0);
+  const int kStage = kA + TERMS * kB;
+  unsigned char* cring = smem + g.stages * kStage;
   // The tensor unit cuts every sum off towards zero.  Over the hundreds of inexact terms of a gradient that
   // adds up to 2^−16 of the result (28672 × 8192, 4096 tokens), so there a chain of kChunk K-blocks goes to one of
   // two accumulators in turn, and the sixteen warps add the other to fp32 sums in registers, rounded to nearest.
@@ -44,15 +39,9 @@
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int s = 0; s < g.stages; ++s) {
-      // copies, and the eight widening warps
-      tc::mbar_init(&full[s], a_is_blocks(AK) ? (kTerms ? 0 : 1) + 8 : 1);
+      tc::mbar_init(&full[s], a_is_blocks(AK) ? 1 + 8 : 1);  // copies, and the eight widening warps
       tc::mbar_init(&empty[s], 1);
     }
-    if (kTerms)
-      for (int s = 0; s < g.terms; ++s) {
-        tc::mbar_init(&tfull[s], 1);
-        tc::mbar_init(&tempty[s], 1);
-      }
     for (int s = 0; s < g.codes; ++s) {
       tc::mbar_init(&raw[s], 1);
       tc::mbar_init(&taken[s], 8);
@@ -82,60 +71,42 @@
   if (warp == 0) {
     if (lane == 0) {
       if (OUT == OUT_T && g.addt) tc::tma_prefetch_2d(&maps.add, i0, j0);  // into L2 for the epilogue
-      int s = 0, issued = 0, ts = 0, tissued = 0;
-      uint32_t ph = 1, tph = 1;
-      auto copy_b = [&](unsigned char* b, int t, int k0, uint64_t* bar) {
-        if (BMN) {
-          for (int q = 0; q < bgroups; ++q) tc::tma_load_2d(b + q * 8192, &maps.b[t], j0 + q * 64, k0, bar);
-        } else {
-          tc::tma_load_2d(b, &maps.b[t], k0, j0, bar);
-        }
-      };
-      constexpr bool kCopies = !a_is_blocks(AK) || !kTerms;  // something here belongs to a stage
+      int s = 0, issued = 0;
+      uint32_t ph = 1;
       for (int kb = 0; kb < nk; ++kb) {
+        if (!g_wait(&empty[s], ph, abrt)) break;
+        unsigned char* a = smem + s * kStage;
+        unsigned char* b = a + kA;
         const int k0 = (kb0 + kb) * G_BK;
-        if (kCopies) {
-          if (!g_wait(&empty[s], ph, abrt)) break;
-          unsigned char* a = smem + s * kStage;
-          tc::mbar_expect_tx(&full[s], (a_is_blocks(AK) ? 0 : kA) + (kTerms ? 0 : kB));
-          if (AK == A_BF16_K) {
+        tc::mbar_expect_tx(&full[s], (a_is_blocks(AK) ? 0 : kA) + TERMS * kB);
+        if (AK == A_BF16_K) {
 #pragma unroll
-            for (int h = 0; h < MH; ++h)
-              tc::tma_load_2d(a + h * 16384, &maps.a, k0, i0 + h * 128, &full[s]);
-          } else if (AK == A_BF16_M) {
+          for (int h = 0; h < MH; ++h)
+            tc::tma_load_2d(a + h * 16384, &maps.a, k0, i0 + h * 128, &full[s]);
+        } else if (AK == A_BF16_M) {
 #pragma unroll
-            for (int h = 0; h < 2 * MH; ++h)
-              tc::tma_load_2d(a + h * 8192, &maps.a, i0 + h * 64, k0, &full[s]);
-          }
-          if (!kTerms) copy_b(a + kA, 0, k0, &full[s]);
-          ++issued;
-          if (++s == g.stages) {
-            s = 0;
-            ph ^= 1;
+          for (int h = 0; h < 2 * MH; ++h)
+            tc::tma_load_2d(a + h * 8192, &maps.a, i0 + h * 64, k0, &full[s]);
+        }
+#pragma unroll
+        for (int t = 0; t < TERMS; ++t) {
+          if (BMN) {
+            for (int q = 0; q < bgroups; ++q)
+              tc::tma_load_2d(b + t * kB + q * 8192, &maps.b[t], j0 + q * 64, k0, &full[s]);
+          } else {
+            tc::tma_load_2d(b + t * kB, &maps.b[t], k0, j0, &full[s]);
           }
         }
-        if (kTerms) {
-          bool live = true;
-#pragma unroll
-          for (int t = 0; t < TERMS; ++t) {
-            if (!live || !(live = g_wait(&tempty[ts], tph, abrt))) break;
-            tc::mbar_expect_tx(&tfull[ts], kB);
-            copy_b(tring + ts * kB, t, k0, &tfull[ts]);
-            ++tissued;
-            if (++ts == g.terms) {
-              ts = 0;
-              tph ^= 1;
-            }
-          }
-          if (!live) break;
+        ++issued;
+        if (++s == g.stages) {
+          s = 0;
+          ph ^= 1;
         }
       }
       // the copies in flight have landed before the CTA's shared memory is given up
-      if (*abrt) {
-        for (int q = 0; q < g.stages && q < issued; ++q)  // (uses of stage q before its last one)
-          tc::mbar_wait(&full[q], uint32_t((issued - 1 - q) / g.stages) & 1, &g_mx_gemm_err);
-        for (int q = 0; kTerms && q < g.terms && q < tissued; ++q)
-          tc::mbar_wait(&tfull[q], uint32_t((tissued - 1 - q) / g.terms) & 1, &g_mx_gemm_err);
+      for (int q = 0; q < g.stages && q < issued; ++q) {
+        const int last = (issued - 1 - q) / g.stages;  // uses of stage q before its last one
+        if (*abrt) tc::mbar_wait(&full[q], uint32_t(last) & 1, &g_mx_gemm_err);
       }
     }
     __syncwarp();
@@ -175,9 +146,8 @@
     if (tc::elect_one()) {
       const uint32_t idesc = tc::idesc_bf16(128, g.BN) | (a_is_mmajor(AK) ? 1u << 15 : 0u) |
                              (BMN ? 1u << 16 : 0u);
-      int s = 0, ts = 0;
-      uint32_t ph = 0, tph = 0;
-      bool live = true;
+      int s = 0;
+      uint32_t ph = 0;
       for (int kb = 0; kb < nk; ++kb) {
         const int chunk = kFold ? kb / kChunk : 0;
         const bool first = kFold ? kb % kChunk == 0 : kb == 0;
@@ -188,12 +158,7 @@
         const uint32_t acc = tmem + uint32_t((chunk & 1) * aset);
 #pragma unroll
         for (int t = 0; t < TERMS; ++t) {
-          if (kTerms) {
-            if (!live || !(live = g_wait(&tfull[ts], tph, abrt))) break;
-            tc::tc_fence_after();
-          }
-          unsigned char* b = kTerms ? tring + ts * kB : a + kA;
-          const uint64_t bd = BMN ? desc_mn_sw128(b) : tc::desc_sw128(b);
+          const uint64_t bd = BMN ? desc_mn_sw128(a + kA + t * kB) : tc::desc_sw128(a + kA + t * kB);
 #pragma unroll
           for (int h = 0; h < MH; ++h) {
             const uint64_t ad =
@@ -204,15 +169,7 @@
                            tc::desc_advance(bd, k * (BMN ? 2048 : 32)), idesc,
                            (!first || k > 0 || t > 0) ? 1u : 0u);
           }
-          if (kTerms) {
-            tc::mma_commit(&tempty[ts]);
-            if (++ts == g.terms) {
-              ts = 0;
-              tph ^= 1;
-            }
-          }
         }
-        if (!live) break;
         tc::mma_commit(&empty[s]);
         if (kFold && (kb % kChunk == kChunk - 1 || kb == nk - 1)) tc::mma_commit(&accf[chunk & 1]);
         if (++s == g.stages) {

@@ -7,10 +7,10 @@
 // them have fewer tiles than SMs or leave a last round half empty.  Z and G are fp32 sums over their
 // splits and stay so: three bf16 parts, which the second products take as three terms.  Sums over tokens, features
 // and columns leave the tensor unit every 8 to 24 of its steps (kFold in mx_gemm_tile.cuh); that and the three
-// parts bring the results from 2^−16 of their size to the error of fp32 sums.  28672 × 8192, rank 256, 4096
-// tokens: 431 µs, of which the second launch takes 270 (301 µs with two parts and sums that stay in the tensor
-// unit: tiles of 256 columns instead of 128 then have room); 4096 × 4096, rank 128, 500 tokens: 30.2 (26.0) µs.
-// What bounds the second launch: 80 KB from L2 per 256 × 128 × 64 step of three terms, 7 TB/s in all.
+// parts bring the results from 2^−16 of their size to the error of fp32 sums.  What they cost, against two parts
+// and sums that stay in the tensor unit: 28672 × 8192, rank 256, 4096 tokens 382 µs (269), where tiles
+// become 128 columns instead of 256 and the second launch brings 80 KB from L2 per 256 × 128 × 64 step, 7 TB/s in
+// all; 8192 × 8192, rank 128, 4096 tokens 154 (136); 4096 × 4096, rank 128, 500 tokens 28.7 (26.7) µs.
 #include "mx_gemm.cuh"
 
 namespace hsl {
@@ -138,6 +138,11 @@ GradPlan grad_plan(int64_t T, int64_t m, int64_t n, int64_t r) {
   auto tiles = [&](int64_t rows, int mh) { return (rows + 128 * mh - 1) / (128 * mh) * ntn; };
   const int64_t nkg = (m + 63) / 64, nkz = (n + 63) / 64, nkt = (T + 63) / 64;
 
+  // Cycles of a launch with na pieces of la cycles and behind them nb of lb.
+  auto span = [](int64_t na, int64_t la, int64_t nb, int64_t lb) {
+    if (na + nb <= 148) return std::max(la, lb);
+    return std::max((na * la + nb * lb) / 148, la) + (na <= 148 ? lb : la + lb) / 2;
+  };
   // First launch: pieces of G, at least 4 K-blocks each, in one round of CTAs, and pieces of Z beside and behind
   // them: shares of the SMs by work, or a whole round of G with Z in smaller pieces that take the SMs as
   // they come free, whichever is done earlier (28672 × 8192, rank 256, 4096 tokens: 64 CTAs of G and 64 of Z
@@ -155,9 +160,7 @@ GradPlan grad_plan(int64_t T, int64_t m, int64_t n, int64_t r) {
       sz = std::max<int64_t>(1, std::min(sz, topz));
       const int64_t ng = tg * sg, nz = tz * sz;  // a piece takes its K-blocks and about 3000 cycles
       const int64_t lg = (nkg + sg - 1) / sg * perg + 3000, lz = (nkz + sz - 1) / sz * perz + 3000;
-      const int64_t span = ng + nz <= 148 ? std::max(lg, lz)
-                                          : std::max((ng * lg + nz * lz) / 148, lg) + (ng <= 148 ? lz : lg + lz) / 2;
-      const int64_t time = span + (sg + sz) * T * r * 8 / 3500;  // and its sums' way through HBM
+      const int64_t time = span(ng, lg, nz, lz) + (sg + sz) * T * r * 8 / 3500;  // and its sums' way through HBM
       if (time >= best) return;
       best = time;
       p.g.MH = mh;
@@ -182,13 +185,26 @@ GradPlan grad_plan(int64_t T, int64_t m, int64_t n, int64_t r) {
                    tiles(m, 2) >= 74 && rings_fit(A_BF16_M, true, Z_TERMS, 2, bn, 2)
                ? 2
                : 1;
-  auto split_t = [&](int ak, int mh, int64_t rows) {
-    const int64_t t = tiles(rows, mh), per = kblock_cycles(ak, Z_TERMS, mh, bn);
-    const int64_t s = std::max<int64_t>(1, std::min<int64_t>(74 / t, nkt / 4));
-    return (nkt - (nkt + s - 1) / s) * per > 6000 + s * rows * r * 8 / 3500 ? int(s) : 1;
+  // (two CTAs above 148 cost as much as a whole round: 1500 tokens, 4096 × 11008, rank 64, dU in two pieces: 60 µs, 36 in one)
+  const int64_t tu = tiles(m, p.u.MH), tv = tiles(n, 1), top = std::max<int64_t>(1, nkt / 4);
+  const int64_t peru = kblock_cycles(A_BF16_M, Z_TERMS, p.u.MH, bn), perv = kblock_cycles(A_INT8_M, Z_TERMS, 1, bn);
+  best = INT64_MAX;
+  auto split_t = [&](int64_t su, int64_t sv) {
+    su = std::max<int64_t>(1, std::min(su, top));
+    sv = std::max<int64_t>(1, std::min(sv, top));
+    const int64_t moved = (su > 1 ? su * m : 0) + (sv > 1 ? sv * n : 0);
+    const int64_t time = span(tu * su, (nkt + su - 1) / su * peru + 3000, tv * sv, (nkt + sv - 1) / sv * perv + 3000) +
+                         (moved ? 6000 + moved * r * 8 / 3500 : 0);
+    if (time >= best) return;
+    best = time;
+    p.u.splits = int(su);
+    p.v.splits = int(sv);
   };
-  p.u.splits = split_t(A_BF16_M, p.u.MH, m);
-  p.v.splits = split_t(A_INT8_M, 1, n);
+  const int64_t share = 148 * tu * peru / (tu * peru + tv * perv) / tu;
+  split_t(1, 1);
+  split_t(share, (148 - std::min<int64_t>(148, tu * std::max<int64_t>(1, share))) / tv);
+  split_t(1, (148 - std::min<int64_t>(148, tu)) / tv);
+  split_t((148 - std::min<int64_t>(148, tv)) / tu, 1);
   fit_rings(&p.u, A_BF16_M, true, Z_TERMS);
   fit_rings(&p.v, A_INT8_M, true, Z_TERMS);
 
@@ -276,7 +292,6 @@ hsl_status mx_gemm_grad_run(const MxOperand& X, int64_t T, int64_t n, const void
     g.BN = sh.BN;
     g.stages = sh.stages;
     g.codes = sh.codes;
-    g.terms = sh.terms;
     g.splits = sh.splits;
     return g;
   };
