@@ -33,7 +33,8 @@
 //   up in warp order, several row tiles at a time.  Where the columns do not fit, K is taken in slices; the rows'
 //   sums stay in shared memory from slice to slice and pass to pass.
 //
-//   28672 × 8192: 30 µs at one token (4.2 TB/s over the whole call, launch and tail included), 44 at eight.
+//   28672 × 8192, calls one behind the other: 29 µs at one token (4.3 TB/s, launch and tail included), 33 at two,
+//   41 at eight.
 //
 // f32 (k_mx_decode_f32): a lane per row, tokens broadcast from shared memory, fp32 FMA, K in ranges.
 #include <cuda.h>
@@ -350,8 +351,9 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         for (int grp = blockIdx.x; grp < groups; grp += gridDim.x) {
           const int row0 = grp * srows;
           for (int u = u0; u < uend; u += a.su, ++step) {
-            // One stage goes out without knowing the passes.  More of them only hold up the kernel that
-            // makes the columns (one token, 28672 × 8192: 37 against 35 µs with a ring full).
+            // One token: a ring full goes out without knowing the passes.  From two on one stage: more of
+            // them only hold up the kernel that makes the columns (8192 × 28672, 8 tokens: 57.8 µs, with a
+            // ring full 59.1; 28672 × 8192 the same either way).
             if (!told && step == (kSelf ? a.stages : 1)) {
               told = true;
               __syncthreads();
@@ -612,7 +614,7 @@ constexpr int DF_SLAB = 512;   // values of K staged at a time: 64 per warp
 // A row's 16 bytes of codes are read by one lane, which uses a whole 32-byte sector with its two blocks.  What
 // bounds it is widening and FMA issue once per 8 tokens, and below that latency: K goes in ranges to
 // about five CTAs per SM, whose sums a second kernel adds in order (4096 × 4096, 8 tokens: 54 µs
-// in one range, 30 in eight; one token 20 µs; slabs of 1024 values cost 2 to 10 µs more).
+// in one range, 27 in eight; one token 18.5 µs; slabs of 1024 values cost 2 to 10 µs more).
 __global__ void __launch_bounds__(DF_WARPS * 32)
     k_mx_decode_f32(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t cpitch,
                     int64_t spitch, const float* __restrict__ X, const float* add, float* Y, int m, int n,
@@ -735,8 +737,8 @@ bool mx_decode_fits(int64_t T, int64_t m, int64_t n) {
 }
 
 // One token's columns cost a CTA less than a kernel that makes them for all, as the first stages of D are on
-// their way meanwhile (28672 × 8192: 32.8 against 34.8 µs); from two tokens on they cost as much or
-// more (2: 36.9 against 34.8 µs; 8: 57 against 43 µs).
+// their way meanwhile (28672 × 8192: 28.9 against 32.7 µs, 11008 × 4096: 12.3 against 14.4).  Of more tokens every
+// CTA would make all columns.
 bool decode_self(int64_t T) { return T == 1; }
 
 // The workspace: per token its exponent and windows (256 bytes), then its columns: eight windows hold every

@@ -30,7 +30,7 @@
 // MH = 2 gives the CTA two 128-row accumulators that share every B tile.  Bound by shared memory: a K-block
 // of 256 × 208 × 64 takes the MMAs 832 cycles, 1090 as measured, in which widened A (32 KB)
 // and B (26 KB) are written once and B is read once per accumulator.  11008 × 4096 at 2048
-// tokens: 150 µs, 1.23 PFLOP/s; the input gradient of 4096 × 11008 137 µs (171 and 161 µs in a row
+// tokens: 144 µs, 1.28 PFLOP/s; the input gradient of 4096 × 11008 137 µs (172 and 162 µs in seconds
 // of calls, where the power limit slows the clock).  Every wait is bounded.
 #pragma once
 

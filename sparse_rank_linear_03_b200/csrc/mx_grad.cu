@@ -5,9 +5,9 @@
 // Five skinny products in two launches (first Z and G, then the three that use them),
 // each launch one grid whose CTAs take tiles of one product or another: alone, most of
 // them have fewer tiles than SMs or leave a last round half empty.  Z and G are fp32 sums over their
-// splits and stay so: three bf16 parts, which the second products take as three terms.  Sums over tokens, features
-// and columns leave the tensor unit every 8 to 24 of its steps (kFold in mx_gemm_tile.cuh); that and the three
-// parts bring the results from 2^−16 of their size to the error of fp32 sums.  What they cost, against two parts
+// splits and stay so: three bf16 parts, which the second products take as three terms.  Sums over tokens and features
+// leave the tensor unit every 16 or 24 of its steps (kFold in mx_gemm_tile.cuh; sums over r are 48 steps at
+// most); that and the three parts bring the results from 2^−16 of their size to the error of fp32 sums.  What they cost, against two parts
 // and sums that stay in the tensor unit: 28672 × 8192, rank 256, 4096 tokens 382 µs (269), where tiles
 // become 128 columns instead of 256 and the second launch brings 80 KB from L2 per 256 × 128 × 64 step, 7 TB/s in
 // all; 8192 × 8192, rank 128, 4096 tokens 154 (136); 4096 × 4096, rank 128, 500 tokens 28.7 (26.7) µs.

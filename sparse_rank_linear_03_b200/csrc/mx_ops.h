@@ -64,10 +64,11 @@ hsl_status mx_gemm_grad_run(const MxOperand& X, int64_t T, int64_t n, const void
 cudaError_t mx_gemm_error_word(uint32_t** p);
 cudaError_t mx_grad_error_word(uint32_t** p);
 // A few tokens (mx_decode.cu), any alignment of X.  bf16: as many as mx_decode_fits says.
-// To 8 tokens, the columns of one register MMA: 28672 × 8192 at 8 tokens 44 µs, the tensor-core kernel 79; 11008 × 4096
-// 21 against 26.  With two MMAs per block, at 16 tokens, it took 99 and 28 µs, the tensor-core kernel 80 and 26.
-// f32 to 32: 4096 × 4096 at 32 tokens 78 µs, the tiled product 88; at 64 tokens 143 and 94 µs; 512 × 4096 at 32
-// tokens 18 and 20, at 64 29 and 20 µs.
+// To 8 tokens, the columns of one register MMA: 28672 × 8192 at 8 tokens 41 µs, the tensor-core kernel 76; 11008 × 4096
+// 18.5 against 22.6.  With two MMAs per block, at 16 tokens, a call alone took 99 and 28 µs, the tensor-core kernel 80
+// and 24.5.
+// f32 to 32: 4096 × 4096 at 32 tokens 76 µs, the tiled product 88; at 64 tokens 141 and 94 µs; 512 × 4096 at 32
+// tokens 16 and 18, at 64 27 and 20 µs.
 constexpr int64_t kMxDecodeMax = 8, kMxDecodeF32Max = 32;
 bool mx_decode_fits(int64_t T, int64_t m, int64_t n);
 cudaError_t mx_decode_error_word(uint32_t** p);

@@ -11,7 +11,7 @@
 // The sums are kept in two levels, folded every 64 terms, so that the rounding error
 // of a long sum grows with the root of 64 terms and of K/64 folds rather than of K.
 // Bound by the fp32 FMA rate and, at small sizes, by the latency of a K loop (64 × 4096 × 4096,
-// gradient of the input: 250 µs in one range of K, 103 in eleven).
+// gradient of the input: 250 µs in one range of K, 99 in eleven).
 #include <algorithm>
 
 #include "common.cuh"
