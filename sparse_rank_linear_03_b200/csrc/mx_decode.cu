@@ -67,8 +67,8 @@ __device__ __forceinline__ void widen_word(uint32_t w, uint32_t (&v)[4]) {
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
       : "r"(w));
 }
-// Four scale bytes (one word) → 2^(e − 110) in fp32 (infinite from e = 238 on): the conversion gives 2^(e − 127) as bf16 pairs
-// (2^−127 a subnormal, 255 a NaN), which widen by shifts.
+// Four scale bytes (one word) → 2^(e − 110) in fp32 (infinite from e = 238 on): the conversion gives 2^(e − 127)
+// as bf16 pairs (2^−127 a subnormal, 255 a NaN), which widen by shifts.
 __device__ __forceinline__ void widen_scales(uint32_t w, float* s) {
   uint32_t p[2];
   asm("{\n\t.reg .b16 a, b;\n\t"
@@ -94,18 +94,22 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 // 2^k, −126 <= k <= 127.
 __device__ __forceinline__ float pow2(int k) { return __uint_as_float(uint32_t(127 + k) << 23); }
 
-// One output's sum by a warp, straight from the token: every product takes its block's power of two in
-// two factors, so that only what is past fp32 itself overflows.  (Inlined: a call costs the kernel 2 µs.)
+// One output's sum by a warp, straight from the token, whose values are finite: every product but those with 0
+// takes its block's power of two in two factors, so that only what is past fp32 itself overflows.  (Inlined: a
+// call costs the kernel 2 µs.)
 __device__ __forceinline__ float dc_again(const uint8_t* codes, const uint8_t* scales, const __nv_bfloat16* x, int n,
                                        int nb) {
   float v = 0.f;
   for (int b = threadIdx.x & 31; b < nb; b += 32) {
     const uint4 q = __ldg(reinterpret_cast<const uint4*>(codes) + b);
     const int e = __ldg(scales + b), s = e - 127;
-    const float f0 = e == 255 ? __uint_as_float(0x7FC00000u) : pow2(s >> 1), f1 = pow2((s + 1) >> 1);
+    const float f0 = pow2(s >> 1), f1 = pow2((s + 1) >> 1);
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-    for (int j = 0; j < min(32, n - b * 32); ++j)
-      v = fmaf(__bfloat162float(x[b * 32 + j]) * f0, mx::e2m1_f32((w[j >> 3] >> ((j & 7) * 4)) & 15u) * f1, v);
+    for (int j = 0; j < min(32, n - b * 32); ++j) {
+      const uint32_t d = (w[j >> 3] >> ((j & 7) * 4)) & 15u;
+      if (d & 7u) v = fmaf(__bfloat162float(x[b * 32 + j]) * f0, mx::e2m1_f32(d) * f1, v);
+    }
+    if (e == 255) v = __uint_as_float(0x7FC00000u);
   }
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
   return v;
@@ -121,7 +125,7 @@ struct DcArgs {
   const uint4* columns;  // [window][token][cpieces] pieces of eight fp16
   const uint8_t *codes, *scales;  // for dc_again
   int64_t pitch, spitch;
-  const __nv_bfloat16* X;  // kSelf
+  const __nv_bfloat16* X;  // kSelf, dc_again
   const __nv_bfloat16* add;
   __nv_bfloat16* Y;
   int m, n, nb, T;

@@ -89,6 +89,18 @@ def test_apply_small_scales_beside_a_large_value(hsl, T, m, n, top, low):
     close(hsl.mx4_apply(D, x), mx.apply(d, f64(x)), mx.apply(np.abs(d), np.abs(f64(x))), n, "bf16")
 
 
+@pytest.mark.parametrize("T,n", [(1, 320), (2, 4096), (8, 777), (9, 320)])
+def test_apply_large_scales_beside_a_large_value(hsl, T, n):
+    """Weights of 2^120, tokens of 2^-60 but for one value of 2^100, whose weights, in the same blocks, are 0."""
+    w = scaled(weights(40, n, n), np.full(-(-n // 32), 120))
+    w[:, 3::32] = 0.0
+    D, d = blocks(hsl, w, "e2m1")
+    x = np.ldexp(1 + np.random.default_rng(n).random((T, n)), -60)
+    x[:, 3] = 2.0 ** 100
+    x = tensor(x, "bf16")
+    close(hsl.mx4_apply(D, x), mx.apply(d, f64(x)), mx.apply(np.abs(d), np.abs(f64(x))), n, "bf16")
+
+
 @pytest.mark.parametrize("T", [1, 4, 8, 9])
 def test_apply_the_largest_weights(hsl, T):
     """One block of 6 · 2^125 (as large weights are held) against values of 2^-100."""
