@@ -178,7 +178,7 @@
         }
       }
       if (!kFold) tc::mma_commit(&accf[0]);
-      if (kFold && *abrt) {  // nothing may write to TMEM when it is given back
+      if (kFold) {  // nothing may write to TMEM when it is given back, also where another warp has given up
         tc::mma_commit(&quiet);
         tc::mbar_wait(&quiet, 0, &g_mx_gemm_err);
       }
