@@ -21,8 +21,9 @@
 //   2^−25, then keeps its bits at every e.  At the other end sums of blocks with e of about 200 and more
 //   (weights of 2^70) may overflow although the result, for small tokens, does not.  That always shows, as an
 //   infinity or a NaN, and such outputs are summed again at the end, as they are, by the warp that issued the
-//   copies (dc_again; if it is every output of 28672 × 8192, 3 ms at one token).  (A look at each unit's scales with a second loop for such units took 33 µs where this takes
-//   29, and so did the same repair as a call from the sixteen warps.)
+//   copies (dc_again; if it is every output of 28672 × 8192, 3 ms at one token).  A look at each unit's scales,
+//   with a second loop for such units, took 33 µs for ordinary weights, where this takes 29; the same repair as
+//   a call from the sixteen warps 31.
 //
 //   One CTA per SM keeps the columns in shared memory and walks over tiles of 16 rows.
 //   Codes and scales come in tiled copies, one of each per stage, a ring of stages ahead of
